@@ -394,6 +394,119 @@ qurl_status qurl_kv_cache_dequant(const void* cache, const float* scale, const i
                                   int head_dim, long long num_slots, void* out, qurl_stream_t stream);
 
 /*
+ * Attention of one new token per sequence over the FP8 cache that
+ * qurl_kv_cache_quant fills (the rollout's decode step between the qkv and the
+ * output projection).  For sequence b and query head h (KV head h / (q_heads /
+ * kv_heads)), over the cached tokens j it sees,
+ *   s_j = scale * sum_d q[b][h][d] * (e4m3 value of k_cache)[slot_j][.][d] * k_scale[slot_j][.]
+ *   out[b][h hd + d] = bf16_RNE( sum_j softmax(s)_j * (e4m3 value of v_cache)[slot_j][.][d] * v_scale[slot_j][.] )
+ *   lse[b][h] = log sum_j exp(s_j)        (to join it with attention over other tokens)
+ * with token j in slot block_table[b][j / block_size] * block_size + j % block_size
+ * (the slots of qurl_kv_cache_quant's slot_mapping), j < seq_lens[b], and, with
+ * window > 0, j >= seq_lens[b] - window.  A sequence that sees no token (length
+ * 0) gets out = 0 and lse = -inf.
+ *   q            [B, ldq] bf16, the q_heads * head_dim query columns first (the
+ *                fused qkv output itself may be passed).
+ *   caches       as in qurl_kv_cache_quant; head_dim a multiple of 16, at most 256.
+ *   block_table  [B, ld_table] int32, max_blocks entries a row; only those that a
+ *                sequence's tokens lie in are read.  block_size >= 1.
+ *   seq_lens     [B] int32, the new token's included once its key is cached;
+ *                negative counts as 0.
+ *   out          [B, ldo] bf16.     lse [B, q_heads] fp32 or NULL.
+ *   workspace    qurl_kv_attn_workspace_size(...) bytes for the same arguments (a
+ *                larger batch's or table's serves a smaller one), 16-byte aligned,
+ *                ZERO-FILLED before its first use: it holds counters that every
+ *                call leaves zero.  Calls that may run at the same time need
+ *                separate workspaces.
+ * Lengths and pages are read on the device: a token whose page is negative or
+ * past num_slots is left out, a length past max_blocks * block_size is cut to
+ * it, and both latch QURL_ERR_INVALID_ARG in the device status word.
+ * Rows are independent, results identical run to run.  B = 0 is valid.
+ * Errors: INVALID_ARG (NULL, a size out of range, q_heads % kv_heads, ld_table <
+ * max_blocks, window < 0, scale not finite), UNSUPPORTED (head_dim; B * q_heads
+ * or max_blocks * block_size of 2^31 or more), ALIGNMENT, WORKSPACE.  One kernel
+ * launch.
+ */
+size_t qurl_kv_attn_workspace_size(int B, int q_heads, int kv_heads, int head_dim, int max_blocks, int block_size);
+qurl_status qurl_kv_attn_decode(const void* q, int ldq, int B, int q_heads, int kv_heads, int head_dim,
+                                const void* k_cache, const float* k_scale, const void* v_cache, const float* v_scale,
+                                long long num_slots, const int32_t* block_table, int ld_table, int max_blocks,
+                                int block_size, const int32_t* seq_lens, int window, float scale, void* out, int ldo,
+                                float* lse, void* workspace, size_t ws_bytes, qurl_stream_t stream);
+
+/*
+ * The residual update between two blocks of a layer with the norms on both
+ * sides of it, then per-token quantization for the next projection ([UAQ] fold
+ * into the norm, [LOSS]).  Per token m:
+ *   n  = (Y * r_y) * gamma_post                  r_y as in qurl_rmsnorm_quant with eps_post; n = Y without gamma_post
+ *   t  = n * gate                                t = n without gate
+ *   H_out = bf16_RNE(H + t * residual_scale)     each product and the sum rounded to fp32
+ *   v  = (H_out * r) * gamma_folded              then codes and scales as qurl_rmsnorm_quant(H_out) gives them,
+ *                                                bit for bit (ms_out [M] fp32 or NULL, likewise)
+ *   Y, H, H_out  [M, K] bf16, row strides ldy, ldh, ldo; H_out may be H (ldo == ldh).
+ *   gamma_post   [K] fp32 or NULL (no norm behind the block).
+ *   gate         bf16 rows, stride ldg elements; ldg = 0: one row [K] for every
+ *                token; or NULL.
+ *   Xq [M, K] codes, sx [M] fp32.
+ * Errors as qurl_rmsnorm_quant.  One kernel launch.
+ */
+qurl_status qurl_residual_rmsnorm_quant(const void* Y, int ldy, const float* gamma_post, float eps_post,
+                                        const void* gate, int ldg, float residual_scale, const void* H, int ldh,
+                                        void* H_out, int ldo, const float* gamma_folded, float eps, int M, int K,
+                                        qurl_qtype qt, void* Xq, float* sx, float* ms_out, qurl_stream_t stream);
+
+/*
+ * The next token of each row of logits from a given uniform number, with the
+ * log-probability the ACR objective later reads as logp_behav.  Row b, of V
+ * logits x (bf16 or fp32, row stride ld):
+ *   w_v = exp((x_v - max x) / temperature);  order: larger x first, then smaller v
+ *   kept: the first top_k of the order, and of those w_v >= min_p; of what is left,
+ *         while the weight before v in the order is below top_p times its whole weight
+ *   token = the first kept v, by index, at which the running kept weight exceeds
+ *           u times the whole kept weight
+ *   logp      = (x_token - max x) / temperature - log sum_v w_v          (all of the row)
+ *   logp_kept = the same over the kept weight: what the token was drawn from
+ * temperature 0 is greedy: the first of the order, logp that of temperature 1,
+ * logp_kept 0.  The weights are held as 62-bit integers (relative error below
+ * 2^-29), so a choice does not depend on the order of a sum.
+ *   temperature [B] fp32, 0 or in [1e-6, 1e6]; NULL: 1.   top_k [B] int32, <= 0 or >= V: off; NULL: off.
+ *   top_p [B] fp32 >= 0, >= 1: off; NULL: off.            min_p [B] fp32 in [0, 1], 0: off; NULL: off.
+ *   u [B] fp32 in [0, 1).  token [B] int64.  logp, logp_kept [B] fp32 or NULL.
+ * -inf logits are never drawn; NaN counts as -inf, +inf as the largest float.
+ * A row with nothing to draw (every logit -inf) gets token -1 and -inf twice; so
+ * does a row with a parameter out of range, which latches QURL_ERR_INVALID_ARG
+ * in the device status word.  B = 0 is valid.  One kernel launch.
+ */
+qurl_status qurl_sample(const void* logits, qurl_ftype x_type, int B, int V, int ld, const float* temperature,
+                        const int32_t* top_k, const float* top_p, const float* min_p, const float* u, int64_t* token,
+                        float* logp, float* logp_kept, qurl_stream_t stream);
+
+/*
+ * Log-probabilities of given tokens (the objective's logp and logp_prox), and
+ * the gradient of its logits.  Row t of the logits x [T, V] (bf16 or fp32, row
+ * stride ld), z = x / temperature:
+ *   lse[t]  = log sum_v exp(z_v),    logp[t] = z_target - lse[t]
+ *   dx_v    = scale * g[t] / (temperature * *denom) * (1[v = target] - exp(z_v - lse[t]))
+ * qurl_token_logprob_grad takes lse as the forward call wrote it; g is the
+ * derivative by logp (qurl_acr_objective's dterm), denom a device double (its
+ * stats + 1, the number of valid tokens) or NULL for 1; a denom that is not
+ * positive gives zeros.  Sums are fp32.
+ *   targets [T] int64: a negative one is padding (logp = lse = 0, a zero gradient
+ *   row whatever lse and g hold); one >= V is treated the same and latches
+ *   QURL_ERR_INVALID_ARG in the device status word.
+ *   dlogits [T, V] of the logits' type, row stride ldd; may be the logits
+ *   themselves (ldd == ld).  Columns V .. ld - 1 are neither read nor written.
+ * -inf logits have probability 0; a row of nothing else gives -inf and a zero
+ * gradient.  NaN and +inf logits are outside the domain.  temperature in [1e-6, 1e6].
+ * T = 0 is valid.  One kernel launch each.
+ */
+qurl_status qurl_token_logprob(const void* logits, qurl_ftype x_type, int T, int V, int ld, const int64_t* targets,
+                               float temperature, float* logp, float* lse, qurl_stream_t stream);
+qurl_status qurl_token_logprob_grad(const void* logits, qurl_ftype x_type, int T, int V, int ld,
+                                    const int64_t* targets, float temperature, const float* lse, const float* g,
+                                    float scale, const double* denom, void* dlogits, int ldd, qurl_stream_t stream);
+
+/*
  * ACR token objective of a quantized rollout ([ACR], [OBJ]): the decoupled-PPO
  * objective with the truncated importance weight of TIS and ACR's adaptive
  * clipping range, over T token slots (the responses of a mini-batch, padded

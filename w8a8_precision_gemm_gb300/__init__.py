@@ -95,6 +95,12 @@ def load() -> ctypes.CDLL:
             "qurl_acr_objective": [P, P, P, P, P, ctypes.c_longlong, f, f, i, P, P, P, P, z, P],
             "qurl_kv_cache_quant": [P, i, i, i, i, i, P, ctypes.c_longlong, P, P, P, P, P],
             "qurl_kv_cache_dequant": [P, P, P, i, i, i, ctypes.c_longlong, P, P],
+            "qurl_kv_attn_decode": [P, i, i, i, i, i, P, P, P, P, ctypes.c_longlong, P, i, i, i, P, i, f, P, i, P, P,
+                                    z, P],
+            "qurl_residual_rmsnorm_quant": [P, i, P, f, P, i, f, P, i, P, i, P, f, i, i, i, P, P, P, P],
+            "qurl_sample": [P, i, i, i, i, P, P, P, P, P, P, P, P, P],
+            "qurl_token_logprob": [P, i, i, i, i, P, f, P, P, P],
+            "qurl_token_logprob_grad": [P, i, i, i, i, P, f, P, P, f, P, P, i, P],
         }
         for name, args in sig.items():
             fn = getattr(L, name)
@@ -106,6 +112,8 @@ def load() -> ctypes.CDLL:
         L.qurl_wide_weights_size.restype = ctypes.c_size_t
         L.qurl_nvfp4_workspace_size.argtypes = [i, i, i]
         L.qurl_nvfp4_workspace_size.restype = ctypes.c_size_t
+        L.qurl_kv_attn_workspace_size.argtypes = [i, i, i, i, i, i]
+        L.qurl_kv_attn_workspace_size.restype = ctypes.c_size_t
         L.qurl_acr_workspace_size.argtypes = []
         L.qurl_acr_workspace_size.restype = ctypes.c_size_t
         L.qurl_status_string.argtypes = [ctypes.c_int]
@@ -148,6 +156,28 @@ def _dense(*ts):
     for t in ts:
         if t is not None and not t.is_contiguous():
             raise ValueError("code / scale / accumulator tensors must be contiguous")
+
+
+def _here(first, *ts):
+    """The tensors of a call live on the current device: its kernels are launched there."""
+    dev = first.device
+    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
+        raise ValueError(f"expected tensors on the current CUDA device, got {dev}")
+    for t in ts:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}")
+
+
+def _typed(t, dtype, what, n=None):
+    if t is not None and (t.dtype != dtype or (n is not None and t.numel() != n)):
+        raise ValueError(f"{what} is {dtype}" + ("" if n is None else f" of {n} values"))
+
+
+def _logits(x):
+    """(type, row stride) of a matrix of logits."""
+    if x.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("logits are bf16 or fp32")
+    return (FP32 if x.dtype == torch.float32 else BF16), _ld(x)
 
 
 # ---------------------------------------------------------------- the C ABI, by name
@@ -295,6 +325,113 @@ def kv_cache(num_slots, kv_heads, head_dim, device="cuda"):
             torch.empty((num_slots, kv_heads), dtype=torch.float32, device=device))
 
 
+def qurl_kv_attn_workspace_size(B, q_heads, kv_heads, head_dim, max_blocks, block_size) -> int:
+    return int(load().qurl_kv_attn_workspace_size(B, q_heads, kv_heads, head_dim, max_blocks, block_size))
+
+
+def qurl_kv_attn_decode(q, q_heads, k_cache, k_scale, v_cache, v_scale, block_table, block_size, seq_lens, scale, out,
+                        workspace, window=0, lse=None, stream=None):
+    """Attention of one new token per row of q [B, >= q_heads * head_dim] over the
+    paged FP8 cache (see include/qurl.h)."""
+    _here(q, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, out, workspace, lse)
+    _dense(k_cache, k_scale, v_cache, v_scale, seq_lens, lse, workspace)
+    B = q.shape[0]
+    num_slots, kv_heads, head_dim = k_cache.shape
+    for c, sc in ((k_cache, k_scale), (v_cache, v_scale)):
+        if c.element_size() != 1 or c.shape != k_cache.shape or sc.dtype != torch.float32 or sc.shape != c.shape[:2]:
+            raise ValueError("caches are 8-bit [slots, kv_heads, head_dim] with fp32 scales [slots, kv_heads]")
+    if q.dtype != torch.bfloat16 or out.dtype != torch.bfloat16 or out.shape[0] != B:
+        raise ValueError("q and out are bf16 [B, ...]")
+    if q.shape[1] < q_heads * head_dim or out.shape[1] < q_heads * head_dim:
+        raise ValueError("q and out have q_heads * head_dim columns at least")
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table is int32 [B, blocks]")
+    _typed(seq_lens, torch.int32, "seq_lens", B)
+    _typed(lse, torch.float32, "lse", B * q_heads)
+    max_blocks = block_table.shape[1]
+    _ok(load().qurl_kv_attn_decode(_ptr(q), _ld(q), B, q_heads, kv_heads, head_dim, _ptr(k_cache), _ptr(k_scale),
+                                   _ptr(v_cache), _ptr(v_scale), num_slots, _ptr(block_table),
+                                   _ld(block_table) if max_blocks else 0, max_blocks, block_size, _ptr(seq_lens),
+                                   window, scale, _ptr(out), _ld(out), _ptr(lse), _ptr(workspace),
+                                   workspace.numel() * workspace.element_size(), _stream(stream)),
+        "qurl_kv_attn_decode")
+
+
+def qurl_residual_rmsnorm_quant(H, Y, gamma_folded, qt, H_out, Xq, sx, gamma_post=None, gate=None, residual_scale=1.0,
+                                eps=1e-6, eps_post=1e-6, ms_out=None, stream=None):
+    """H_out = H + residual_scale * gate * RMSNorm(Y), then RMSNorm and per-token
+    quantization of H_out (see include/qurl.h).  gate [M, K], or [K] / [1, K] for every token."""
+    _here(Y, H, gamma_folded, H_out, Xq, sx, gamma_post, gate, ms_out)
+    _dense(gamma_folded, gamma_post, Xq, sx, ms_out)
+    M, K = Y.shape
+    for t, what in ((Y, "Y"), (H, "H"), (H_out, "H_out")):
+        if t.dtype != torch.bfloat16 or t.shape != (M, K):
+            raise ValueError(f"{what} is bf16 [M, K]")
+    for t, what in ((gamma_folded, "gamma_folded"), (gamma_post, "gamma_post")):
+        _typed(t, torch.float32, what, K)
+    _typed(sx, torch.float32, "sx", M)
+    _typed(ms_out, torch.float32, "ms_out", M)
+    if Xq.element_size() != 1 or Xq.numel() != M * K:
+        raise ValueError("Xq is one byte per code [M, K]")
+    ldg = 0
+    if gate is not None:
+        rows = 1 if gate.dim() == 1 else gate.shape[0]
+        if gate.dtype != torch.bfloat16 or gate.dim() > 2 or gate.shape[-1] != K or rows not in (1, M) \
+                or gate.stride(-1) != 1:
+            raise ValueError("gate is bf16 [M, K], [1, K] or [K]")
+        ldg = 0 if rows == 1 else gate.stride(0)
+    _ok(load().qurl_residual_rmsnorm_quant(_ptr(Y), _ld(Y), _ptr(gamma_post), eps_post, _ptr(gate), ldg,
+                                           residual_scale, _ptr(H), _ld(H), _ptr(H_out), _ld(H_out),
+                                           _ptr(gamma_folded), eps, M, K, qt, _ptr(Xq), _ptr(sx), _ptr(ms_out),
+                                           _stream(stream)), "qurl_residual_rmsnorm_quant")
+
+
+def qurl_sample(logits, u, token, temperature=None, top_k=None, top_p=None, min_p=None, logp=None, logp_kept=None,
+                stream=None):
+    """One token per row of logits [B, V] from uniform numbers u [B] (see include/qurl.h)."""
+    _here(logits, u, token, temperature, top_k, top_p, min_p, logp, logp_kept)
+    _dense(u, token, temperature, top_k, top_p, min_p, logp, logp_kept)
+    B, V = logits.shape
+    xt, ld = _logits(logits)
+    for t, what in ((u, "u"), (temperature, "temperature"), (top_p, "top_p"), (min_p, "min_p"), (logp, "logp"),
+                    (logp_kept, "logp_kept")):
+        _typed(t, torch.float32, what, B)
+    _typed(top_k, torch.int32, "top_k", B)
+    _typed(token, torch.int64, "token", B)
+    _ok(load().qurl_sample(_ptr(logits), xt, B, V, ld, _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p),
+                           _ptr(u), _ptr(token), _ptr(logp), _ptr(logp_kept), _stream(stream)), "qurl_sample")
+
+
+def qurl_token_logprob(logits, targets, logp, lse, temperature=1.0, stream=None):
+    """Log-probabilities of targets [T] under logits [T, V] (see include/qurl.h)."""
+    _here(logits, targets, logp, lse)
+    _dense(targets, logp, lse)
+    T, V = logits.shape
+    xt, ld = _logits(logits)
+    _typed(targets, torch.int64, "targets", T)
+    _typed(logp, torch.float32, "logp", T)
+    _typed(lse, torch.float32, "lse", T)
+    _ok(load().qurl_token_logprob(_ptr(logits), xt, T, V, ld, _ptr(targets), temperature, _ptr(logp), _ptr(lse),
+                                  _stream(stream)), "qurl_token_logprob")
+
+
+def qurl_token_logprob_grad(logits, targets, lse, g, dlogits, temperature=1.0, scale=1.0, denom=None, stream=None):
+    """The logits' gradient of scale * sum_t g[t] logp[t] / denom (see include/qurl.h)."""
+    _here(logits, targets, lse, g, dlogits, denom)
+    _dense(targets, lse, g, denom)
+    T, V = logits.shape
+    xt, ld = _logits(logits)
+    if dlogits.dtype != logits.dtype or dlogits.shape != logits.shape:
+        raise ValueError("dlogits has the logits' type and shape")
+    _typed(targets, torch.int64, "targets", T)
+    _typed(lse, torch.float32, "lse", T)
+    _typed(g, torch.float32, "g", T)
+    _typed(denom, torch.float64, "denom", 1)
+    _ok(load().qurl_token_logprob_grad(_ptr(logits), xt, T, V, ld, _ptr(targets), temperature, _ptr(lse), _ptr(g),
+                                       scale, _ptr(denom), _ptr(dlogits), _ld(dlogits), _stream(stream)),
+        "qurl_token_logprob_grad")
+
+
 def qurl_check_device_status(stream=None):
     _ok(load().qurl_check_device_status(_stream(stream)), "qurl_check_device_status")
 
@@ -407,6 +544,70 @@ def gemm_acc(Xq, Wq, qt, ws=None, stream=None):
     acc = torch.empty((M, N), dtype=torch.int32 if qt == INT8 else torch.float32, device=Xq.device)
     qurl_w8a8_gemm_acc(Xq, Wq, qt, acc, ws, stream)
     return acc
+
+
+def kv_attn_workspace(B, q_heads, kv_heads, head_dim, max_blocks, block_size, device="cuda") -> torch.Tensor:
+    """Scratch for kv_attn_decode calls of at most this size: zero-filled once
+    (its counters), left ready for reuse by every call."""
+    n = qurl_kv_attn_workspace_size(B, q_heads, kv_heads, head_dim, max_blocks, block_size)
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def kv_attn_decode(q, q_heads, k_cache, k_scale, v_cache, v_scale, block_table, block_size, seq_lens, scale=None,
+                   window=0, want_lse=False, ws=None, stream=None):
+    """Attention of one new token per sequence over the paged FP8 cache.  scale
+    defaults to head_dim ** -0.5.  Returns out [B, q_heads * head_dim] bf16, or
+    (out, lse [B, q_heads])."""
+    B, (_, kv_heads, hd) = q.shape[0], k_cache.shape
+    if ws is None:
+        ws = kv_attn_workspace(B, q_heads, kv_heads, hd, block_table.shape[1], block_size, q.device)
+    out = torch.empty((B, q_heads * hd), dtype=torch.bfloat16, device=q.device)
+    lse = torch.empty((B, q_heads), dtype=torch.float32, device=q.device) if want_lse else None
+    qurl_kv_attn_decode(q, q_heads, k_cache, k_scale, v_cache, v_scale, block_table, block_size, seq_lens,
+                        hd ** -0.5 if scale is None else scale, out, ws, window, lse, stream)
+    return (out, lse) if want_lse else out
+
+
+def residual_rmsnorm_quant(H, Y, gamma_folded, qt, gamma_post=None, gate=None, residual_scale=1.0, eps=1e-6,
+                           eps_post=1e-6, inplace=False, stream=None):
+    """The residual update, its norms and the quantizer behind them.  Returns
+    (H_out, Xq, sx); with inplace, H_out is H."""
+    M, K = Y.shape
+    H_out = H if inplace else torch.empty((M, K), dtype=torch.bfloat16, device=Y.device)
+    Xq = torch.empty((M, K), dtype=code_dtype(qt), device=Y.device)
+    sx = torch.empty(M, dtype=torch.float32, device=Y.device)
+    qurl_residual_rmsnorm_quant(H, Y, gamma_folded, qt, H_out, Xq, sx, gamma_post, gate, residual_scale, eps, eps_post,
+                                None, stream)
+    return H_out, Xq, sx
+
+
+def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, want_kept=False, stream=None):
+    """The next token of each row from uniform numbers u.  Returns (token int64
+    [B], logp [B]), with want_kept also logp_kept [B]."""
+    B = logits.shape[0]
+    token = torch.empty(B, dtype=torch.int64, device=logits.device)
+    logp = torch.empty(B, dtype=torch.float32, device=logits.device)
+    kept = torch.empty(B, dtype=torch.float32, device=logits.device) if want_kept else None
+    qurl_sample(logits, u, token, temperature, top_k, top_p, min_p, logp, kept, stream)
+    return (token, logp, kept) if want_kept else (token, logp)
+
+
+def token_logprob(logits, targets, temperature=1.0, stream=None):
+    """Log-probabilities of the targets.  Returns (logp [T], lse [T]); the
+    gradient call takes lse."""
+    T = logits.shape[0]
+    logp = torch.empty(T, dtype=torch.float32, device=logits.device)
+    lse = torch.empty(T, dtype=torch.float32, device=logits.device)
+    qurl_token_logprob(logits, targets, logp, lse, temperature, stream)
+    return logp, lse
+
+
+def token_logprob_grad(logits, targets, lse, g, temperature=1.0, scale=1.0, denom=None, inplace=False, stream=None):
+    """The logits' gradient of scale * sum_t g[t] logp[t] / denom; with inplace, in the logits' place."""
+    d = logits if inplace else torch.empty_strided(logits.shape, logits.stride(), dtype=logits.dtype,
+                                                   device=logits.device)
+    qurl_token_logprob_grad(logits, targets, lse, g, d, temperature, scale, denom, stream)
+    return d
 
 
 def count_diff(a, b, stream=None) -> torch.Tensor:

@@ -167,6 +167,16 @@ qurl_status check_gemm(const void* Xq, const void* Wq, int M, int N, int K, int 
   return QURL_OK;
 }
 
+// Rows of logits (bf16 or fp32) of V values, row stride ld elements.
+qurl_status check_logits(const void* x, int type, int V, int ld) {
+  if (!x || !valid_dim(V) || ld < V || (type != QURL_BF16 && type != QURL_FP32)) return QURL_ERR_INVALID_ARG;
+  const int esize = (type == QURL_FP32) ? 4 : 2;
+  if (!aligned16(x) || (static_cast<long long>(ld) * esize) % 16 != 0) return QURL_ERR_ALIGNMENT;
+  return QURL_OK;
+}
+
+bool valid_temperature(float t) { return t >= 1e-6f && t <= 1e6f; }
+
 #define QURL_TRY(expr)                    \
   do {                                    \
     const qurl_status _s = (expr);        \
@@ -884,6 +894,162 @@ qurl_status qurl_kv_cache_dequant(const void* cache, const float* scale, const i
   QURL_CUDA(qurl::launch_kv_cache_dequant(cache, scale, reinterpret_cast<const long long*>(slots), n, kv_heads,
                                           head_dim, num_slots, out, dev->status,
                                           reinterpret_cast<cudaStream_t>(stream)));
+  return QURL_OK;
+}
+
+size_t qurl_kv_attn_workspace_size(int B, int q_heads, int kv_heads, int head_dim, int max_blocks, int block_size) {
+  if (B < 0 || q_heads <= 0 || kv_heads <= 0 || head_dim <= 0 || max_blocks < 0 || block_size <= 0) return 0;
+  return qurl::attn_workspace_bytes(B, q_heads, kv_heads, head_dim, static_cast<long long>(max_blocks) * block_size,
+                                    device_sms());
+}
+
+qurl_status qurl_kv_attn_decode(const void* q, int ldq, int B, int q_heads, int kv_heads, int head_dim,
+                                const void* k_cache, const float* k_scale, const void* v_cache, const float* v_scale,
+                                long long num_slots, const int32_t* block_table, int ld_table, int max_blocks,
+                                int block_size, const int32_t* seq_lens, int window, float scale, void* out, int ldo,
+                                float* lse, void* workspace, size_t ws_bytes, qurl_stream_t stream) {
+  if (B < 0 || q_heads <= 0 || kv_heads <= 0 || head_dim <= 0 || num_slots < 0 || max_blocks < 0 || block_size <= 0 ||
+      ld_table < max_blocks || window < 0 || !std::isfinite(scale) || q_heads % kv_heads != 0)
+    return QURL_ERR_INVALID_ARG;
+  if (head_dim % 16 != 0 || head_dim > 256) return QURL_ERR_UNSUPPORTED;
+  const long long q_dim = static_cast<long long>(q_heads) * head_dim;
+  if (ldq < q_dim || ldo < q_dim) return QURL_ERR_INVALID_ARG;
+  if (static_cast<long long>(max_blocks) * block_size >= (1LL << 31) ||
+      static_cast<long long>(B) * q_heads >= (1LL << 31))
+    return QURL_ERR_UNSUPPORTED;
+  if (B == 0) return QURL_OK;
+  if (!q || !seq_lens || !out || !workspace || (max_blocks > 0 && !block_table) ||
+      (num_slots > 0 && (!k_cache || !k_scale || !v_cache || !v_scale)))
+    return QURL_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) || !aligned16(workspace) ||
+      (static_cast<long long>(ldq) * 2) % 16 != 0 || (static_cast<long long>(ldo) * 2) % 16 != 0 ||
+      (reinterpret_cast<uintptr_t>(k_scale) & 3u) != 0 || (reinterpret_cast<uintptr_t>(v_scale) & 3u) != 0 ||
+      (reinterpret_cast<uintptr_t>(block_table) & 3u) != 0 || (reinterpret_cast<uintptr_t>(seq_lens) & 3u) != 0 ||
+      (reinterpret_cast<uintptr_t>(lse) & 3u) != 0)
+    return QURL_ERR_ALIGNMENT;
+  DevState* dev = nullptr;
+  QURL_TRY(device_state(&dev));
+  if (ws_bytes < qurl::attn_workspace_bytes(B, q_heads, kv_heads, head_dim,
+                                            static_cast<long long>(max_blocks) * block_size, dev->num_sms))
+    return QURL_ERR_WORKSPACE;
+  qurl::AttnArgs a{};
+  a.q = reinterpret_cast<const __nv_bfloat16*>(q);
+  a.ldq = ldq;
+  a.B = B;
+  a.q_heads = q_heads;
+  a.kv_heads = kv_heads;
+  a.head_dim = head_dim;
+  a.k_cache = reinterpret_cast<const uint8_t*>(k_cache);
+  a.k_scale = k_scale;
+  a.v_cache = reinterpret_cast<const uint8_t*>(v_cache);
+  a.v_scale = v_scale;
+  a.num_slots = num_slots;
+  a.block_table = block_table;
+  a.ld_table = ld_table;
+  a.max_blocks = max_blocks;
+  a.block_size = block_size;
+  a.seq_lens = seq_lens;
+  a.window = window;
+  a.scale = scale;
+  a.out = reinterpret_cast<__nv_bfloat16*>(out);
+  a.ldo = ldo;
+  a.lse = lse;
+  a.ws = workspace;
+  a.status = dev->status;
+  QURL_CUDA(qurl::launch_kv_attn_decode(a, dev->num_sms, reinterpret_cast<cudaStream_t>(stream)));
+  return QURL_OK;
+}
+
+qurl_status qurl_residual_rmsnorm_quant(const void* Y, int ldy, const float* gamma_post, float eps_post,
+                                        const void* gate, int ldg, float residual_scale, const void* H, int ldh,
+                                        void* H_out, int ldo, const float* gamma_folded, float eps, int M, int K,
+                                        qurl_qtype qt, void* Xq, float* sx, float* ms_out, qurl_stream_t stream) {
+  QURL_TRY(check_act(Y, M, K, ldy));
+  QURL_TRY(check_act(H, M, K, ldh));
+  QURL_TRY(check_act(H_out, M, K, ldo));
+  if (!gamma_folded || !Xq || !sx || !valid_qt(qt) || !std::isfinite(residual_scale) || !(eps >= 0.0f) ||
+      !std::isfinite(eps) || (gamma_post && (!(eps_post >= 0.0f) || !std::isfinite(eps_post))))
+    return QURL_ERR_INVALID_ARG;
+  if (gate && ldg != 0 && ldg < K) return QURL_ERR_INVALID_ARG;
+  if (H_out == H && ldo != ldh) return QURL_ERR_INVALID_ARG;
+  if (!aligned16(gamma_folded) || !aligned16(gamma_post) || !aligned16(gate) || !aligned16(Xq) ||
+      (static_cast<long long>(ldg) * 2) % 16 != 0)
+    return QURL_ERR_ALIGNMENT;
+  DevState* dev = nullptr;
+  QURL_TRY(device_state(&dev));
+  QURL_CUDA(qurl::launch_residual_rmsnorm_quant(Y, ldy, gamma_post, eps_post, gate, ldg, residual_scale, H, ldh, H_out,
+                                                ldo, gamma_folded, eps, M, K, qt, Xq, sx, ms_out,
+                                                reinterpret_cast<cudaStream_t>(stream)));
+  return QURL_OK;
+}
+
+qurl_status qurl_sample(const void* logits, qurl_ftype x_type, int B, int V, int ld, const float* temperature,
+                        const int32_t* top_k, const float* top_p, const float* min_p, const float* u, int64_t* token,
+                        float* logp, float* logp_kept, qurl_stream_t stream) {
+  if (B < 0) return QURL_ERR_INVALID_ARG;
+  if (B == 0) return QURL_OK;
+  QURL_TRY(check_logits(logits, x_type, V, ld));
+  if (!u || !token) return QURL_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(token) & 7u) != 0) return QURL_ERR_ALIGNMENT;
+  for (const void* p : {static_cast<const void*>(temperature), static_cast<const void*>(top_k),
+                        static_cast<const void*>(top_p), static_cast<const void*>(min_p), static_cast<const void*>(u),
+                        static_cast<const void*>(logp), static_cast<const void*>(logp_kept)})
+    if ((reinterpret_cast<uintptr_t>(p) & 3u) != 0) return QURL_ERR_ALIGNMENT;
+  DevState* dev = nullptr;
+  QURL_TRY(device_state(&dev));
+  qurl::SampleArgs a{};
+  a.logits = logits;
+  a.B = B;
+  a.V = V;
+  a.ld = ld;
+  a.temperature = temperature;
+  a.top_k = top_k;
+  a.top_p = top_p;
+  a.min_p = min_p;
+  a.u = u;
+  a.token = reinterpret_cast<long long*>(token);
+  a.logp = logp;
+  a.logp_kept = logp_kept;
+  a.status = dev->status;
+  while ((1LL << a.shift) < V) ++a.shift;
+  QURL_CUDA(qurl::launch_sample(a, x_type == QURL_FP32, reinterpret_cast<cudaStream_t>(stream)));
+  return QURL_OK;
+}
+
+qurl_status qurl_token_logprob(const void* logits, qurl_ftype x_type, int T, int V, int ld, const int64_t* targets,
+                               float temperature, float* logp, float* lse, qurl_stream_t stream) {
+  if (T < 0 || !valid_temperature(temperature)) return QURL_ERR_INVALID_ARG;
+  if (T == 0) return QURL_OK;
+  QURL_TRY(check_logits(logits, x_type, V, ld));
+  if (!targets || !logp || !lse) return QURL_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(targets) & 7u) != 0 || (reinterpret_cast<uintptr_t>(logp) & 3u) != 0 ||
+      (reinterpret_cast<uintptr_t>(lse) & 3u) != 0)
+    return QURL_ERR_ALIGNMENT;
+  DevState* dev = nullptr;
+  QURL_TRY(device_state(&dev));
+  QURL_CUDA(qurl::launch_token_logprob(logits, x_type == QURL_FP32, T, V, ld,
+                                       reinterpret_cast<const long long*>(targets), 1.0f / temperature, logp, lse,
+                                       dev->status, reinterpret_cast<cudaStream_t>(stream)));
+  return QURL_OK;
+}
+
+qurl_status qurl_token_logprob_grad(const void* logits, qurl_ftype x_type, int T, int V, int ld,
+                                    const int64_t* targets, float temperature, const float* lse, const float* g,
+                                    float scale, const double* denom, void* dlogits, int ldd, qurl_stream_t stream) {
+  if (T < 0 || !valid_temperature(temperature) || !std::isfinite(scale)) return QURL_ERR_INVALID_ARG;
+  if (T == 0) return QURL_OK;
+  QURL_TRY(check_logits(logits, x_type, V, ld));
+  QURL_TRY(check_logits(dlogits, x_type, V, ldd));
+  if (!targets || !lse || !g || (dlogits == logits && ldd != ld)) return QURL_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(targets) & 7u) != 0 || (reinterpret_cast<uintptr_t>(denom) & 7u) != 0 ||
+      (reinterpret_cast<uintptr_t>(lse) & 3u) != 0 || (reinterpret_cast<uintptr_t>(g) & 3u) != 0)
+    return QURL_ERR_ALIGNMENT;
+  DevState* dev = nullptr;
+  QURL_TRY(device_state(&dev));
+  QURL_CUDA(qurl::launch_token_logprob_grad(logits, x_type == QURL_FP32, T, V, ld,
+                                            reinterpret_cast<const long long*>(targets), 1.0f / temperature, lse, g,
+                                            scale, denom, dlogits, ldd, dev->num_sms, dev->status,
+                                            reinterpret_cast<cudaStream_t>(stream)));
   return QURL_OK;
 }
 

@@ -1,0 +1,146 @@
+// residual.cu -- the residual update between two blocks of a layer, fused with
+// the norms on both sides of it and the next projection's quantizer:
+//
+//   n  = y                          or (y * r_y) * gamma_post   (RMSNorm of the block's output)
+//   t  = n * gate                   (per channel or per token and channel; optional)
+//   h' = bf16_RNE(h + t * rs)       (the residual stream, stored)
+//   v  = (h' * r_h) * gamma'        (the next block's RMSNorm, UAQ-folded gain)
+//   codes, sx = per-token quantization of v
+//
+// Each product and sum is rounded to fp32 as written; r = 1 / sqrt(ms + eps)
+// with ms as in the RMSNorm quantizer.  The second half works on the stored
+// bf16 h', so its codes are bit for bit those of qurl_rmsnorm_quant(h').
+//
+// Bound by HBM: 2 (y) + 2 (h) + 2 (h') + 1 (codes) bytes per value, against
+// 11 for the three passes (norm, update, norm and quantize) it stands for.  One
+// row per CTA, the row kept in registers from its only read to the codes.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "internal.h"
+#include "ptx.cuh"
+#include "rowquant.cuh"
+
+namespace qurl {
+namespace {
+
+using namespace rq;
+
+constexpr int kNC = 8;        // 16-byte vectors cached per thread
+constexpr int kThreads = 512;  // most threads of a row CTA
+
+struct ResidualArgs {
+  const __nv_bfloat16* Y;
+  const __nv_bfloat16* H;
+  const __nv_bfloat16* gate;  // null: 1
+  __nv_bfloat16* Hout;
+  const float* gamma_post;  // null: no norm behind the block
+  const float* gamma;
+  long long ldy, ldh, ldg, ldo;
+  float eps_post, rs, eps;
+  int K, qt;
+  uint8_t* Xq;
+  float* sx;
+  float* ms_out;
+};
+
+// h + ((y normalised) * gate) * rs of 8 values, rounded to bf16.
+__device__ __forceinline__ uint4 update8(const ResidualArgs& a, const uint4 yu, const uint4 hu, const uint4* grow, int idx,
+                                         float2 r2, float2 rs2) {
+  float2 n[4], h[4];
+  if (a.gamma_post)
+    norm8(yu, reinterpret_cast<const float4*>(a.gamma_post), idx, r2, n);
+  else
+    bf16x8_to_f2(yu, n);
+  if (grow) {
+    float2 g[4];
+    bf16x8_to_f2(__ldg(grow + idx), g);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) n[e] = mul2(n[e], g[e]);
+  }
+  bf16x8_to_f2(hu, h);
+  uint32_t o[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    // (scalar products and sums: the paired ones were seen to join into an FMA here)
+    const float sx = __fadd_rn(h[e].x, __fmul_rn(n[e].x, rs2.x));
+    const float sy = __fadd_rn(h[e].y, __fmul_rn(n[e].y, rs2.y));
+    const __nv_bfloat162 p = __floats2bfloat162_rn(sx, sy);
+    o[e] = *reinterpret_cast<const uint32_t*>(&p);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+template <int NC, int MAXT = kThreads, int MINB = 1>
+__global__ void __launch_bounds__(MAXT, MINB) residual_rmsnorm_quant_kernel(const ResidualArgs a) {
+  griddep_wait();
+  griddep_launch_dependents();
+  __shared__ RowScratch sh;
+  const int m = blockIdx.x;
+  const uint4* yrow = reinterpret_cast<const uint4*>(a.Y + static_cast<size_t>(m) * a.ldy);
+  const uint4* hrow = reinterpret_cast<const uint4*>(a.H + static_cast<size_t>(m) * a.ldh);
+  const uint4* grow = a.gate ? reinterpret_cast<const uint4*>(a.gate + static_cast<size_t>(m) * a.ldg) : nullptr;
+  uint4* orow = reinterpret_cast<uint4*>(a.Hout + static_cast<size_t>(m) * a.ldo);
+  const int nvec = a.K >> 3;
+  // h is read by plain loads: h_out may be the same rows
+  uint4 yc[NC], hc[NC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int idx = threadIdx.x + c * blockDim.x;
+    if (idx < nvec) {
+      yc[c] = __ldg(yrow + idx);
+      hc[c] = hrow[idx];
+    }
+  }
+  float2 r2 = splat2(1.0f);
+  if (a.gamma_post) {
+    float ms, r;
+    row_rms<NC, false>(yrow, a.K, yc, reinterpret_cast<const float4*>(a.gamma_post), a.eps_post, sh.red, ms, r);
+    r2 = splat2(r);
+  }
+  const float2 rs2 = splat2(a.rs);
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int idx = threadIdx.x + c * blockDim.x;
+    if (idx < nvec) orow[idx] = hc[c] = update8(a, yc[c], hc[c], grow, idx, r2, rs2);
+  }
+  for (int idx = threadIdx.x + NC * blockDim.x; idx < nvec; idx += blockDim.x)
+    orow[idx] = update8(a, __ldg(yrow + idx), hrow[idx], grow, idx, r2, rs2);
+  const CodeSums none{};
+  rmsnorm_quant_cached<NC, true>(m, orow, hc, a.K, a.gamma, a.eps, a.qt, a.Xq, a.sx, a.ms_out, nullptr, none, sh);
+}
+
+}  // namespace
+
+cudaError_t launch_residual_rmsnorm_quant(const void* Y, long long ldy, const float* gamma_post, float eps_post,
+                                          const void* gate, long long ldg, float rs, const void* H, long long ldh,
+                                          void* Hout, long long ldo, const float* gamma, float eps, int M, int K,
+                                          int qt, void* Xq, float* sx, float* ms_out, cudaStream_t st) {
+  ResidualArgs a{};
+  a.Y = reinterpret_cast<const __nv_bfloat16*>(Y);
+  a.H = reinterpret_cast<const __nv_bfloat16*>(H);
+  a.gate = reinterpret_cast<const __nv_bfloat16*>(gate);
+  a.Hout = reinterpret_cast<__nv_bfloat16*>(Hout);
+  a.gamma_post = gamma_post;
+  a.gamma = gamma;
+  a.ldy = ldy;
+  a.ldh = ldh;
+  a.ldg = ldg;
+  a.ldo = ldo;
+  a.eps_post = eps_post;
+  a.rs = rs;
+  a.eps = eps;
+  a.K = K;
+  a.qt = qt;
+  a.Xq = reinterpret_cast<uint8_t*>(Xq);
+  a.sx = sx;
+  a.ms_out = ms_out;
+  const int nvec = K / 8;
+  int t = 32;
+  while (t < kThreads && t * (M < 304 ? 2 : 4) < nvec) t *= 2;
+  return launch_pdl(residual_rmsnorm_quant_kernel<kNC>, dim3(M), dim3(t), 0, st, a);
+}
+
+}  // namespace qurl

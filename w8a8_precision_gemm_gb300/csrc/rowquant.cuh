@@ -360,23 +360,31 @@ __device__ __forceinline__ float scaled_absmax(float amax, float pre) {
   return pre == 0.0f ? 0.0f : __fmul_rn(amax, fabsf(pre));
 }
 
+// A 16-byte vector of a row: through the read-only path, or (kOwn) by a plain
+// load where the row is one that the calling thread itself has written.
+template <bool kOwn>
+__device__ __forceinline__ uint4 load_vec(const uint4* p) {
+  if constexpr (kOwn) return *p;
+  else return __ldg(p);
+}
+
 // Visit the 16-byte vectors idx = threadIdx.x + c * blockDim.x of a row: the
 // first kVPT from the register cache (fully unrolled, so the cache stays in
 // registers), the rest (rows longer than kVPT * blockDim vectors) from memory.
-template <int NC, typename F>
+template <int NC, bool kOwn = false, typename F>
 __device__ __forceinline__ void for_vectors(const uint4* row, int nvec, const uint4 (&cache)[NC], F&& f) {
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     const int idx = threadIdx.x + c * blockDim.x;
     if (idx < nvec) f(cache[c], idx);
   }
-  for (int idx = threadIdx.x + NC * blockDim.x; idx < nvec; idx += blockDim.x) f(__ldg(row + idx), idx);
+  for (int idx = threadIdx.x + NC * blockDim.x; idx < nvec; idx += blockDim.x) f(load_vec<kOwn>(row + idx), idx);
 }
 
 // The same vectors, visited warp-uniformly: every lane calls f(u, idx, valid)
 // in every step of its warp (u is undefined where !valid), so f may use warp
 // collectives.  blockDim.x is a multiple of 32.
-template <int NC, typename F>
+template <int NC, bool kOwn = false, typename F>
 __device__ __forceinline__ void for_vectors_warp(const uint4* row, int nvec, const uint4 (&cache)[NC], F&& f) {
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
@@ -386,7 +394,7 @@ __device__ __forceinline__ void for_vectors_warp(const uint4* row, int nvec, con
   for (int i0 = NC * blockDim.x + (threadIdx.x & ~31); i0 < nvec; i0 += blockDim.x) {
     const int idx = i0 + (threadIdx.x & 31);
     const bool valid = idx < nvec;
-    f(valid ? __ldg(row + idx) : make_uint4(0, 0, 0, 0), idx, valid);
+    f(valid ? load_vec<kOwn>(row + idx) : make_uint4(0, 0, 0, 0), idx, valid);
   }
 }
 
@@ -444,6 +452,87 @@ __device__ __forceinline__ void quant_act_row(int m, const __nv_bfloat16* __rest
   sums_end(sh.cnt, sums, m);
 }
 
+// Mean of squares of a row (block_mean_sq) and r = 1 / sqrt(ms + eps).  Each
+// x^2 is exact in fp32 (a bf16 has an 8-bit significand); the sum is carried as
+// an unevaluated pair s + c (error-free two-sum per term, Knuth) and divided by
+// K in fp64, so ms is the fp32 rounding of the mean to within ~2^-44 relative
+// -- the same fp32 value a plain fp64 sum gives, except when the mean lies that
+// close to a rounding midpoint.  The gain of the vectors this thread normalises
+// is read while the sums are reduced.
+template <int NC, bool kOwn>
+__device__ __forceinline__ void row_rms(const uint4* row, int K, const uint4 (&cache)[NC], const float4* gain,
+                                        float eps, float* red, float& ms, float& r) {
+  const int nvec = K >> 3;
+  float2 ss2 = make_float2(0.0f, 0.0f), sc2 = make_float2(0.0f, 0.0f);  // even / odd k
+  for_vectors<NC, kOwn>(row, nvec, cache, [&](const uint4 u, int) {
+    float2 x[4];
+    bf16x8_to_f2(u, x);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) two_sum_acc2(ss2, sc2, mul2(x[e], x[e]));
+  });
+  float ss = ss2.x, sc = sc2.x;
+  two_sum_acc(ss, sc, ss2.y);
+  sc = __fadd_rn(sc, sc2.y);
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int idx = threadIdx.x + c * blockDim.x;
+    if (idx < nvec) asm volatile("prefetch.global.L1 [%0];" ::"l"(gain + 2 * idx));
+  }
+  block_mean_sq(ss, sc, red, K, eps, ms, r);
+}
+
+// (x * r) * gain of 8 values, each product rounded to fp32.
+__device__ __forceinline__ void norm8(const uint4 u, const float4* gain, int idx, float2 r2, float2 (&x)[4]) {
+  bf16x8_to_f2(u, x);
+  const float4 ga = __ldg(gain + 2 * idx), gb = __ldg(gain + 2 * idx + 1);
+  const float2 g[4] = {make_float2(ga.x, ga.y), make_float2(ga.z, ga.w), make_float2(gb.x, gb.y),
+                       make_float2(gb.z, gb.w)};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) x[e] = mul2(mul2(x[e], r2), g[e]);
+}
+
+// RMSNorm of row m, whose vectors are in the register cache (and at `row`,
+// read again where the row is longer than the cache; kOwn: the calling thread
+// wrote them), with the folded gain gamma', then per-token quantization
+// (ms_out[m], when given, receives the row's mean of squares).  sums_begin and
+// a barrier come before it.
+template <int NC, bool kOwn>
+__device__ __forceinline__ void rmsnorm_quant_cached(int m, const uint4* row, const uint4 (&cache)[NC], int K,
+                                                     const float* __restrict__ gamma, float eps, int qt,
+                                                     uint8_t* __restrict__ Xq, float* __restrict__ sx,
+                                                     float* __restrict__ ms_out, uint8_t* __restrict__ x16,
+                                                     const CodeSums& sums, RowScratch& sh) {
+  const float4* g4 = reinterpret_cast<const float4*>(gamma);
+  const int nvec = K >> 3;
+  float ms, r;
+  row_rms<NC, kOwn>(row, K, cache, g4, eps, sh.red, ms, r);
+  if (threadIdx.x == 0 && ms_out) ms_out[m] = ms;
+  // v = (x * r) * gamma'
+  const float2 r2 = splat2(r);
+  float amax = 0.0f;
+  for_vectors<NC, kOwn>(row, nvec, cache, [&](const uint4 u, int idx) {
+    float2 x[4];
+    norm8(u, g4, idx, r2, x);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fmaxf(fabsf(x[e].x), fabsf(x[e].y)));
+  });
+  amax = block_reduce<true>(amax, sh.red);
+  const Enc en = make_enc(amax, qt);
+  if (threadIdx.x == 0) sx[m] = en.scale;
+  uint8_t* out = Xq + static_cast<size_t>(m) * K;
+  uint8_t* out16 = x16 ? x16 + static_cast<size_t>(m) * K * 2 : nullptr;
+  for_vectors_warp<NC, kOwn>(row, nvec, cache, [&](const uint4 u, int idx, bool valid) {
+    int2 v = make_int2(0, 0);
+    if (valid) {
+      float2 x[4];
+      norm8(u, g4, idx, r2, x);
+      v = store8(out, out16, idx, x, en);
+    }
+    sums_add_warp(sh.cnt, sums, idx, v);
+  });
+  sums_end(sh.cnt, sums, m);
+}
+
 // RMSNorm of row m with the folded gain gamma', then per-token quantization
 // (ms_out[m], when given, receives the row's mean of squares).
 template <int NC>
@@ -456,67 +545,9 @@ __device__ __forceinline__ void rmsnorm_quant_row(int m, const __nv_bfloat16* __
   __syncthreads();  // the previous row's reductions and sums are done with the scratch
   sums_begin(sh.cnt, sums);
   const uint4* row = reinterpret_cast<const uint4*>(X + static_cast<size_t>(m) * ldx);
-  const float4* g4 = reinterpret_cast<const float4*>(gamma);
-  const int nvec = K >> 3;
   uint4 cache[NC];
-  fill_cache(row, nvec, cache);
-  // mean of squares.  Each x^2 is exact in fp32 (a bf16 has an 8-bit
-  // significand); the sum is carried as an unevaluated pair s + c (error-free
-  // two-sum per term, Knuth) and divided by K in fp64, so ms is the fp32
-  // rounding of the mean to within ~2^-44 relative -- the same fp32 value a
-  // plain fp64 sum gives, except when the mean lies that close to a rounding
-  // midpoint.
-  float2 ss2 = make_float2(0.0f, 0.0f), sc2 = make_float2(0.0f, 0.0f);  // even / odd k
-  for_vectors(row, nvec, cache, [&](const uint4 u, int) {
-    float2 x[4];
-    bf16x8_to_f2(u, x);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) two_sum_acc2(ss2, sc2, mul2(x[e], x[e]));
-  });
-  float ss = ss2.x, sc = sc2.x;
-  two_sum_acc(ss, sc, ss2.y);
-  sc = __fadd_rn(sc, sc2.y);
-  // the gain of the vectors this thread normalises is read while the sums are reduced
-#pragma unroll
-  for (int c = 0; c < NC; ++c) {
-    const int idx = threadIdx.x + c * blockDim.x;
-    if (idx < nvec) asm volatile("prefetch.global.L1 [%0];" ::"l"(g4 + 2 * idx));
-  }
-  float ms, r;
-  block_mean_sq(ss, sc, sh.red, K, eps, ms, r);
-  if (threadIdx.x == 0 && ms_out) ms_out[m] = ms;
-  // v = (x * r) * gamma'
-  const float2 r2 = splat2(r);
-  auto normed = [&](const uint4 u, int idx, float2 (&x)[4]) {
-    bf16x8_to_f2(u, x);
-    const float4 ga = __ldg(g4 + 2 * idx), gb = __ldg(g4 + 2 * idx + 1);
-    const float2 g[4] = {make_float2(ga.x, ga.y), make_float2(ga.z, ga.w), make_float2(gb.x, gb.y),
-                         make_float2(gb.z, gb.w)};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = mul2(mul2(x[e], r2), g[e]);
-  };
-  float amax = 0.0f;
-  for_vectors(row, nvec, cache, [&](const uint4 u, int idx) {
-    float2 x[4];
-    normed(u, idx, x);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fmaxf(fabsf(x[e].x), fabsf(x[e].y)));
-  });
-  amax = block_reduce<true>(amax, sh.red);
-  const Enc en = make_enc(amax, qt);
-  if (threadIdx.x == 0) sx[m] = en.scale;
-  uint8_t* out = Xq + static_cast<size_t>(m) * K;
-  uint8_t* out16 = x16 ? x16 + static_cast<size_t>(m) * K * 2 : nullptr;
-  for_vectors_warp(row, nvec, cache, [&](const uint4 u, int idx, bool valid) {
-    int2 v = make_int2(0, 0);
-    if (valid) {
-      float2 x[4];
-      normed(u, idx, x);
-      v = store8(out, out16, idx, x, en);
-    }
-    sums_add_warp(sh.cnt, sums, idx, v);
-  });
-  sums_end(sh.cnt, sums, m);
+  fill_cache(row, K >> 3, cache);
+  rmsnorm_quant_cached<NC, false>(m, row, cache, K, gamma, eps, qt, Xq, sx, ms_out, x16, sums, sh);
 }
 
 __device__ __forceinline__ float silu_ratio(float g, float den) {
