@@ -898,9 +898,10 @@ qurl_status qurl_kv_cache_dequant(const void* cache, const float* scale, const i
 }
 
 size_t qurl_kv_attn_workspace_size(int B, int q_heads, int kv_heads, int head_dim, int max_blocks, int block_size) {
-  if (B < 0 || q_heads <= 0 || kv_heads <= 0 || head_dim <= 0 || max_blocks < 0 || block_size <= 0) return 0;
-  return qurl::attn_workspace_bytes(B, q_heads, kv_heads, head_dim, static_cast<long long>(max_blocks) * block_size,
-                                    device_sms());
+  if (B < 0 || q_heads <= 0 || kv_heads <= 0 || head_dim <= 0 || max_blocks < 0 || block_size <= 0 ||
+      q_heads % kv_heads != 0)
+    return 0;
+  return qurl::attn_workspace_bytes(q_heads, kv_heads, head_dim, device_sms());
 }
 
 qurl_status qurl_kv_attn_decode(const void* q, int ldq, int B, int q_heads, int kv_heads, int head_dim,
@@ -929,9 +930,7 @@ qurl_status qurl_kv_attn_decode(const void* q, int ldq, int B, int q_heads, int 
     return QURL_ERR_ALIGNMENT;
   DevState* dev = nullptr;
   QURL_TRY(device_state(&dev));
-  if (ws_bytes < qurl::attn_workspace_bytes(B, q_heads, kv_heads, head_dim,
-                                            static_cast<long long>(max_blocks) * block_size, dev->num_sms))
-    return QURL_ERR_WORKSPACE;
+  if (ws_bytes < qurl::attn_workspace_bytes(q_heads, kv_heads, head_dim, dev->num_sms)) return QURL_ERR_WORKSPACE;
   qurl::AttnArgs a{};
   a.q = reinterpret_cast<const __nv_bfloat16*>(q);
   a.ldq = ldq;

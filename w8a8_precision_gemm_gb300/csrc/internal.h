@@ -195,7 +195,7 @@ struct AttnArgs {
   void* ws;
   int* status;
 };
-size_t attn_workspace_bytes(int B, int q_heads, int kv_heads, int head_dim, long long max_len, int num_sms);
+size_t attn_workspace_bytes(int q_heads, int kv_heads, int head_dim, int num_sms);
 cudaError_t launch_kv_attn_decode(const AttnArgs& a, int num_sms, cudaStream_t st);
 // sample.cu: one token per row of logits from a given uniform number (qurl_sample).
 struct SampleArgs {
