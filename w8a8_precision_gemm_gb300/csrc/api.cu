@@ -1010,8 +1010,7 @@ qurl_status qurl_sample(const void* logits, qurl_ftype x_type, int B, int V, int
   a.logp = logp;
   a.logp_kept = logp_kept;
   a.status = dev->status;
-  while ((1LL << a.shift) < V) ++a.shift;
-  QURL_CUDA(qurl::launch_sample(a, x_type == QURL_FP32, reinterpret_cast<cudaStream_t>(stream)));
+  QURL_CUDA(qurl::launch_sample(a, x_type == QURL_FP32, dev->num_sms, reinterpret_cast<cudaStream_t>(stream)));
   return QURL_OK;
 }
 

@@ -9,6 +9,7 @@
 #include <atomic>
 #include <cstddef>
 #include <cstdint>
+#include <utility>
 
 namespace qurl {
 
@@ -125,10 +126,10 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
   return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
 }
 
-// launch_pdl for a kernel whose CTAs work in clusters of two (grid.x even).
+// launch_pdl for a kernel whose CTAs work in clusters of `cluster` (which divides grid.x).
 template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl_pair(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                            Args&&... args) {
+cudaError_t launch_pdl_cluster(void (*kern)(KArgs...), int cluster, dim3 grid, dim3 block, size_t smem,
+                               cudaStream_t st, Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
@@ -138,13 +139,20 @@ cudaError_t launch_pdl_pair(void (*kern)(KArgs...), dim3 grid, dim3 block, size_
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   g_kernel_launches.fetch_add(1, std::memory_order_relaxed);
   return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
+}
+
+// ... in clusters of two (grid.x even).
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl_pair(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                            Args&&... args) {
+  return launch_pdl_cluster(kern, 2, grid, block, smem, st, std::forward<Args>(args)...);
 }
 
 // quant.cu.  x16 (may be null): also write the INT8 codes as fp16 [M, K]
@@ -210,10 +218,10 @@ struct SampleArgs {
   long long* token;
   float* logp;       // null: not wanted
   float* logp_kept;  // null: not wanted
-  int shift;         // 62 - log2 of the largest weight
+  int shift;         // ceil(log2 V) + 1, set by the launch
   int* status;
 };
-cudaError_t launch_sample(const SampleArgs& a, bool f32, cudaStream_t st);
+cudaError_t launch_sample(const SampleArgs& a, bool f32, int num_sms, cudaStream_t st);
 // logprob.cu: log-probabilities of given tokens and the logits' gradient.
 cudaError_t launch_token_logprob(const void* X, bool f32, long long T, int V, long long ld, const long long* targets,
                                  float inv_t, float* logp, float* lse, int* status, cudaStream_t st);
