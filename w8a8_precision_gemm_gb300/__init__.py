@@ -60,6 +60,8 @@ def exported_names() -> list[str]:
 def load() -> ctypes.CDLL:
     """Load libqurl.so (built by ``_build.build()``); raises if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -131,12 +133,12 @@ def _ptr(t):
         return None
     if not t.is_cuda:
         raise ValueError("libqurl takes device tensors only")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _stream(stream=None):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    # (the raw handle of torch.cuda.current_stream(), without the Stream object it is wrapped in)
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) if stream is None else stream.cuda_stream
 
 
 def _ok(rc: int, where: str):
@@ -160,12 +162,12 @@ def _dense(*ts):
 
 def _here(first, *ts):
     """The tensors of a call live on the current device: its kernels are launched there."""
-    dev = first.device
-    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
-        raise ValueError(f"expected tensors on the current CUDA device, got {dev}")
+    dev = first.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise ValueError(f"expected tensors on the current CUDA device, got {first.device}")
     for t in ts:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}")
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors on {first.device} and {t.device}")
 
 
 def _typed(t, dtype, what, n=None):

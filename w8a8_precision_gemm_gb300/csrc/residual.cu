@@ -30,6 +30,10 @@ using namespace rq;
 
 constexpr int kNC = 8;        // 16-byte vectors cached per thread
 constexpr int kThreads = 512;  // most threads of a row CTA
+#ifndef KMANY
+#define KMANY 4
+#endif
+constexpr int kMany = KMANY;
 
 struct ResidualArgs {
   const __nv_bfloat16* Y;
@@ -73,7 +77,10 @@ __device__ __forceinline__ uint4 update8(const ResidualArgs& a, const uint4 yu, 
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-template <int NC, int MAXT = kThreads, int MINB = 1>
+// One row per CTA.  NC: vectors a thread holds; KEEP: they are all of the row
+// (no thread has more), and the normalised values stay in registers between the
+// absmax and the codes instead of being computed twice.
+template <int NC, bool KEEP, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) residual_rmsnorm_quant_kernel(const ResidualArgs a) {
   griddep_wait();
   griddep_launch_dependents();
@@ -106,10 +113,37 @@ __global__ void __launch_bounds__(MAXT, MINB) residual_rmsnorm_quant_kernel(cons
     const int idx = threadIdx.x + c * blockDim.x;
     if (idx < nvec) orow[idx] = hc[c] = update8(a, yc[c], hc[c], grow, idx, r2, rs2);
   }
-  for (int idx = threadIdx.x + NC * blockDim.x; idx < nvec; idx += blockDim.x)
-    orow[idx] = update8(a, __ldg(yrow + idx), hrow[idx], grow, idx, r2, rs2);
-  const CodeSums none{};
-  rmsnorm_quant_cached<NC, true>(m, orow, hc, a.K, a.gamma, a.eps, a.qt, a.Xq, a.sx, a.ms_out, nullptr, none, sh);
+  if constexpr (!KEEP) {
+    for (int idx = threadIdx.x + NC * blockDim.x; idx < nvec; idx += blockDim.x)
+      orow[idx] = update8(a, __ldg(yrow + idx), hrow[idx], grow, idx, r2, rs2);
+    const CodeSums none{};
+    rmsnorm_quant_cached<NC, true>(m, orow, hc, a.K, a.gamma, a.eps, a.qt, a.Xq, a.sx, a.ms_out, nullptr, none, sh);
+  } else {
+    const float4* g4 = reinterpret_cast<const float4*>(a.gamma);
+    float ms, r;
+    row_rms<NC, true>(orow, a.K, hc, g4, a.eps, sh.red, ms, r);
+    if (threadIdx.x == 0 && a.ms_out) a.ms_out[m] = ms;
+    r2 = splat2(r);
+    float2 v[NC][4];
+    float amax = 0.0f;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int idx = threadIdx.x + c * blockDim.x;
+      if (idx >= nvec) continue;
+      norm8(hc[c], g4, idx, r2, v[c]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fmaxf(fabsf(v[c][e].x), fabsf(v[c][e].y)));
+    }
+    amax = block_reduce<true>(amax, sh.red);
+    const Enc en = make_enc(amax, a.qt);
+    if (threadIdx.x == 0) a.sx[m] = en.scale;
+    uint8_t* out = a.Xq + static_cast<size_t>(m) * a.K;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int idx = threadIdx.x + c * blockDim.x;
+      if (idx < nvec) store8(out, nullptr, idx, v[c], en);
+    }
+  }
 }
 
 }  // namespace
@@ -137,10 +171,15 @@ cudaError_t launch_residual_rmsnorm_quant(const void* Y, long long ldy, const fl
   a.Xq = reinterpret_cast<uint8_t*>(Xq);
   a.sx = sx;
   a.ms_out = ms_out;
+  // As few vectors a thread as the row allows: its serial chain is short and
+  // many rows are resident.
   const int nvec = K / 8;
-  int t = 32;
-  while (t < kThreads && t * (M < 304 ? 2 : 4) < nvec) t *= 2;
-  return launch_pdl(residual_rmsnorm_quant_kernel<kNC>, dim3(M), dim3(t), 0, st, a);
+  const int one = (nvec + 31) / 32 * 32, two = (nvec + 63) / 64 * 32;
+  // few rows: a vector a thread
+  if (M < 304 && nvec <= 1024) return launch_pdl(residual_rmsnorm_quant_kernel<1, true, 1024, 1>, dim3(M), dim3(one), 0, st, a);
+  if (two <= 320) return launch_pdl(residual_rmsnorm_quant_kernel<2, true, 320, kMany>, dim3(M), dim3(two), 0, st, a);
+  if (two <= 512) return launch_pdl(residual_rmsnorm_quant_kernel<2, true, 512, 3>, dim3(M), dim3(two), 0, st, a);
+  return launch_pdl(residual_rmsnorm_quant_kernel<kNC, false, kThreads, 1>, dim3(M), dim3(kThreads), 0, st, a);
 }
 
 }  // namespace qurl

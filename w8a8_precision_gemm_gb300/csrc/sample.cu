@@ -23,12 +23,15 @@
 //
 // A row is worked on by a cluster of 1 to 8 CTAs, as many as fill the GPU with
 // the batch.  Pass 1 takes the maximum; the threads' own maxima give a cut above
-// which about 300 logits lie.  Pass 2 (the row now comes from L2)
-// takes the sum and sends the logits above the cut to the cluster's first CTA,
-// which ranks them against each other and draws -- all there is to do unless the
-// kept set is larger.  Then a histogram of the whole row by equal steps of x
-// (count and weight) finds the step in which a limit falls, the step's logits
-// alone are collected, and a radix select among them gives the limit.
+// which about 128 logits lie.  Pass 2 (the row now comes from L2) takes the sum
+// and sends the logits above the cut to the cluster's first CTA, which ranks
+// them against each other and draws -- all there is to do unless the kept set is
+// larger.  Then an eighth of the row says between which logits a limit falls; one
+// pass adds up what lies above and cuts the window into 512 steps of count and
+// weight (shared-memory atomics are what a histogram of the whole row would be
+// bound by), the logits of the one step that holds the limit are collected, a
+// radix select among them gives it, and a last pass gives every segment's kept
+// weight.  A limit outside its window is looked for in the whole row.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -46,11 +49,11 @@ using u64 = unsigned long long;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTable = 512;
-constexpr int kSeg = 1024;       // logits per segment: a warp's step, and the unit of the final search
-constexpr int kMaxSegs = 512;    // segments (of a multiple of kSeg logits) a row is cut into at most
+constexpr int kSeg = 512;        // logits per segment (or a multiple), the unit of the final search
+constexpr int kMaxSegs = 512;    // segments a row is cut into at most
 constexpr int kShort = 512;      // candidates ranked against each other
-constexpr int kAim = 320;        // candidates the cut aims at
-constexpr int kList = 4096;      // logits of one histogram step collected for the radix select
+constexpr int kAim = 128;        // candidates the cut aims at, more for a large top-k
+constexpr int kList = 1536;      // logits of one step collected for the radix select
 constexpr int kBins = 512;
 constexpr u64 kAll = ~0ull;
 
@@ -89,7 +92,7 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 
 // Position of a logit in the order: smaller comes first.
 __device__ __forceinline__ u64 place(float x, int i) {
-  return (static_cast<u64>(~order_key(x)) << 32) | static_cast<uint32_t>(i);
+  return (static_cast<u64>(~order_key(clean(x))) << 32) | static_cast<uint32_t>(i);
 }
 __device__ __forceinline__ float place_logit(u64 p) { return key_value(~static_cast<uint32_t>(p >> 32)); }
 
@@ -108,24 +111,27 @@ constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: adding it rounds to an int
 // that exponent for the largest logit (in relative rows of x - top).
 __device__ __forceinline__ u64 weight(float x, const Scale& s, const uint32_t* table) {
   float d = x, dl = 0.0f;
-  if (s.rel) {  // x - top as an exact pair (two-sum)
+  if (s.rel) {  // x - top as an exact pair (two-sum); +inf counts as the largest float
+    x = x > FLT_MAX ? FLT_MAX : x;
     d = __fsub_rn(x, s.top);
     const float bb = __fsub_rn(d, x);
     dl = __fsub_rn(__fsub_rn(x, __fsub_rn(d, bb)), __fadd_rn(s.top, bb)) * s.chi;
   }
   const float ph = __fmul_rn(d, s.chi);
-  const float pl = fmaf(d, s.clo, fmaf(d, s.chi, -ph)) + dl;
+  float pl = fmaf(d, s.clo, fmaf(d, s.chi, -ph));
+  if (s.rel) pl += dl;
   // ph + pl = k / 512 + r, |r| <= 2^-10 and a little
   const float t = fmaf(ph, static_cast<float>(kTable), kMagic);
   const int k = static_cast<int>(__float_as_uint(t));  // 0x4B400000 + k
   const float r = fmaf(t - kMagic, -1.0f / kTable, ph) + pl;
-  // 2^r - 1 = y + y^2 / 2 + y^3 / 6, y = r ln 2: the next term is below 2^-43
-  const float y = r * 0.693147180559945309f;
-  const float q = fmaf(y * y, fmaf(y, 1.0f / 6.0f, 0.5f), y);
-  const int qi = static_cast<int>(__float_as_uint(fmaf(q, 4294967296.0f, kMagic))) - 0x4B400000;
+  // 2^32 (2^r - 1) = 2^32 (r ln 2 + (r ln 2)^2 / 2 + (r ln 2)^3 / 6) as an integer: the next term is below 2^-43
+  constexpr double kLn2 = 0.69314718055994530942, kUnit = 4294967296.0;
+  const float c = fmaf(r, fmaf(r, static_cast<float>(kUnit * kLn2 * kLn2 * kLn2 / 6), static_cast<float>(kUnit * kLn2 * kLn2 / 2)),
+                       static_cast<float>(kUnit * kLn2));
+  const int qi = static_cast<int>(__float_as_uint(fmaf(r, c, kMagic))) - 0x4B400000;
   const uint32_t tj = table[k & (kTable - 1)];
   const uint32_t w = tj + static_cast<uint32_t>(__mulhi(static_cast<int>(tj), qi));
-  const int n = min(s.bias - (k >> 9), 63);  // bits to shift (w : 0) down by
+  const int n = s.bias - (k >> 9);  // bits to shift (w : 0) down by: 0 .. 63 where the weight is not 0
   const u64 v = (static_cast<u64>(w) << 32) >> (n & 63);
   return ph > s.zero ? v : 0;  // (false for what is not a number)
 }
@@ -143,61 +149,84 @@ struct Load;
 template <>
 struct Load<float> {
   static constexpr int N = 4;
-  static __device__ __forceinline__ float one(const float* p) { return clean(__ldg(p)); }
+  static __device__ __forceinline__ float one(const float* p) { return __ldg(p); }
   static __device__ __forceinline__ void vec(const uint4 u, float (&x)[4]) {
-    x[0] = clean(__uint_as_float(u.x));
-    x[1] = clean(__uint_as_float(u.y));
-    x[2] = clean(__uint_as_float(u.z));
-    x[3] = clean(__uint_as_float(u.w));
+    x[0] = __uint_as_float(u.x);
+    x[1] = __uint_as_float(u.y);
+    x[2] = __uint_as_float(u.z);
+    x[3] = __uint_as_float(u.w);
   }
 };
 template <>
 struct Load<__nv_bfloat16> {
   static constexpr int N = 8;
   static __device__ __forceinline__ float one(const __nv_bfloat16* p) {
-    return clean(__bfloat162float(*p));
+    return __bfloat162float(*p);
   }
   static __device__ __forceinline__ void vec(const uint4 u, float (&x)[8]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      x[2 * e] = clean(__uint_as_float(w[e] << 16));
-      x[2 * e + 1] = clean(__uint_as_float(w[e] & 0xFFFF0000u));
+      x[2 * e] = __uint_as_float(w[e] << 16);
+      x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
     }
   }
 };
 
-// A CTA's part of a row: segments s0 .. s1 of `seg` logits, its warps in turn.
+// A warp's part of a row: steps t0 .. t1 of 32 vectors, whole segments of `per`
+// steps.
 template <typename T>
 struct Part {
+  static constexpr int N = Load<T>::N;
   const T* x;
-  int V, seg, s0, s1;
+  int V, per, t0, t1;
 
-  // f(x, i) for every logit of segment s, by the calling warp
-  template <typename F>
-  __device__ __forceinline__ void segment(int s, F&& f) const {
-    constexpr int N = Load<T>::N, U = 4;  // U vectors in flight a lane
-    const int lane = threadIdx.x & 31;
-    const int end = static_cast<int>(min(static_cast<long long>(s + 1) * seg, static_cast<long long>(V)));
-    int i = s * seg;
-    for (; i + 32 * N * U <= end; i += 32 * N * U) {
-      uint4 u[U];
-#pragma unroll
-      for (int e = 0; e < U; ++e) u[e] = __ldg(reinterpret_cast<const uint4*>(x + i) + e * 32 + lane);
-#pragma unroll
-      for (int e = 0; e < U; ++e) {
-        float v[N];
-        Load<T>::vec(u[e], v);
-#pragma unroll
-        for (int j = 0; j < N; ++j) f(v[j], i + (e * 32 + lane) * N + j);
-      }
-    }
-    for (i += lane; i < end; i += 32) f(Load<T>::one(x + i), i);
+  __device__ __forceinline__ uint4 load(int t) const {
+    const int v = t * 32 + (threadIdx.x & 31);
+    return t < t1 && v < V / N ? __ldg(reinterpret_cast<const uint4*>(x) + v) : make_uint4(0, 0, 0, 0);
   }
-  // f for every logit of the part
+  // f(x, i, n): N logits from index i on, n of them in the row (the rest are -inf)
+  template <typename F>
+  __device__ __forceinline__ void step(int t, const uint4 u, F&& f) const {
+    const int i = (t * 32 + (threadIdx.x & 31)) * N, n = min(V - i, N);
+    float v[N];
+    if (n == N) {
+      Load<T>::vec(u, v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < N; ++e) v[e] = e < n ? Load<T>::one(x + i + e) : -INFINITY;
+    }
+    f(v, i, n);
+  }
+  // f for every vector of the part, end(s) after each segment s; two steps are in flight.  (Not unrolled: several
+  // such loops with a thousand instructions each do not fit the instruction cache, which halved their speed.)
+  template <typename F, typename E>
+  __device__ __forceinline__ void run(F&& f, E&& end) const {
+    uint4 a = load(t0), b = load(t0 + 1);
+#pragma unroll 1
+    for (int t = t0; t < t1; ++t) {
+      const uint4 c = load(t + 2);
+      step(t, a, f);
+      if ((t + 1) % per == 0 || t + 1 == t1) end(t / per);
+      a = b;
+      b = c;
+    }
+  }
   template <typename F>
   __device__ __forceinline__ void all(F&& f) const {
-    for (int s = s0 + (threadIdx.x >> 5); s < s1; s += kWarps) segment(s, f);
+    run(f, [](int) {});
+  }
+  // f for every `stride`-th step
+  template <typename F>
+  __device__ __forceinline__ void sample(int stride, F&& f) const {
+    int t = t0 + (threadIdx.x >> 5) % stride;
+    uint4 a = load(t);
+#pragma unroll 1
+    for (; t < t1; t += stride) {
+      const uint4 b = load(t + stride);
+      step(t, a, f);
+      a = b;
+    }
   }
 };
 
@@ -209,11 +238,6 @@ __device__ __forceinline__ void remote_add64(uint32_t a, u64 v) {
 }
 __device__ __forceinline__ void remote_add32(uint32_t a, uint32_t v) {
   asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
-}
-__device__ __forceinline__ uint32_t remote_take(uint32_t a) {
-  uint32_t r;
-  asm volatile("atom.relaxed.cluster.shared::cluster.add.u32 %0, [%1], 1;" : "=r"(r) : "r"(a) : "memory");
-  return r;
 }
 __device__ __forceinline__ void remote_max32(uint32_t a, uint32_t v) {
   asm volatile("red.relaxed.cluster.shared::cluster.max.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
@@ -229,12 +253,16 @@ __device__ __forceinline__ void remote_put64(uint32_t a, u64 v) {
 enum : int { kDone = 0, kHistogram = 1, kCollect = 2, kSums = 3 };
 
 struct Shared {
-  u64 list[kList];  // first CTA: places of the candidates, then of one histogram step
+  u64 own[kList];   // places that this CTA found: candidates, then the logits of one step
+  u64 list[kList];  // first CTA: those of the whole cluster
   u64 w[kShort];    // their weights
-  u64 mass[kBins];
-  u64 segs[kMaxSegs];
+  u64 mass[kBins];          // by step: weight,
+  u64 segs[kMaxSegs];       // by segment: weight above the window (first CTA, at the end: all kept weight),
+  u64 part_segs[kMaxSegs];  // and between it and the step that was collected
   u64 part[kWarps];
-  uint32_t count[kBins];
+  uint32_t count[kBins];    // and count
+  u64 sample_mass[kBins];   // first CTA: those of the sample
+  uint32_t sample_count[kBins];
   uint32_t table[kTable];
   u64 hist[256];
   u64 total;       // first CTA: the row's sum (weights, or 2^32 times the fp32 one)
@@ -243,8 +271,19 @@ struct Shared {
   uint32_t top, low;  // ordered keys: largest logit, smallest
   uint32_t cut;       // ordered key
   uint32_t n;         // first CTA: entries of the list
-  int order, bin;     // the next step, and its histogram step
+  uint32_t own_n, own_at;
+  int order, bin;     // what to do next, and the step to collect
+  float hi, lo, ref, scale;  // the window: logits above hi, those down to lo by (ref - x) scale
+  u64 picked;
+  u64 above_mass;     // first CTA: what lies above the window
+  u64 above_count;
+  u64 have;           // first CTA: weight of the candidates (0: they were too many)
+  double drop;        // temperature ln(min_p)
+  float share;        // of the sample that lies before a limit
   int found;
+  int pick_lo, pick_hi;
+  float sq[kWarps];
+  uint32_t short_n;   // candidates ranked
   int token;
   float chi, clo;
   u64 found_before;
@@ -295,17 +334,46 @@ __device__ u64 block_scan(u64 v, u64& all, Shared& sh) {
 // them stay below it.  each(f) calls f(place) for the elements, by the block.
 template <bool kMass, typename Each>
 __device__ u64 radix_select(Each&& each, const Scale& s, u64 target, Shared& sh) {
-  u64 prefix = 0, before = 0;
-  for (int shift = 56; shift >= 0; shift -= 8) {
+  // the bits that all elements share are skipped (a digit that all share would have every thread add to one counter)
+  u64 least = kAll, most = 0;
+  each([&](u64 p) {
+    least = p < least ? p : least;
+    most = p > most ? p : most;
+  });
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    sh.hist[0] = kAll;
+    sh.hist[1] = 0;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const u64 a = __shfl_xor_sync(0xFFFFFFFFu, least, o), b = __shfl_xor_sync(0xFFFFFFFFu, most, o);
+    least = a < least ? a : least;
+    most = b > most ? b : most;
+  }
+  if ((threadIdx.x & 31) == 0) {
+    atomicMin(&sh.hist[0], least);
+    atomicMax(&sh.hist[1], most);
+  }
+  __syncthreads();
+  least = sh.hist[0];
+  most = sh.hist[1];
+  if (least > most) return kAll;  // no elements
+  int top = 64 - __clzll(static_cast<long long>(least ^ most));  // bits not known yet
+  u64 prefix = top == 64 ? 0 : most & (kAll << top), before = 0;
+  while (top > 0) {
+    const int shift = max(top - 8, 0);
+    const u64 known = top == 64 ? 0 : kAll << top;
+    const uint32_t digits = (1u << (top - shift)) - 1;
     __syncthreads();
     sh.hist[threadIdx.x] = 0;
     if (threadIdx.x == 0) sh.found = -1;
     __syncthreads();
-    const u64 known = shift == 56 ? 0 : kAll << (shift + 8);
     each([&](u64 p) {
       if ((p & known) != prefix) return;
       const u64 v = kMass ? weight(place_logit(p), s, sh.table) : 1ull;
-      if (v) atomicAdd(&sh.hist[(p >> shift) & 255], v);
+      if (v) atomicAdd(&sh.hist[static_cast<uint32_t>(p >> shift) & digits], v);
     });
     __syncthreads();
     const u64 v = sh.hist[threadIdx.x];
@@ -319,6 +387,7 @@ __device__ u64 radix_select(Each&& each, const Scale& s, u64 target, Shared& sh)
     if (sh.found < 0) return kAll;
     before = sh.found_before;
     prefix |= static_cast<u64>(sh.found) << shift;
+    top = shift;
   }
   return prefix;
 }
@@ -350,13 +419,41 @@ __device__ __forceinline__ Params params_of(const SampleArgs& a, int b) {
   return p;
 }
 
+// floor(f * v) for f in [0, 1); `rest`: whether something was cut off.
+__device__ __forceinline__ u64 fraction(float f, u64 v, bool& rest) {
+  const uint32_t b = __float_as_uint(f);
+  rest = false;
+  if (b < 0x00800000u) return 0;  // 0, or below 2^-126
+  const u64 m = (b & 0x7FFFFFu) | 0x800000u;
+  const int e = 150 - static_cast<int>(b >> 23);  // f = m 2^-e, 24 <= e
+  const u64 hi = __umul64hi(v, m), lo = v * m;
+  if (e < 64) {
+    rest = (lo & ((1ull << e) - 1)) != 0;
+    return (hi << (64 - e)) | (lo >> e);
+  }
+  rest = true;
+  return e < 128 ? hi >> (e - 64) : 0;
+}
 // The weight that ends a nucleus: the smallest integer not below top_p times base (at least 1).
 __device__ __forceinline__ u64 nucleus(float top_p, u64 base) {
-  const u64 t = static_cast<u64>(ceil(static_cast<double>(top_p) * static_cast<double>(base)));
+  bool rest;
+  u64 t = fraction(top_p, base, rest);
+  if (rest) ++t;
   return t < 1 ? 1 : t;
 }
 __device__ __forceinline__ u64 goal_of(float u, u64 mass) {
-  return static_cast<u64>(static_cast<double>(u) * static_cast<double>(mass));
+  bool rest;
+  return fraction(u, mass, rest);
+}
+
+// log(a / b) of a >= b > 0, to an ulp or two of fp32: the quotient as a pair, log1p where it is below 2.
+__device__ __forceinline__ float log_ratio(u64 a, u64 b) {
+  const float ah = __ull2float_rd(a), bh = __ull2float_rd(b);
+  const float al = static_cast<float>(a - static_cast<u64>(ah)), bl = static_cast<float>(b - static_cast<u64>(bh));
+  const float qh = __fdiv_rn(ah, bh);
+  const float ql = __fdiv_rn(fmaf(-qh, bh, ah) + al - qh * bl, bh);
+  if (qh < 2.0f) return log1pf((qh - 1.0f) + ql);
+  return logf(qh) + __fdiv_rn(ql, qh);
 }
 
 template <typename T>
@@ -372,34 +469,51 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
   const Params pr = params_of(a, b);
   const int seg = kSeg * ((a.V - 1) / (kSeg * kMaxSegs) + 1);
   const int nseg = (a.V - 1) / seg + 1;
-  const Part<T> row{reinterpret_cast<const T*>(a.logits) + static_cast<long long>(b) * a.ld, a.V, seg,
-                    static_cast<int>(static_cast<long long>(nseg) * rank / cluster),
-                    static_cast<int>(static_cast<long long>(nseg) * (rank + 1) / cluster)};
+  constexpr int N = Load<T>::N;
+  const int s0 = static_cast<int>(static_cast<long long>(nseg) * rank / cluster);  // this CTA's segments
+  const int s1 = static_cast<int>(static_cast<long long>(nseg) * (rank + 1) / cluster);
+  const int warp = tid >> 5, per = seg / (32 * N), steps = (a.V - 1) / (32 * N) + 1;
+  const Part<T> row{reinterpret_cast<const T*>(a.logits) + static_cast<long long>(b) * a.ld, a.V, per,
+                    min(steps, (s0 + (s1 - s0) * warp / kWarps) * per),
+                    min(steps, (s0 + (s1 - s0) * (warp + 1) / kWarps) * per)};
   for (int i = tid; i < kTable; i += kThreads) sh.table[i] = g_exp2.v[i];
   for (int i = tid; i < kBins; i += kThreads) {
     sh.count[i] = 0;
     sh.mass[i] = 0;
+    sh.sample_count[i] = 0;
+    sh.sample_mass[i] = 0;
   }
   if (tid == 0) {
     sh.top = 0;
     sh.low = 0xFFFFFFFFu;
     sh.cut = 0;
     sh.n = 0;
+    sh.own_n = 0;
     sh.total = 0;
     sh.token = 0x7FFFFFFF;
-    const double c = 1.4426950408889634074 / static_cast<double>(pr.temp);
-    sh.chi = static_cast<float>(c);
-    sh.clo = static_cast<float>(c - static_cast<double>(sh.chi));
+    // log2(e) / temperature as a pair
+    constexpr double kLog2e = 1.4426950408889634074;
+    constexpr float lh = static_cast<float>(kLog2e), ll = static_cast<float>(kLog2e - static_cast<double>(static_cast<float>(kLog2e)));
+    const float ch = __fdiv_rn(lh, pr.temp);
+    sh.chi = ch;
+    sh.clo = __fdiv_rn(fmaf(-ch, pr.temp, lh) + ll, pr.temp);
+    sh.have = 0;
+    if (pr.min_p > 0.0f) sh.drop = static_cast<double>(pr.temp) * log(static_cast<double>(pr.min_p));
   }
   __syncthreads();
   if (cluster > 1) cluster_sync();  // every CTA's counters are set before another adds to them
 
   // ---- pass 1: the largest logit and the smallest
   float m = -INFINITY, lo = INFINITY;
-  row.all([&](float x, int) {
-    m = fmaxf(m, x);
-    lo = fminf(lo, x);
+  row.all([&](const float (&x)[N], int, int n) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      m = fmaxf(m, x[e]);
+      lo = fminf(lo, e < n ? x[e] : INFINITY);
+    }
   });
+  m = clean(m);  // (the maximum leaves out what is not a number)
+  lo = clean(lo);
   const float own = m;  // this thread's largest
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -434,10 +548,11 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
   // k >> 9 carries the magic number's 0x4B400000 >> 9; (w : 0) has its leading bit at 62 and the largest weight
   // at S or S + 1, S = 62 - shift
   s.bias = (0x4B400000 >> 9) + e0 + a.shift;
-  s.zero = s.rel ? -70.0f : top * s.chi - 70.0f;
+  s.zero = (s.rel ? 0.0f : top * s.chi) - (60.0f - a.shift);
   const float extent = fminf(32.0f / (s.chi * 0.69314718f), top - key_value(sh.low));  // -inf logits: the first
   const float binscale = extent > 0.0f ? kBins / extent : 0.0f;
-  auto bin_of = [&](float x) { return min(kBins - 1, static_cast<int>(fminf((top - x) * binscale, 1e6f))); };
+  // (+inf falls into the first step, -inf and what is not a number into the last)
+  auto bin_of = [&](float x) { return min(kBins - 1, static_cast<int>(fmaxf(fminf((top - x) * binscale, 1e6f), 0.0f))); };
 
   const bool has_k = pr.top_k > 0, has_m = pr.min_p > 0.0f, has_p = pr.top_p < 1.0f;
   const bool truncated = has_k || has_m || has_p;
@@ -448,8 +563,9 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
     if (a.V > kShort) {
       if (own != -INFINITY) atomicAdd(&sh.count[bin_of(own)], 1u);
       __syncthreads();
-      const float t = 32.0f * min(kWarps, row.s1 - row.s0);
-      const u64 want = static_cast<u64>(t * (1.0f - ex2(-1.4427f * kAim / (cluster * t)))) + 1;
+      const float t = 32.0f * min(kWarps, s1 - s0);
+      const float aim = has_k ? fminf(kShort * 0.75f, pr.top_k * 1.25f + 32.0f) : static_cast<float>(kAim);
+      const u64 want = static_cast<u64>(t * (1.0f - ex2(-1.4427f * aim / (cluster * t)))) + 1;
       u64 all;
       const u64 c0 = sh.count[2 * tid], c1 = sh.count[2 * tid + 1];
       const u64 before = block_scan(c0 + c1, all, sh);
@@ -465,44 +581,73 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
     else __syncthreads();
   }
 
+  // hands the CTA's own list to the first one, unless the lists together exceed the room (their count says so)
+  auto send = [&](uint32_t room) {
+    __syncthreads();
+    if (tid == 0) {
+      asm volatile("atom.relaxed.cluster.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(sh.own_at) : "r"(remote(&sh.n, 0)), "r"(sh.own_n) : "memory");
+    }
+    __syncthreads();
+    const uint32_t n = sh.own_n, at = sh.own_at, r_list = remote(sh.list, 0);
+    if (at + n <= room)
+      for (uint32_t i = tid; i < n; i += kThreads) remote_put64(r_list + 8 * (at + i), sh.own[i]);
+    __syncthreads();
+    if (tid == 0) sh.own_n = 0;
+  };
+
   // ---- pass 2: the sum, the candidates, and (nothing cut off) the segments' sums
   const float cut = sh.cut == 0 ? -INFINITY : key_value(sh.cut);
   {
-    const uint32_t r_n = remote(&sh.n, 0), r_list = remote(sh.list, 0), r_segs = remote(sh.segs, 0);
+    const uint32_t r_segs = remote(sh.segs, 0);
     u64 z = 0;
     if (exact_total && !has_p) {
-      for (int sg = row.s0 + (tid >> 5); sg < row.s1; sg += kWarps) {
-        u64 v = 0;
-        row.segment(sg, [&](float x, int) { v += weight(x, s, sh.table); });
-        v = warp_sum(v);
-        if ((tid & 31) == 0) {
-          remote_put64(r_segs + 8 * sg, v);
-          z += v;
-        }
-      }
+      u64 v = 0;
+      row.run(
+          [&](const float (&x)[N], int, int) {
+#pragma unroll
+            for (int e = 0; e < N; ++e) v += weight(x[e], s, sh.table);
+          },
+          [&](int sg) {
+            v = warp_sum(v);
+            if ((tid & 31) == 0) {
+              remote_put64(r_segs + 8 * sg, v);
+              z += v;
+            }
+            v = 0;
+          });
     } else {
-      auto candidate = [&](float x, int i) {
-        if (x >= cut) {
-          const uint32_t at = remote_take(r_n);
-          if (at < kShort) remote_put64(r_list + 8 * at, place(x, i));
-        }
+      auto candidates = [&](const float (&x)[N], int i, int n) {
+        float most = x[0];
+#pragma unroll
+        for (int e = 1; e < N; ++e) most = fmaxf(most, x[e]);
+        if (!(most >= cut)) return;
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+          if (x[e] >= cut && e < n) {
+            const uint32_t at = atomicAdd(&sh.own_n, 1u);
+            if (at < kShort) sh.own[at] = place(x[e], i + e);
+          }
       };
       if (exact_total) {
-        row.all([&](float x, int i) {
-          z += weight(x, s, sh.table);
-          candidate(x, i);
+        row.all([&](const float (&x)[N], int i, int n) {
+#pragma unroll
+          for (int e = 0; e < N; ++e) z += weight(x[e], s, sh.table);
+          candidates(x, i, n);
         });
       } else {
         float zf = 0.0f;
-        row.all([&](float x, int i) {
-          zf += ex2((x - top) * s.chi);
-          candidate(x, i);
+        row.all([&](const float (&x)[N], int i, int n) {
+          // (what is not a number: 0; +inf, the top: 1)
+#pragma unroll
+          for (int e = 0; e < N; ++e) zf += __saturatef(ex2((x[e] - top) * s.chi));
+          candidates(x, i, n);
         });
         z = __float2ull_rn(zf * 4294967296.0f);
       }
     }
     z = block_sum(z, sh);
     if (tid == 0) remote_add64(remote(&sh.total, 0), z);
+    if (truncated) send(kShort);
   }
   if (cluster > 1) cluster_sync();
   else __syncthreads();
@@ -513,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
   u64 edge = kAll;   // places that min_p allows
   if (has_m) {
     // w >= min_p  <=>  x >= top + temperature ln(min_p)
-    const double e = static_cast<double>(top) + static_cast<double>(pr.temp) * log(static_cast<double>(pr.min_p));
+    const double e = static_cast<double>(top) + sh.drop;
     float f = static_cast<float>(e);
     if (static_cast<double>(f) < e) f = nextafterf(f, INFINITY);
     edge = (static_cast<u64>(~order_key(clean(f))) << 32) | 0xFFFFFFFFull;
@@ -525,21 +670,32 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
       remote_put64(remote(&sh.limit, r), limit);
     }
   };
+  auto tell_window = [&](float hi, float lo, float ref, float scale) {  // likewise
+    for (int r = 0; r < cluster; ++r) {
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote(&sh.hi, r)), "f"(hi) : "memory");
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote(&sh.lo, r)), "f"(lo) : "memory");
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote(&sh.ref, r)), "f"(ref) : "memory");
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote(&sh.scale, r)), "f"(scale) : "memory");
+    }
+  };
   auto heard = [&] {  // every CTA: the first one's order
     if (cluster > 1) cluster_sync();
     else __syncthreads();
     return sh.order;
   };
-  auto finish = [&](int token) {  // one thread
-    a.token[b] = token;
-    const double x = Load<T>::one(row.x + token);
-    const double ln2 = 0.69314718055994530942;
-    const double zt = (s.rel ? x - static_cast<double>(top) : x) / static_cast<double>(pr.temp);
-    const double unit = ln2 * (e0 - (62 - a.shift));
-    double z = static_cast<double>(sh.total);
-    if (!exact_total) z = z * 0x1p-32 * static_cast<double>(weight(top, s, sh.table));
-    if (a.logp) a.logp[b] = static_cast<float>(zt - (log(z) + unit));
-    if (a.logp_kept) a.logp_kept[b] = pr.greedy ? 0.0f : static_cast<float>(zt - (log(static_cast<double>(mass)) + unit));
+  auto finish = [&](int token) {  // two threads, one for each logarithm
+    // log w_token - log w_top = (x - top) / temperature, from an exact difference
+    const float x = clean(Load<T>::one(row.x + token));
+    const u64 w_top = weight(top, s, sh.table);
+    const double d = (static_cast<double>(x) - static_cast<double>(top)) * (static_cast<double>(s.chi) + s.clo) * 0.69314718055994530942;
+    if (tid == 0) {
+      a.token[b] = token;
+      u64 z = sh.total, unit = w_top;
+      if (!exact_total) unit = 1ull << 32;
+      if (a.logp) a.logp[b] = static_cast<float>(d - log_ratio(z, unit));
+    } else if (a.logp_kept) {
+      a.logp_kept[b] = pr.greedy ? 0.0f : static_cast<float>(d - log_ratio(mass, w_top));
+    }
   };
 
   if (first) {
@@ -547,7 +703,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
     int next = truncated ? kHistogram : kDone;
     if (truncated && n <= kShort) {
       // thread t holds candidates t and t + kThreads
-      u64 p[2], w[2], cnt[2] = {0, 0}, before[2] = {0, 0};
+      u64 p[2], w[2], before[2] = {0, 0};
+      uint32_t cnt[2] = {0, 0};
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int i = tid + e * kThreads;
@@ -556,14 +713,22 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
         if (i < n) sh.w[i] = w[e];
       }
       __syncthreads();
-      for (int j = 0; j < n; ++j) {
-        const u64 pj = sh.list[j], wj = sh.w[j];
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
+      auto rank = [&](int e) {
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) {
+          const u64 pj = sh.list[j], wj = sh.w[j];
           if (pj < p[e]) {
             ++cnt[e];
             before[e] += wj;
           }
+        }
+      };
+      rank(0);
+      if (n > kThreads) rank(1);
+      const u64 ranked = block_sum(w[0] + w[1], sh);
+      if (tid == 0) {
+        sh.have = ranked;
+        sh.short_n = static_cast<uint32_t>(n);
       }
       // the set that top-k and min-p leave, if it lies above the cut
       const u64 lowest = cut == -INFINITY ? kAll : (static_cast<u64>(~order_key(cut)) << 32) | 0xFFFFFFFFull;
@@ -571,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
       bool in[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e)
-        in[e] = tid + e * kThreads < n && (!has_k || cnt[e] < static_cast<u64>(pr.top_k)) && p[e] <= edge;
+        in[e] = tid + e * kThreads < n && (!has_k || cnt[e] < static_cast<uint32_t>(pr.top_k)) && p[e] <= edge;
       u64 base = 0;
       if (exact_total) {
         base = sh.total;
@@ -581,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
       }
       if (inside) {
         const u64 target = has_p ? nucleus(pr.top_p, base) : kAll;
-        const u64 have = exact_total ? block_sum(w[0] + w[1], sh) : base;  // weight of what is ranked
+        const u64 have = exact_total ? ranked : base;
         if (!has_p || have >= target || n == a.V) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) in[e] = in[e] && before[e] < target;
@@ -593,144 +758,347 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
             if (tid + e * kThreads < n && !in[e]) sh.w[tid + e * kThreads] = 0;
           __syncthreads();
           u64 upto[2] = {0, 0};
-          const uint32_t i0 = static_cast<uint32_t>(p[0]), i1 = static_cast<uint32_t>(p[1]);
-          for (int j = 0; j < n; ++j) {
-            const uint32_t ij = static_cast<uint32_t>(sh.list[j]);
-            const u64 wj = sh.w[j];
-            if (ij <= i0) upto[0] += wj;
-            if (ij <= i1) upto[1] += wj;
-          }
+          auto run = [&](int e) {
+            const uint32_t ie = static_cast<uint32_t>(p[e]);
+#pragma unroll 4
+            for (int j = 0; j < n; ++j)
+              if (static_cast<uint32_t>(sh.list[j]) <= ie) upto[e] += sh.w[j];
+          };
+          run(0);
+          if (n > kThreads) run(1);
 #pragma unroll
           for (int e = 0; e < 2; ++e)
             if (in[e] && w[e] != 0 && upto[e] > goal) atomicMin(&sh.token, static_cast<int>(static_cast<uint32_t>(p[e])));
           __syncthreads();
-          if (tid == 0) finish(sh.token);
+          if (tid == 0 || tid == 32) finish(sh.token);
           next = kDone;
         }
       }
     } else if (!truncated) {
       mass = sh.total;
     }
-    if (tid == 0) tell(next, 0);
+    if (tid == 0) tell(next, n <= kShort ? 1 : 0);
   }
   int order = heard();
 
   if (order == kHistogram) {
-    // ---- the kept set is larger: count and weight of the row by equal steps of x
-    row.all([&](float x, int) {
-      const u64 w = weight(x, s, sh.table);
-      const int k = bin_of(x);
-      atomicAdd(&sh.count[k], 1u);
-      if (w) atomicAdd(&sh.mass[k], w);
-    });
-    __syncthreads();
-    if (!first) {
-      for (int k = tid; k < kBins; k += kThreads)
-        if (sh.count[k]) {
-          remote_add32(remote(&sh.count[k], 0), sh.count[k]);
-          remote_add64(remote(&sh.mass[k], 0), sh.mass[k]);
-        }
-    }
-    if (cluster > 1) cluster_sync();
-    else __syncthreads();
-    // the limits in turn: top-k, the weight that min-p leaves, top-p; each looks into one step
-    u64 base = 0;
-    for (int stage = 0; stage < 3; ++stage) {
-      // (uniform over the cluster: stages depend on the row's parameters alone)
-      const bool on = stage == 0 ? has_k : stage == 1 ? !exact_total : has_p;
-      if (!on) continue;
-      u64 before = 0;  // count (stage 0) or weight of the steps before the one looked into
-      u64 target = 0;
-      int step = 0;
-      if (first) {
-        if (stage == 2 && exact_total) base = sh.total;
-        if (stage == 0) target = static_cast<u64>(pr.top_k);
-        if (stage == 2) target = nucleus(pr.top_p, base);
-        if (stage == 1) {
-          // the step of the limit so far (min-p's edge, or the top-k element found)
-          if (edge < limit) limit = edge;
-          step = bin_of(place_logit(limit));
-        }
-        const u64 v0 = stage == 0 ? sh.count[2 * tid] : sh.mass[2 * tid];
-        const u64 v1 = stage == 0 ? sh.count[2 * tid + 1] : sh.mass[2 * tid + 1];
-        u64 all;
-        const u64 c = block_scan(v0 + v1, all, sh);
-        __syncthreads();
-        if (tid == 0) sh.found = -1;
-        __syncthreads();
-        if (stage == 1) {
-          if (step >> 1 == tid) {
-            sh.found = step;
-            sh.found_before = (step & 1) ? c + v0 : c;
-          }
-        } else if (c < target && target <= c + v0 + v1) {
-          sh.found = target <= c + v0 ? 2 * tid : 2 * tid + 1;
-          sh.found_before = target <= c + v0 ? c : c + v0;
-        }
-        __syncthreads();
-        step = sh.found;
-        before = sh.found_before;
-        if (tid == 0) {
-          sh.n = 0;
-          tell(kCollect, step);
-        }
-      }
-      heard();
-      const int want = sh.bin;
-      if (want >= 0) {
-        const uint32_t r_n = remote(&sh.n, 0), r_list = remote(sh.list, 0);
-        row.all([&](float x, int i) {
-          if (bin_of(x) != want) return;
-          const uint32_t at = remote_take(r_n);
-          if (at < kList) remote_put64(r_list + 8 * at, place(x, i));
-        });
+    // ---- the kept set is larger.  A sample (of what lies below the cut, when the candidates' weight is known)
+    const float below = sh.bin ? cut : INFINITY;
+    auto gather = [&](u64* mass_to, uint32_t* count_to) {  // the CTAs' steps into the first one's
+      __syncthreads();
+      for (int k = tid; k < kBins; k += kThreads) {
+        if (sh.mass[k] && (!first || mass_to != sh.mass)) remote_add64(remote(mass_to + k, 0), sh.mass[k]);
+        if (sh.count[k] && (!first || count_to != sh.count)) remote_add32(remote(count_to + k, 0), sh.count[k]);
       }
       if (cluster > 1) cluster_sync();
       else __syncthreads();
-      if (first && want >= 0) {
-        const int n = static_cast<int>(sh.n);
-        auto listed = [&](auto&& f) {
-          for (int i = tid; i < n; i += kThreads) f(sh.list[i]);
-        };
-        auto whole = [&](auto&& f) {  // more logits in the step than the list holds (many equal ones): the row again
-          for (int i = tid; i < a.V; i += kThreads) {
-            const float x = Load<T>::one(row.x + i);
-            if (bin_of(x) == want) f(place(x, i));
-          }
-        };
+    };
+    auto clear = [&] {
+      for (int k = tid; k < kBins; k += kThreads) {
+        sh.mass[k] = 0;
+        sh.count[k] = 0;
+      }
+      __syncthreads();
+    };
+    row.sample(steps >= 256 * cluster ? 8 : 1, [&](const float (&x)[N], int, int n) {
+      u64 w[N];
+#pragma unroll
+      for (int e = 0; e < N; ++e) w[e] = weight(x[e], s, sh.table);
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        if (!(x[e] < below) || e >= n) continue;
+        const int k = bin_of(x[e]);
+        atomicAdd(&sh.count[k], 1u);
+        if (w[e]) atomicAdd(&sh.mass[k], w[e]);
+      }
+    });
+    gather(sh.sample_mass, sh.sample_count);
+
+    // the limits in turn: top-k, the weight that min-p leaves, top-p
+    u64 base = 0;
+    int collected = -1;  // the step whose logits the list holds
+    for (int stage = 0; stage < 3; ++stage) {
+      // the same in every CTA (stage 1 after a top-k: only if the first CTA says that min-p cuts deeper)
+      const bool on = stage == 0 ? has_k : stage == 1 ? has_m : has_p;
+      if (!on) continue;
+      u64 target = 0;
+      bool skip = false;
+      if (first) {
+        clear();
+        float hi = INFINITY, lo = -INFINITY, ref = top, scale = binscale;  // the whole row
         if (stage == 1) {
-          u64 v = 0;
-          auto add = [&](u64 p) {
-            if (p <= limit) v += weight(place_logit(p), s, sh.table);
-          };
-          if (n <= kList) listed(add);
-          else whole(add);
-          base = before + block_sum(v, sh);
+          if (edge >= limit) skip = true;  // (base is known from the top-k stage)
+          else limit = edge;
+          hi = lo = ref = place_logit(limit);
+          scale = 0.0f;
         } else {
-          u64 l;
-          if (stage == 0)
-            l = n <= kList ? radix_select<false>(listed, s, target - before, sh) : radix_select<false>(whole, s, target - before, sh);
-          else
-            l = n <= kList ? radix_select<true>(listed, s, target - before, sh) : radix_select<true>(whole, s, target - before, sh);
-          if (l < limit) limit = l;
+          if (stage == 2 && exact_total) base = sh.total;
+          target = stage == 0 ? static_cast<u64>(pr.top_k) : nucleus(pr.top_p, base);
+          // how far down the sample the target lies, give or take 4 sigma of what was counted to there
+          const bool ranked = sh.have != 0;
+          const u64 v0 = stage == 0 ? sh.sample_count[2 * tid] : sh.sample_mass[2 * tid];
+          const u64 v1 = stage == 0 ? sh.sample_count[2 * tid + 1] : sh.sample_mass[2 * tid + 1];
+          u64 all;
+          const u64 c = block_scan(v0 + v1, all, sh);
+          if (tid == 0) {
+            const double total = stage == 0    ? static_cast<double>(a.V)
+                                 : exact_total ? static_cast<double>(sh.total)
+                                               : static_cast<double>(sh.total) * 0x1p-32 *
+                                                     static_cast<double>(weight(top, s, sh.table));
+            const double known = !ranked ? 0.0 : static_cast<double>(stage == 0 ? sh.short_n : sh.have);
+            sh.share = static_cast<float>((static_cast<double>(target) - known) / fmax(total - known, 1.0));
+            sh.pick_lo = kBins;
+            sh.pick_hi = -1;
+          }
+          __syncthreads();
+          const float share = sh.share;
+          // the estimate's deviation: sqrt(f (1 - f) / n) for n equal weights; for unequal ones n is (sum w)^2 / sum w^2,
+          // taken by steps (a step's weights are nearly equal)
+          float sq = 0.0f;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float n = static_cast<float>(sh.sample_count[2 * tid + e]);
+            const float w = static_cast<float>(e ? v1 : v0);
+            if (n > 0.0f) sq += w / n * w;
+          }
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) sq += __shfl_xor_sync(0xFFFFFFFFu, sq, o);
+          if ((tid & 31) == 0) sh.sq[warp] = sq;
+          __syncthreads();
+          sq = 0.0f;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) sq += sh.sq[w];
+          const float whole = static_cast<float>(all);
+          const float spread = 4.0f * sqrtf(fmaxf(share * (1.0f - share), 0.0f) * sq) + 0.002f * whole;  // (sq = whole^2 / n)
+          const float a0 = fmaxf(share * whole - spread, 0.0f), a1 = share * whole + spread;
+          if (share > 0.0f && all > 0) {
+            // the last pair of steps before a0 is reached, the first after a1
+            if (static_cast<float>(c) <= a0 && a0 <= static_cast<float>(c + v0 + v1)) atomicMax(&sh.pick_hi, 2 * tid);
+            if (static_cast<float>(c) < a1 && a1 <= static_cast<float>(c + v0 + v1)) atomicMin(&sh.pick_lo, 2 * tid + 2);
+          }
+          __syncthreads();
+          if (share <= 0.0f && ranked) {  // among the candidates
+            lo = cut;
+            scale = top > cut ? kBins / (top - cut) : 0.0f;
+          } else if (sh.pick_hi >= 0 && binscale > 0.0f) {
+            if (sh.pick_hi > 0) hi = top - static_cast<float>(sh.pick_hi) / binscale;
+            else if (ranked) hi = cut;  // (the sample starts below the cut)
+            if (sh.pick_lo < kBins) lo = top - static_cast<float>(sh.pick_lo) / binscale;
+            ref = fminf(hi, top);
+            const float range = ref - fmaxf(lo, top - extent);
+            scale = range > 0.0f ? kBins / range : 0.0f;
+          }
+        }
+        if (tid == 0) {
+          sh.above_mass = 0;
+          sh.above_count = 0;
+          if (!skip) tell_window(hi, lo, ref, scale);
+          tell(skip ? kDone : kHistogram, 0);
         }
       }
+      if (heard() == kDone) continue;  // nothing to look for in this stage
+      for (int attempt = 0; attempt < 2; ++attempt) {
+        const float hi = sh.hi, lo = sh.lo, ref = sh.ref, scale = sh.scale;
+        auto step_of = [&](float x) { return min(kBins - 1, static_cast<int>(fminf(fmaxf((ref - x) * scale, 0.0f), 1e6f))); };
+        if (!first) clear();
+        u64 n_above = 0, w_above = 0;
+        u64 v = 0;
+        row.run(
+            [&](const float (&x)[N], int, int n) {
+              float most = x[0];
+#pragma unroll
+              for (int e = 1; e < N; ++e) most = fmaxf(most, x[e]);
+              if (!(most >= lo)) return;
+              u64 w[N];
+#pragma unroll
+              for (int e = 0; e < N; ++e) w[e] = weight(x[e], s, sh.table);
+#pragma unroll
+              for (int e = 0; e < N; ++e) {
+                v += x[e] > hi ? w[e] : 0;
+                n_above += x[e] > hi ? 1 : 0;
+              }
+#pragma unroll
+              for (int e = 0; e < N; ++e)
+                if (x[e] >= lo && x[e] <= hi && e < n) {
+                  const int k = step_of(x[e]);
+                  if (stage == 0) atomicAdd(&sh.count[k], 1u);
+                  if (w[e]) atomicAdd(&sh.mass[k], w[e]);
+                }
+            },
+            [&](int sg) {
+              v = warp_sum(v);
+              if ((tid & 31) == 0) {
+                sh.segs[sg] = v;
+                w_above += v;
+              }
+              v = 0;
+            });
+        w_above = block_sum(w_above, sh);
+        n_above = block_sum(n_above, sh);
+        if (tid == 0) {
+          remote_add64(remote(&sh.above_mass, 0), w_above);
+          remote_add64(remote(&sh.above_count, 0), n_above);
+        }
+        gather(sh.mass, sh.count);
+        u64 before = 0;
+        if (first) {
+          const u64 over = stage == 0 ? sh.above_count : sh.above_mass;
+          const u64 v0 = stage == 0 ? sh.count[2 * tid] : sh.mass[2 * tid];
+          const u64 v1 = stage == 0 ? sh.count[2 * tid + 1] : sh.mass[2 * tid + 1];
+          u64 all;
+          const u64 c = over + block_scan(v0 + v1, all, sh);
+          __syncthreads();
+          if (tid == 0) sh.found = stage == 1 ? 0 : -1;
+          if (tid == 0) sh.found_before = over;
+          __syncthreads();
+          if (stage != 1 && c < target && target <= c + v0 + v1) {
+            sh.found = target <= c + v0 ? 2 * tid : 2 * tid + 1;
+            sh.found_before = target <= c + v0 ? c : c + v0;
+          }
+          __syncthreads();
+          before = sh.found_before;
+          const int step = sh.found;
+          // not in the window: once more with the whole row (where nothing lies above it)
+          const bool again = step < 0 && (hi < INFINITY || lo > -INFINITY);
+          if (stage == 0) {  // the weight of the steps before
+            u64 m0 = 0;
+            for (int k = tid; k < (step < 0 ? kBins : step); k += kThreads) m0 += sh.mass[k];
+            base = sh.above_mass + block_sum(m0, sh);
+          }
+          if (again) clear();
+          if (tid == 0) {
+            sh.n = 0;
+            if (again) {
+              sh.above_mass = 0;
+              sh.above_count = 0;
+              tell_window(INFINITY, -INFINITY, top, binscale);
+            }
+            tell(again ? kHistogram : kCollect, step);
+          }
+        }
+        if (heard() == kHistogram) continue;
+        const int want = collected = sh.bin;
+        if (want >= 0) {
+          // the step's logits, and the segments' weight between the window's upper end and the step
+          u64 v = 0;
+          row.run(
+              [&](const float (&x)[N], int i, int n) {
+                float most = x[0];
+#pragma unroll
+                for (int e = 1; e < N; ++e) most = fmaxf(most, x[e]);
+                if (!(most >= lo)) return;
+                bool before_step = false;
+                int k[N];  // kBins: not in the window
+#pragma unroll
+                for (int e = 0; e < N; ++e) {
+                  k[e] = x[e] >= lo && x[e] <= hi && e < n ? step_of(x[e]) : kBins;
+                  before_step = before_step || k[e] < want;
+                }
+                if (before_step) {
+#pragma unroll
+                  for (int e = 0; e < N; ++e) {
+                    const u64 w = weight(x[e], s, sh.table);
+                    v += k[e] < want ? w : 0;
+                  }
+                }
+#pragma unroll
+                for (int e = 0; e < N; ++e)
+                  if (k[e] == want) {
+                    const uint32_t at = atomicAdd(&sh.own_n, 1u);
+                    if (at < kList) sh.own[at] = place(x[e], i + e);
+                  }
+              },
+              [&](int sg) {
+                v = warp_sum(v);
+                if ((tid & 31) == 0) sh.part_segs[sg] = v;
+                v = 0;
+              });
+          send(kList);
+        }
+        if (cluster > 1) cluster_sync();
+        else __syncthreads();
+        if (first && want >= 0) {
+          const int n = static_cast<int>(sh.n);
+          auto listed = [&](auto&& f) {
+            for (int i = tid; i < n; i += kThreads) f(sh.list[i]);
+          };
+          auto whole = [&](auto&& f) {  // more logits in the step than the list holds (many equal ones): the row again
+            for (int i = tid; i < a.V; i += kThreads) {
+              const float x = Load<T>::one(row.x + i);
+              if (x >= lo && x <= hi && step_of(x) == want) f(place(x, i));
+            }
+          };
+          if (stage != 1) {
+            u64 l = kAll;
+            if (n <= kThreads) {  // ranked against each other
+              const u64 p = tid < n ? sh.list[tid] : kAll;
+              const u64 w = tid >= n ? 0 : stage == 0 ? 1 : weight(place_logit(p), s, sh.table);
+              if (tid < n) sh.w[tid] = w;
+              if (tid == 0) sh.picked = kAll;
+              __syncthreads();
+              u64 c = before;
+#pragma unroll 4
+              for (int j = 0; j < n; ++j)
+                if (sh.list[j] < p) c += sh.w[j];
+              if (c < target && target <= c + w) sh.picked = p;
+              __syncthreads();
+              l = sh.picked;
+            } else if (stage == 0)
+              l = n <= kList ? radix_select<false>(listed, s, target - before, sh) : radix_select<false>(whole, s, target - before, sh);
+            else
+              l = n <= kList ? radix_select<true>(listed, s, target - before, sh) : radix_select<true>(whole, s, target - before, sh);
+            if (l < limit) limit = l;
+          }
+          if (stage != 2) {  // what the limit leaves
+            u64 v = 0;
+            auto add = [&](u64 p) {
+              if (p <= limit) v += weight(place_logit(p), s, sh.table);
+            };
+            if (n <= kList) listed(add);
+            else whole(add);
+            base = (stage == 1 ? sh.above_mass : base) + block_sum(v, sh);
+          }
+        }
+        break;
+      }
     }
-    if (first && tid == 0) tell(kSums, 0);
+    // ---- the kept weight of every segment: above the last window, between it and the step, and of the step
+    const int n_last = first ? static_cast<int>(sh.n) : 0;
+    if (first && tid == 0) tell(kSums, collected >= 0 && n_last <= kList ? 1 : 0);
     order = heard();
-    // ---- the kept weight of every segment
+    const bool quick = sh.bin == 1;
     limit = sh.limit;
+    const float hi = sh.hi;
     const uint32_t r_segs = remote(sh.segs, 0);
-    for (int sg = row.s0 + (tid >> 5); sg < row.s1; sg += kWarps) {
+    if (quick) {
+      if (first)
+        for (int sg = s0 + tid; sg < s1; sg += kThreads) sh.segs[sg] += sh.part_segs[sg];
+      else
+        for (int sg = s0 + tid; sg < s1; sg += kThreads) remote_put64(r_segs + 8 * sg, sh.segs[sg] + sh.part_segs[sg]);
+    } else {  // (a step of more logits than the list holds)
+      const float least = limit == kAll ? -INFINITY : place_logit(limit);
       u64 v = 0;
-      row.segment(sg, [&](float x, int i) {
-        if (place(x, i) <= limit) v += weight(x, s, sh.table);
-      });
-      v = warp_sum(v);
-      if ((tid & 31) == 0) remote_put64(r_segs + 8 * sg, v);
+      row.run(
+          [&](const float (&x)[N], int i, int n) {
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+              if (x[e] <= hi && x[e] >= least && e < n && place(x[e], i + e) <= limit) v += weight(x[e], s, sh.table);
+          },
+          [&](int sg) {
+            v = warp_sum(v);
+            if ((tid & 31) == 0) remote_put64(r_segs + 8 * sg, sh.segs[sg] + v);
+            v = 0;
+          });
     }
     if (cluster > 1) cluster_sync();
     else __syncthreads();
+    if (first && quick) {
+      for (int i = tid; i < n_last; i += kThreads) {
+        const u64 p = sh.list[i];
+        if (p <= limit) atomicAdd(&sh.segs[static_cast<int>(static_cast<uint32_t>(p)) / seg], weight(place_logit(p), s, sh.table));
+      }
+      __syncthreads();
+    }
   }
 
   // ---- the token's segment, then the token
@@ -761,7 +1129,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
       run += all;
     }
     __syncthreads();
-    if (tid == 0) finish(sh.token);
+    if (tid == 0 || tid == 32) finish(sh.token);
   }
 }
 
@@ -782,6 +1150,9 @@ cudaError_t launch_sample(const SampleArgs& a_in, bool f32, int num_sms, cudaStr
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!attr_done[dev][f32]) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(sizeof(Shared)));
+    if (e != cudaSuccess) return e;
+    // (the default split of an SM's memory need not leave room for four CTAs)
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess) return e;
     attr_done[dev][f32] = true;
   }
