@@ -216,6 +216,23 @@ struct Part {
   __device__ __forceinline__ void all(F&& f) const {
     run(f, [](int) {});
   }
+  // the first reading, from HBM: six steps in flight
+  template <typename F>
+  __device__ __forceinline__ void first(F&& f) const {
+    constexpr int D = 6;
+    uint4 u[D];
+#pragma unroll
+    for (int d = 0; d < D; ++d) u[d] = load(t0 + d);
+#pragma unroll 1
+    for (int t = t0; t < t1; t += D) {
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        const uint4 c = u[d];
+        u[d] = load(t + d + D);
+        if (t + d < t1) step(t + d, c, f);
+      }
+    }
+  }
   // f for every `stride`-th step
   template <typename F>
   __device__ __forceinline__ void sample(int stride, F&& f) const {
@@ -505,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
 
   // ---- pass 1: the largest logit and the smallest
   float m = -INFINITY, lo = INFINITY;
-  row.all([&](const float (&x)[N], int, int n) {
+  row.first([&](const float (&x)[N], int, int n) {
 #pragma unroll
     for (int e = 0; e < N; ++e) {
       m = fmaxf(m, x[e]);
