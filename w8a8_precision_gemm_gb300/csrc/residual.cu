@@ -77,6 +77,64 @@ __device__ __forceinline__ uint4 update8(const ResidualArgs& a, const uint4 yu, 
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+// Block reductions of the row kernel: each has scratch of its own, so nothing
+// has to be read before the next one may write (one barrier fewer than the
+// shared ones), and the maximum, which a warp reduces in one instruction, is
+// taken by every warp itself (another one fewer).
+struct RmsScratch {
+  float part[2 * (1024 / 32)];
+  float ms, r;
+};
+
+// (s + c) / K rounded to fp32 and 1 / sqrt(ms + eps), as mean_sq gives them, with
+// the quotient as an fp32 pair (2^-47) instead of in fp64 (2^-52): the fp64
+// division is a chain of slow instructions that a whole block waits for.
+__device__ __forceinline__ void mean_sq_pair(float s, float c, int K, float eps, float& ms, float& r) {
+  const float k = static_cast<float>(K);  // exact: these rows have at most 2 x 512 vectors
+  float lo = 0.0f, hi = s;
+  two_sum_acc(hi, lo, c);
+  const float q = __fdiv_rn(hi, k);
+  ms = __fadd_rn(q, __fdiv_rn(__fadd_rn(__fmaf_rn(-q, k, hi), lo), k));
+  r = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(ms, eps)));
+}
+
+template <int NC, bool kOwn>
+__device__ __forceinline__ void row_rms_once(const uint4* row, int K, const uint4 (&cache)[NC], const float4* gain, float eps,
+                                             RmsScratch& sh, float& ms, float& r) {
+  float s, c;
+  row_sum_sq<NC, kOwn>(row, K, cache, gain, s, c);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+  warp_pair_sum(s, c);
+  if (lane == 0) {
+    sh.part[2 * warp] = s;
+    sh.part[2 * warp + 1] = c;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    s = lane < nw ? sh.part[2 * lane] : 0.0f;
+    c = lane < nw ? sh.part[2 * lane + 1] : 0.0f;
+    warp_pair_sum(s, c);
+    if (lane == 0) mean_sq_pair(s, c, K, eps, sh.ms, sh.r);
+  }
+  __syncthreads();
+  ms = sh.ms;
+  r = sh.r;
+}
+
+__device__ __forceinline__ float warp_fmax(float v) {
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+__device__ __forceinline__ float block_max_once(float v, float* part) {
+  v = warp_fmax(v);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+  __syncthreads();
+  const int lane = threadIdx.x & 31;
+  return warp_fmax(lane < (blockDim.x >> 5) ? part[lane] : 0.0f);
+}
+
 // One row per CTA.  NC: vectors a thread holds; KEEP: they are all of the row
 // (no thread has more), and the normalised values stay in registers between the
 // absmax and the codes instead of being computed twice.
@@ -85,6 +143,8 @@ __global__ void __launch_bounds__(MAXT, MINB) residual_rmsnorm_quant_kernel(cons
   griddep_wait();
   griddep_launch_dependents();
   __shared__ RowScratch sh;
+  __shared__ RmsScratch rms[2];
+  __shared__ float top[32];
   const int m = blockIdx.x;
   const uint4* yrow = reinterpret_cast<const uint4*>(a.Y + static_cast<size_t>(m) * a.ldy);
   const uint4* hrow = reinterpret_cast<const uint4*>(a.H + static_cast<size_t>(m) * a.ldh);
@@ -104,7 +164,7 @@ __global__ void __launch_bounds__(MAXT, MINB) residual_rmsnorm_quant_kernel(cons
   float2 r2 = splat2(1.0f);
   if (a.gamma_post) {
     float ms, r;
-    row_rms<NC, false>(yrow, a.K, yc, reinterpret_cast<const float4*>(a.gamma_post), a.eps_post, sh.red, ms, r);
+    row_rms_once<NC, false>(yrow, a.K, yc, reinterpret_cast<const float4*>(a.gamma_post), a.eps_post, rms[0], ms, r);
     r2 = splat2(r);
   }
   const float2 rs2 = splat2(a.rs);
@@ -121,7 +181,7 @@ __global__ void __launch_bounds__(MAXT, MINB) residual_rmsnorm_quant_kernel(cons
   } else {
     const float4* g4 = reinterpret_cast<const float4*>(a.gamma);
     float ms, r;
-    row_rms<NC, true>(orow, a.K, hc, g4, a.eps, sh.red, ms, r);
+    row_rms_once<NC, true>(orow, a.K, hc, g4, a.eps, rms[1], ms, r);
     if (threadIdx.x == 0 && a.ms_out) a.ms_out[m] = ms;
     r2 = splat2(r);
     float2 v[NC][4];
@@ -134,7 +194,7 @@ __global__ void __launch_bounds__(MAXT, MINB) residual_rmsnorm_quant_kernel(cons
 #pragma unroll
       for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fmaxf(fabsf(v[c][e].x), fabsf(v[c][e].y)));
     }
-    amax = block_reduce<true>(amax, sh.red);
+    amax = block_max_once(amax, top);
     const Enc en = make_enc(amax, a.qt);
     if (threadIdx.x == 0) a.sx[m] = en.scale;
     uint8_t* out = a.Xq + static_cast<size_t>(m) * a.K;

@@ -84,8 +84,7 @@ __device__ __forceinline__ void two_sum_acc2(float2& s, float2& c, float2 y) {
 // x^2, divided in fp64 and rounded to fp32) and r = 1 / sqrt(ms + eps)
 // (correctly rounded fp32 square root and division), computed by one thread
 // and handed to every thread of the block.
-__device__ __forceinline__ void block_mean_sq(float s, float c, float* red, int K, float eps, float& ms, float& r) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+__device__ __forceinline__ void warp_pair_sum(float& s, float& c) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const float os = __shfl_xor_sync(0xFFFFFFFFu, s, o);
@@ -93,6 +92,16 @@ __device__ __forceinline__ void block_mean_sq(float s, float c, float* red, int 
     two_sum_acc(s, c, os);
     c = __fadd_rn(c, oc);
   }
+}
+
+__device__ __forceinline__ void mean_sq(float s, float c, int K, float eps, float& ms, float& r) {
+  ms = static_cast<float>((static_cast<double>(s) + static_cast<double>(c)) / static_cast<double>(K));
+  r = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(ms, eps)));
+}
+
+__device__ __forceinline__ void block_mean_sq(float s, float c, float* red, int K, float eps, float& ms, float& r) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+  warp_pair_sum(s, c);
   if (lane == 0) {
     red[2 * warp] = s;
     red[2 * warp + 1] = c;
@@ -101,18 +110,8 @@ __device__ __forceinline__ void block_mean_sq(float s, float c, float* red, int 
   if (warp == 0) {
     float ts = lane < nw ? red[2 * lane] : 0.0f;
     float tc = lane < nw ? red[2 * lane + 1] : 0.0f;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const float os = __shfl_xor_sync(0xFFFFFFFFu, ts, o);
-      const float oc = __shfl_xor_sync(0xFFFFFFFFu, tc, o);
-      two_sum_acc(ts, tc, os);
-      tc = __fadd_rn(tc, oc);
-    }
-    if (lane == 0) {
-      const float m = static_cast<float>((static_cast<double>(ts) + static_cast<double>(tc)) / static_cast<double>(K));
-      red[64] = m;
-      red[65] = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(m, eps)));
-    }
+    warp_pair_sum(ts, tc);
+    if (lane == 0) mean_sq(ts, tc, K, eps, red[64], red[65]);
   }
   __syncthreads();
   ms = red[64];
@@ -458,10 +457,10 @@ __device__ __forceinline__ void quant_act_row(int m, const __nv_bfloat16* __rest
 // K in fp64, so ms is the fp32 rounding of the mean to within ~2^-44 relative
 // -- the same fp32 value a plain fp64 sum gives, except when the mean lies that
 // close to a rounding midpoint.  The gain of the vectors this thread normalises
-// is read while the sums are reduced.
+// is read while the sums are reduced.  row_sum_sq: this thread's part, a pair.
 template <int NC, bool kOwn>
-__device__ __forceinline__ void row_rms(const uint4* row, int K, const uint4 (&cache)[NC], const float4* gain,
-                                        float eps, float* red, float& ms, float& r) {
+__device__ __forceinline__ void row_sum_sq(const uint4* row, int K, const uint4 (&cache)[NC], const float4* gain,
+                                           float& ss, float& sc) {
   const int nvec = K >> 3;
   float2 ss2 = make_float2(0.0f, 0.0f), sc2 = make_float2(0.0f, 0.0f);  // even / odd k
   for_vectors<NC, kOwn>(row, nvec, cache, [&](const uint4 u, int) {
@@ -470,7 +469,8 @@ __device__ __forceinline__ void row_rms(const uint4* row, int K, const uint4 (&c
 #pragma unroll
     for (int e = 0; e < 4; ++e) two_sum_acc2(ss2, sc2, mul2(x[e], x[e]));
   });
-  float ss = ss2.x, sc = sc2.x;
+  ss = ss2.x;
+  sc = sc2.x;
   two_sum_acc(ss, sc, ss2.y);
   sc = __fadd_rn(sc, sc2.y);
 #pragma unroll
@@ -478,7 +478,14 @@ __device__ __forceinline__ void row_rms(const uint4* row, int K, const uint4 (&c
     const int idx = threadIdx.x + c * blockDim.x;
     if (idx < nvec) asm volatile("prefetch.global.L1 [%0];" ::"l"(gain + 2 * idx));
   }
-  block_mean_sq(ss, sc, red, K, eps, ms, r);
+}
+
+template <int NC, bool kOwn>
+__device__ __forceinline__ void row_rms(const uint4* row, int K, const uint4 (&cache)[NC], const float4* gain,
+                                        float eps, float* red, float& ms, float& r) {
+  float s, c;
+  row_sum_sq<NC, kOwn>(row, K, cache, gain, s, c);
+  block_mean_sq(s, c, red, K, eps, ms, r);
 }
 
 // (x * r) * gain of 8 values, each product rounded to fp32.
