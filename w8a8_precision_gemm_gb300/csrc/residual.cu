@@ -30,10 +30,6 @@ using namespace rq;
 
 constexpr int kNC = 8;        // 16-byte vectors cached per thread
 constexpr int kThreads = 512;  // most threads of a row CTA
-#ifndef KMANY
-#define KMANY 4
-#endif
-constexpr int kMany = KMANY;
 
 struct ResidualArgs {
   const __nv_bfloat16* Y;
@@ -90,7 +86,7 @@ struct RmsScratch {
 // the quotient as an fp32 pair (2^-47) instead of in fp64 (2^-52): the fp64
 // division is a chain of slow instructions that a whole block waits for.
 __device__ __forceinline__ void mean_sq_pair(float s, float c, int K, float eps, float& ms, float& r) {
-  const float k = static_cast<float>(K);  // exact: these rows have at most 2 x 512 vectors
+  const float k = static_cast<float>(K);  // exact: these rows have at most 1024 vectors
   float lo = 0.0f, hi = s;
   two_sum_acc(hi, lo, c);
   const float q = __fdiv_rn(hi, k);
@@ -231,14 +227,19 @@ cudaError_t launch_residual_rmsnorm_quant(const void* Y, long long ldy, const fl
   a.Xq = reinterpret_cast<uint8_t*>(Xq);
   a.sx = sx;
   a.ms_out = ms_out;
-  // As few vectors a thread as the row allows: its serial chain is short and
-  // many rows are resident.
   const int nvec = K / 8;
-  const int one = (nvec + 31) / 32 * 32, two = (nvec + 63) / 64 * 32;
-  // few rows: a vector a thread
-  if (M < 304 && nvec <= 1024) return launch_pdl(residual_rmsnorm_quant_kernel<1, true, 1024, 1>, dim3(M), dim3(one), 0, st, a);
-  if (two <= 320) return launch_pdl(residual_rmsnorm_quant_kernel<2, true, 320, kMany>, dim3(M), dim3(two), 0, st, a);
-  if (two <= 512) return launch_pdl(residual_rmsnorm_quant_kernel<2, true, 512, 3>, dim3(M), dim3(two), 0, st, a);
+  auto threads = [&](int nc) { return dim3(static_cast<unsigned>(((nvec + nc - 1) / nc + 31) / 32 * 32)); };
+  // Few rows (less than two an SM): a vector a thread, the shortest chain.  Else
+  // four vectors a thread: fewer warps wait at each reduction.  8192 x 5120 (FP8,
+  // both norms), us at resident CTAs: 1 vector 116 (2), 108 (3); 2 vectors 90 (3),
+  // 80 (4); 3 vectors 73 (5); 4 vectors 73 (5), 71 (6), 70 (7), 75 (8); 5 vectors
+  // 72 (6), 70 (8).  Persistent CTAs that load the next row into the registers the
+  // current one leaves free measured 85 or more: the registers cost more
+  // resident rows than the early loads gain.
+  if (M < 304 && nvec <= 1024)
+    return launch_pdl(residual_rmsnorm_quant_kernel<1, true, 1024, 1>, dim3(M), threads(1), 0, st, a);
+  if (nvec <= 4 * 160) return launch_pdl(residual_rmsnorm_quant_kernel<4, true, 160, 7>, dim3(M), threads(4), 0, st, a);
+  if (nvec <= 4 * 256) return launch_pdl(residual_rmsnorm_quant_kernel<4, true, 256, 4>, dim3(M), threads(4), 0, st, a);
   return launch_pdl(residual_rmsnorm_quant_kernel<kNC, false, kThreads, 1>, dim3(M), dim3(kThreads), 0, st, a);
 }
 
