@@ -1027,7 +1027,7 @@ qurl_status qurl_token_logprob(const void* logits, qurl_ftype x_type, int T, int
   QURL_TRY(device_state(&dev));
   QURL_CUDA(qurl::launch_token_logprob(logits, x_type == QURL_FP32, T, V, ld,
                                        reinterpret_cast<const long long*>(targets), 1.0f / temperature, logp, lse,
-                                       dev->status, reinterpret_cast<cudaStream_t>(stream)));
+                                       dev->num_sms, dev->status, reinterpret_cast<cudaStream_t>(stream)));
   return QURL_OK;
 }
 

@@ -224,7 +224,7 @@ struct SampleArgs {
 cudaError_t launch_sample(const SampleArgs& a, bool f32, int num_sms, cudaStream_t st);
 // logprob.cu: log-probabilities of given tokens and the logits' gradient.
 cudaError_t launch_token_logprob(const void* X, bool f32, long long T, int V, long long ld, const long long* targets,
-                                 float inv_t, float* logp, float* lse, int* status, cudaStream_t st);
+                                 float inv_t, float* logp, float* lse, int num_sms, int* status, cudaStream_t st);
 cudaError_t launch_token_logprob_grad(const void* X, bool f32, long long T, int V, long long ld,
                                       const long long* targets, float inv_t, const float* lse, const float* g,
                                       float scale, const double* denom, void* dX, long long ldd, int num_sms,
