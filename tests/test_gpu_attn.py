@@ -130,6 +130,13 @@ def test_long_sequences_and_batches():
     check(make([2048 + 13 * i for i in range(48)], 40, 8, 128, 16, seed=6))
 
 
+def test_sequences_over_many_ranges():
+    """One KV head, sequences that begin and end inside ranges of their neighbours: partial sums joined in groups."""
+    check(make([20000, 9000, 31234, 128, 17, 12345], 8, 1, 64, 32, seed=21))
+    check(make([150001], 2, 1, 32, 128, seed=22))
+    check(make([5000] * 9, 3, 3, 64, 16, seed=23))
+
+
 def test_peaked_and_flat_scores():
     check(make([900], 10, 2, 128, 16, seed=1, peak=6.0))
     a = make([900], 10, 2, 128, 16, seed=2)

@@ -36,7 +36,8 @@
 // that run together share the cache lines that hold several heads' scales.  A
 // sequence that ends up in several ranges leaves unnormalised partial sums in
 // the workspace, and the unit that finishes it last (a counter per range and
-// head) joins them in range order: one launch, the same result every run.
+// head) joins them in range order (a sequence over many ranges in groups): one
+// launch, the same result every run.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -54,6 +55,9 @@ constexpr int kTile = 128;      // tokens per tile
 constexpr int kSoftmax = 128;   // threads 0..127: softmax and sums (TMEM lanes)
 constexpr int kLoaders = 128;   // threads 128..255
 constexpr int kThreads = kSoftmax + kLoaders + 32;  // and the MMA warp
+// Tiles per range at least: a tile more costs a unit about 0.75 us, joining partial sums about 3.
+constexpr int kMinTiles = 4;
+constexpr int kJoin = 12;        // partial sums that one unit joins; of more, groups of that many are joined first
 constexpr float kNone = -1e30f;  // a maximum over no tokens (log2 units)
 
 constexpr int round16(int n) { return (n + 15) / 16 * 16; }
@@ -90,7 +94,7 @@ struct AttnPlan {
   int per_part;   // query heads per part (the last may have fewer)
   int grid;
   float* partial;     // [2 R][heads][G][head_dim], then [2 R][heads][G][2] of (maximum, sum)
-  unsigned* counter;  // [R][heads]
+  unsigned* counter;  // [3][R][heads]: sequences that begin in a range; groups, see below
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -198,6 +202,8 @@ struct Shared {
   uint64_t drain;
   uint32_t tmem;
   int chunk;                             // sequences per thread of the scan
+  int ranges;                            // ranges in use: the first `longer` have base + 1 tiles, the others base
+  long long base, longer;
   long long tiles_before[kSoftmax + 1];  // tiles before each thread's chunk
   uint32_t valid[3][4];                  // tokens of a stage that count
   float qfac[3][16];                     // per head: what turns a raw score into log2 units
@@ -206,6 +212,12 @@ struct Shared {
   int last;
 };
 
+// a / b of small results: 32-bit where both fit (64-bit divisions took a microsecond of the call's start).
+__device__ __forceinline__ int quotient(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<int>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
+  return static_cast<int>(a / b);
+}
+
 // Walks the segments (one sequence's tiles inside one range) of the CTA's
 // units in order; every role walks the same ones.
 struct Walk {
@@ -213,7 +225,6 @@ struct Walk {
   const AttnPlan& p;
   const Shared& sh;
   long long total;  // tiles of all sequences
-  int reff;         // ranges in use
   int unit, heads;
   // current segment
   int head, range, b;
@@ -224,7 +235,6 @@ struct Walk {
 
   __device__ Walk(const AttnArgs& a_, const AttnPlan& p_, const Shared& sh_)
       : a(a_), p(p_), sh(sh_), total(sh_.tiles_before[kSoftmax]), unit(blockIdx.x), heads(a_.kv_heads * p_.parts) {
-    reff = static_cast<int>(total < p.ranges ? total : p.ranges);
     at = range_end = 0;
     b = 0;
     s = {0, 0, 0};
@@ -233,6 +243,8 @@ struct Walk {
     head = range = 0;
     unit -= gridDim.x;
   }
+
+  __device__ long long start_of(int r) const { return r * sh.base + (r < sh.longer ? r : sh.longer); }
 
   __device__ bool next() {
     if (at < range_end) {  // the rest of the range: the next sequence that has tiles
@@ -243,11 +255,11 @@ struct Walk {
       } while (s.tiles == 0);
     } else {
       unit += gridDim.x;
-      if (unit >= reff * heads) return false;
+      if (unit >= sh.ranges * heads) return false;
       range = unit / heads;
       head = unit - range * heads;
-      at = total * range / reff;
-      range_end = total * (range + 1) / reff;
+      at = start_of(range);
+      range_end = start_of(range + 1);
       int lo = 0, hi = kSoftmax;  // the chunk of sequences that holds tile `at`
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -270,7 +282,10 @@ struct Walk {
     return true;
   }
   // the range that holds tile t of the row of all tiles
-  __device__ int range_of(long long t) const { return static_cast<int>(((t + 1) * reff - 1) / total); }
+  __device__ int range_of(long long t) const {
+    const long long over = t - sh.longer * (sh.base + 1);
+    return over < 0 ? quotient(t, sh.base + 1) : static_cast<int>(sh.longer) + quotient(over, sh.base);
+  }
 };
 
 template <int G, int PANELS>
@@ -351,7 +366,17 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<G, PANELS>::CTAS)
       long long add = 0;
       for (int w = 0; w < warp; ++w) add += sh.tiles_before[32 * (w + 1)];
       named_barrier(1, kSoftmax);
-      sh.tiles_before[tid + 1] += add;
+      add += sh.tiles_before[tid + 1];
+      sh.tiles_before[tid + 1] = add;
+      if (tid == kSoftmax - 1) {  // all tiles
+        const long long want = (add + kMinTiles - 1) / kMinTiles;
+        sh.ranges = static_cast<int>(want < p.ranges ? want : p.ranges);
+        if (sh.ranges > 0) {
+          const long long base = (add >> 32) == 0 ? static_cast<uint32_t>(add) / static_cast<uint32_t>(sh.ranges) : add / sh.ranges;
+          sh.base = base;
+          sh.longer = add - base * sh.ranges;
+        }
+      }
     }
     __syncthreads();
   }
@@ -385,6 +410,15 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<G, PANELS>::CTAS)
         if (!ok) break;
         const uint32_t mask = __ballot_sync(0xFFFFFFFFu, at >= 0);
         if (lane == 0) sh.valid[st][w] = mask;
+        // a new segment's queries (warp w takes heads w and w + 4, a lane 8 of a head's dimensions) are read while
+        // the rows are gathered
+        uint4 qu[2] = {};
+        const __nv_bfloat16* qsrc = a.q + static_cast<long long>(k.b) * a.ldq + static_cast<long long>(kvh * group + h0) * hd;
+        if (t == k.t0 && lane * 8 < hd) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (w + 4 * i < nh) qu[i] = __ldg(reinterpret_cast<const uint4*>(qsrc + static_cast<long long>(w + 4 * i) * hd) + lane);
+        }
         {
           const uint32_t n = at >= 0 ? 4 : 0;
           const long long i = at >= 0 ? at : 0;
@@ -411,20 +445,17 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<G, PANELS>::CTAS)
         }
         cp_async_arrive(&sh.full[st]);
         if (t == k.t0) {
-          // the segment's queries: warp w takes heads w, w + 4, ...; a lane 8 of a head's dimensions
           const int qb = seg % C::STAGES;
-          for (int h = w; h < nh; h += 4) {
-            const __nv_bfloat16* src = a.q + static_cast<long long>(k.b) * a.ldq +
-                                       static_cast<long long>(kvh * group + h0 + h) * hd;
-            float x[8] = {};
-            if (lane * 8 < hd) {
-              const uint4 u = __ldg(reinterpret_cast<const uint4*>(src) + lane);
-              const uint32_t uw[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                x[2 * e] = __uint_as_float(uw[e] << 16);
-                x[2 * e + 1] = __uint_as_float(uw[e] & 0xFFFF0000u);
-              }
+          for (int i = 0; i < 2; ++i) {
+            const int h = w + 4 * i;
+            if (h >= nh) break;
+            float x[8];
+            const uint32_t uw[4] = {qu[i].x, qu[i].y, qu[i].z, qu[i].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              x[2 * e] = __uint_as_float(uw[e] << 16);
+              x[2 * e + 1] = __uint_as_float(uw[e] & 0xFFFF0000u);
             }
             float m = 0.0f;
 #pragma unroll
@@ -643,7 +674,80 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<G, PANELS>::CTAS)
       __nv_bfloat16* out = a.out + static_cast<long long>(k.b) * a.ldo + static_cast<long long>(qh) * hd;
       float* lse = a.lse ? a.lse + static_cast<long long>(k.b) * a.q_heads + qh : nullptr;
       const int r0 = k.range_of(k.seq_tile0), r1 = k.range_of(k.seq_tile0 + k.s.tiles - 1);
-      if (r0 == r1) {
+      const int n = r1 - r0 + 1;  // ranges that hold tiles of the sequence
+      bool done = n == 1;
+      if (!done) {
+        const int heads = k.heads;
+        auto row_of = [&](int range) { return (2LL * range + (range == r0 ? 1 : 0)) * heads + k.head; };
+        // this thread's part of (m, l, acc) into a row of the workspace, then one more arrival on a counter;
+        // whether it was the last of `of`, whose rows are then visible
+        auto leave = [&](long long row, unsigned* counter, int of) {
+#pragma unroll
+          for (int h = 0; h < G; ++h) {
+            if (h >= nh) break;
+#pragma unroll
+            for (int q = 0; q < PANELS; ++q)
+              if (q * 128 + tid < hd) __stcg(p.partial + (row * G + h) * hd + q * 128 + tid, acc[q][h]);
+            if (tid == 0) __stcg(reinterpret_cast<float2*>(part_ml + (row * G + h) * 2), make_float2(m[h], l[h]));
+          }
+          __threadfence();
+          named_barrier(1, kSoftmax);
+          if (tid == 0) {
+            sh.last = atomicAdd(counter, 1u) == static_cast<unsigned>(of - 1);
+            if (sh.last) *counter = 0;  // ready for the next call
+            __threadfence();
+          }
+          named_barrier(1, kSoftmax);
+          return sh.last != 0;
+        };
+        // (m, l, acc) = the rows of ranges from, from + step, ... (`of` of them), added in order
+        auto join = [&](int from, int step, int of) {
+#pragma unroll
+          for (int h = 0; h < G; ++h) {
+            m[h] = kNone;
+            l[h] = 0.0f;
+#pragma unroll
+            for (int q = 0; q < PANELS; ++q) acc[q][h] = 0.0f;
+          }
+#pragma unroll 2
+          for (int i = 0; i < of; ++i) {
+            const long long row = row_of(from + i * step) * G;
+            const float2 ml = lane < nh ? __ldcg(reinterpret_cast<const float2*>(part_ml + (row + lane) * 2)) : make_float2(kNone, 0.0f);
+            float o[PANELS][G];
+#pragma unroll
+            for (int h = 0; h < G; ++h)
+#pragma unroll
+              for (int q = 0; q < PANELS; ++q)
+                o[q][h] = h < nh && q * 128 + tid < hd ? __ldcg(p.partial + (row + h) * hd + q * 128 + tid) : 0.0f;
+#pragma unroll
+            for (int h = 0; h < G; ++h) {
+              const float mr = __shfl_sync(0xFFFFFFFFu, ml.x, h), lr = __shfl_sync(0xFFFFFFFFu, ml.y, h);
+              const float mn = fmaxf(m[h], mr), f0 = ex2(m[h] - mn), f1 = ex2(mr - mn);
+              m[h] = mn;
+              l[h] = l[h] * f0 + lr * f1;
+#pragma unroll
+              for (int q = 0; q < PANELS; ++q) acc[q][h] = acc[q][h] * f0 + o[q][h] * f1;
+            }
+          }
+        };
+        unsigned* counter = p.counter + static_cast<long long>(r0) * heads + k.head;
+        const int groups = (n + kJoin - 1) / kJoin;
+        if (groups == 1) {
+          done = leave(row_of(k.range), counter, n);
+          if (done) join(r0, 1, n);
+        } else {
+          const int g0 = r0 + (k.range - r0) / kJoin * kJoin, of = min(kJoin, r1 + 1 - g0);
+          // (two sequences may have a group that begins in a range: the one that the range ends, the one it begins)
+          const long long at = static_cast<long long>(g0 == r0 ? 2 : 1) * p.ranges + g0;
+          if (leave(row_of(k.range), p.counter + at * heads + k.head, of)) {
+            join(g0, 1, of);
+            named_barrier(1, kSoftmax);  // every thread has read the group's rows; its first one takes their sum
+            done = leave(row_of(g0), counter, groups);
+            if (done) join(r0, kJoin, groups);
+          }
+        }
+      }
+      if (done) {
 #pragma unroll
         for (int h = 0; h < G; ++h) {
           if (h >= nh) break;
@@ -652,46 +756,6 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<G, PANELS>::CTAS)
           for (int q = 0; q < PANELS; ++q)
             if (q * 128 + tid < hd) out[static_cast<long long>(h) * hd + q * 128 + tid] = __float2bfloat16_rn(acc[q][h] * inv);
           if (lse && tid == 0) lse[h] = l[h] > 0.0f ? (m[h] + log2f(l[h])) * 0.693147180559945309f : -INFINITY;
-        }
-      } else {
-        const int heads = k.heads;
-        auto row_of = [&](int range) { return (2LL * range + (range == r0 ? 1 : 0)) * heads + k.head; };
-        const long long row = row_of(k.range);
-#pragma unroll
-        for (int h = 0; h < G; ++h) {
-          if (h >= nh) break;
-#pragma unroll
-          for (int q = 0; q < PANELS; ++q)
-            if (q * 128 + tid < hd) p.partial[(row * G + h) * hd + q * 128 + tid] = acc[q][h];
-          if (tid == 0) *reinterpret_cast<float2*>(part_ml + (row * G + h) * 2) = make_float2(m[h], l[h]);
-        }
-        __threadfence();  // the partial is visible device-wide before the unit is counted
-        named_barrier(1, kSoftmax);
-        if (tid == 0) sh.last = atomicAdd(p.counter + static_cast<long long>(r0) * heads + k.head, 1u) == static_cast<unsigned>(r1 - r0);
-        named_barrier(1, kSoftmax);
-        if (sh.last) {
-          __threadfence();
-          for (int h = 0; h < nh; ++h) {
-            float mm = kNone;
-            for (int r = r0; r <= r1; ++r) mm = fmaxf(mm, __ldcg(part_ml + (row_of(r) * G + h) * 2));
-            float ll = 0.0f, o[PANELS] = {};
-#pragma unroll 4
-            for (int r = r0; r <= r1; ++r) {
-              const long long pr = row_of(r) * G + h;
-              const float2 ml = __ldcg(reinterpret_cast<const float2*>(part_ml + pr * 2));
-              const float f = ex2(ml.x - mm);
-              ll += f * ml.y;
-#pragma unroll
-              for (int q = 0; q < PANELS; ++q)
-                if (q * 128 + tid < hd) o[q] += f * __ldcg(p.partial + pr * hd + q * 128 + tid);
-            }
-            const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
-#pragma unroll
-            for (int q = 0; q < PANELS; ++q)
-              if (q * 128 + tid < hd) out[static_cast<long long>(h) * hd + q * 128 + tid] = __float2bfloat16_rn(o[q] * inv);
-            if (lse && tid == 0) lse[h] = ll > 0.0f ? (mm + log2f(ll)) * 0.693147180559945309f : -INFINITY;
-          }
-          if (tid == 0) p.counter[static_cast<long long>(r0) * heads + k.head] = 0;  // ready for the next call
         }
       }
       (void)got;
@@ -729,7 +793,7 @@ AttnPlan plan_attn(int q_heads, int kv_heads, int head_dim, int num_sms, size_t*
   const long long units = p.ranges * heads;
   p.grid = static_cast<int>(units < slots ? units : slots);
   const int G = p.per_part <= 5 ? 5 : kMaxG;
-  const size_t counters = (static_cast<size_t>(units) * 4 + 255) & ~static_cast<size_t>(255);
+  const size_t counters = (static_cast<size_t>(units) * 12 + 255) & ~static_cast<size_t>(255);
   *bytes = counters + static_cast<size_t>(2 * units) * G * (head_dim + 2) * 4;
   return p;
 }
@@ -745,6 +809,8 @@ cudaError_t launch_inst(const AttnArgs& a, const AttnPlan& p, cudaStream_t st) {
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!attr_done[dev]) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess) return e;
     attr_done[dev] = true;
   }
@@ -764,7 +830,7 @@ cudaError_t launch_kv_attn_decode(const AttnArgs& a, int num_sms, cudaStream_t s
   AttnPlan p = plan_attn(a.q_heads, a.kv_heads, a.head_dim, num_sms, &bytes);
   const size_t units = static_cast<size_t>(p.ranges) * a.kv_heads * p.parts;
   p.counter = reinterpret_cast<unsigned*>(a.ws);
-  p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + ((units * 4 + 255) & ~static_cast<size_t>(255)));
+  p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + ((units * 12 + 255) & ~static_cast<size_t>(255)));
   if (a.head_dim <= 128) return p.per_part <= 5 ? launch_inst<5, 1>(a, p, st) : launch_inst<kMaxG, 1>(a, p, st);
   return p.per_part <= 5 ? launch_inst<5, 2>(a, p, st) : launch_inst<kMaxG, 2>(a, p, st);
 }
