@@ -162,17 +162,23 @@ def _dense(*ts):
 
 def _here(first, *ts):
     """The tensors of a call live on the current device: its kernels are launched there."""
-    dev = first.get_device()
-    if dev < 0 or dev != torch._C._cuda_getDevice():
-        raise ValueError(f"expected tensors on the current CUDA device, got {first.device}")
-    for t in ts:
+    dev = torch._C._cuda_getDevice() if first.is_cuda else -2
+    for t in (first, *ts):
         if t is not None and t.get_device() != dev:
-            raise ValueError(f"tensors on {first.device} and {t.device}")
+            raise ValueError(f"expected tensors on the current CUDA device, got {first.device} and {t.device}")
 
 
-def _typed(t, dtype, what, n=None):
-    if t is not None and (t.dtype != dtype or (n is not None and t.numel() != n)):
-        raise ValueError(f"{what} is {dtype}" + ("" if n is None else f" of {n} values"))
+def _vec(dtype, n, *named):
+    """Contiguous vectors of n values: (tensor or None, name) pairs -> their addresses."""
+    out = []
+    for t, name in named:
+        if t is None:
+            out.append(None)
+        elif t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
+            raise ValueError(f"{name} is {dtype}, {n} contiguous values")
+        else:
+            out.append(t.data_ptr())
+    return out
 
 
 def _logits(x):
@@ -336,25 +342,26 @@ def qurl_kv_attn_decode(q, q_heads, k_cache, k_scale, v_cache, v_scale, block_ta
     """Attention of one new token per row of q [B, >= q_heads * head_dim] over the
     paged FP8 cache (see include/qurl.h)."""
     _here(q, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, out, workspace, lse)
-    _dense(k_cache, k_scale, v_cache, v_scale, seq_lens, lse, workspace)
-    B = q.shape[0]
-    num_slots, kv_heads, head_dim = k_cache.shape
-    for c, sc in ((k_cache, k_scale), (v_cache, v_scale)):
-        if c.element_size() != 1 or c.shape != k_cache.shape or sc.dtype != torch.float32 or sc.shape != c.shape[:2]:
-            raise ValueError("caches are 8-bit [slots, kv_heads, head_dim] with fp32 scales [slots, kv_heads]")
-    if q.dtype != torch.bfloat16 or out.dtype != torch.bfloat16 or out.shape[0] != B:
+    num_slots, kv_heads, head_dim = shape = k_cache.shape
+    B, columns = q.shape
+    rows, max_blocks = block_table.shape
+    if (v_cache.shape != shape or k_cache.element_size() != 1 or v_cache.element_size() != 1
+            or not k_cache.is_contiguous() or not v_cache.is_contiguous()):
+        raise ValueError("caches are contiguous, 8-bit, [slots, kv_heads, head_dim]")
+    if q.dtype is not torch.bfloat16 or out.dtype is not torch.bfloat16 or out.shape[0] != B:
         raise ValueError("q and out are bf16 [B, ...]")
-    if q.shape[1] < q_heads * head_dim or out.shape[1] < q_heads * head_dim:
+    if min(columns, out.shape[1]) < q_heads * head_dim:
         raise ValueError("q and out have q_heads * head_dim columns at least")
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B:
+    if block_table.dtype is not torch.int32 or rows != B:
         raise ValueError("block_table is int32 [B, blocks]")
-    _typed(seq_lens, torch.int32, "seq_lens", B)
-    _typed(lse, torch.float32, "lse", B * q_heads)
-    max_blocks = block_table.shape[1]
-    _ok(load().qurl_kv_attn_decode(_ptr(q), _ld(q), B, q_heads, kv_heads, head_dim, _ptr(k_cache), _ptr(k_scale),
-                                   _ptr(v_cache), _ptr(v_scale), num_slots, _ptr(block_table),
-                                   _ld(block_table) if max_blocks else 0, max_blocks, block_size, _ptr(seq_lens),
-                                   window, scale, _ptr(out), _ld(out), _ptr(lse), _ptr(workspace),
+    _dense(workspace)
+    ks, vs = _vec(torch.float32, num_slots * kv_heads, (k_scale, "k_scale"), (v_scale, "v_scale"))
+    lens, = _vec(torch.int32, B, (seq_lens, "seq_lens"))
+    lse_at, = _vec(torch.float32, B * q_heads, (lse, "lse"))
+    _ok(load().qurl_kv_attn_decode(q.data_ptr(), _ld(q), B, q_heads, kv_heads, head_dim, k_cache.data_ptr(), ks,
+                                   v_cache.data_ptr(), vs, num_slots, block_table.data_ptr(),
+                                   _ld(block_table) if max_blocks else 0, max_blocks, block_size, lens, window, scale,
+                                   out.data_ptr(), _ld(out), lse_at, workspace.data_ptr(),
                                    workspace.numel() * workspace.element_size(), _stream(stream)),
         "qurl_kv_attn_decode")
 
@@ -364,17 +371,14 @@ def qurl_residual_rmsnorm_quant(H, Y, gamma_folded, qt, H_out, Xq, sx, gamma_pos
     """H_out = H + residual_scale * gate * RMSNorm(Y), then RMSNorm and per-token
     quantization of H_out (see include/qurl.h).  gate [M, K], or [K] / [1, K] for every token."""
     _here(Y, H, gamma_folded, H_out, Xq, sx, gamma_post, gate, ms_out)
-    _dense(gamma_folded, gamma_post, Xq, sx, ms_out)
-    M, K = Y.shape
+    M, K = shape = Y.shape
     for t, what in ((Y, "Y"), (H, "H"), (H_out, "H_out")):
-        if t.dtype != torch.bfloat16 or t.shape != (M, K):
+        if t.dtype is not torch.bfloat16 or t.shape != shape:
             raise ValueError(f"{what} is bf16 [M, K]")
-    for t, what in ((gamma_folded, "gamma_folded"), (gamma_post, "gamma_post")):
-        _typed(t, torch.float32, what, K)
-    _typed(sx, torch.float32, "sx", M)
-    _typed(ms_out, torch.float32, "ms_out", M)
-    if Xq.element_size() != 1 or Xq.numel() != M * K:
-        raise ValueError("Xq is one byte per code [M, K]")
+    gamma, post = _vec(torch.float32, K, (gamma_folded, "gamma_folded"), (gamma_post, "gamma_post"))
+    sx_at, ms_at = _vec(torch.float32, M, (sx, "sx"), (ms_out, "ms_out"))
+    if Xq.element_size() != 1 or Xq.numel() != M * K or not Xq.is_contiguous():
+        raise ValueError("Xq is one byte per code, contiguous [M, K]")
     ldg = 0
     if gate is not None:
         rows = 1 if gate.dim() == 1 else gate.shape[0]
@@ -382,56 +386,50 @@ def qurl_residual_rmsnorm_quant(H, Y, gamma_folded, qt, H_out, Xq, sx, gamma_pos
                 or gate.stride(-1) != 1:
             raise ValueError("gate is bf16 [M, K], [1, K] or [K]")
         ldg = 0 if rows == 1 else gate.stride(0)
-    _ok(load().qurl_residual_rmsnorm_quant(_ptr(Y), _ld(Y), _ptr(gamma_post), eps_post, _ptr(gate), ldg,
-                                           residual_scale, _ptr(H), _ld(H), _ptr(H_out), _ld(H_out),
-                                           _ptr(gamma_folded), eps, M, K, qt, _ptr(Xq), _ptr(sx), _ptr(ms_out),
-                                           _stream(stream)), "qurl_residual_rmsnorm_quant")
+    _ok(load().qurl_residual_rmsnorm_quant(Y.data_ptr(), _ld(Y), post, eps_post, _ptr(gate), ldg, residual_scale,
+                                           H.data_ptr(), _ld(H), H_out.data_ptr(), _ld(H_out), gamma, eps, M, K, qt,
+                                           Xq.data_ptr(), sx_at, ms_at, _stream(stream)),
+        "qurl_residual_rmsnorm_quant")
 
 
 def qurl_sample(logits, u, token, temperature=None, top_k=None, top_p=None, min_p=None, logp=None, logp_kept=None,
                 stream=None):
     """One token per row of logits [B, V] from uniform numbers u [B] (see include/qurl.h)."""
     _here(logits, u, token, temperature, top_k, top_p, min_p, logp, logp_kept)
-    _dense(u, token, temperature, top_k, top_p, min_p, logp, logp_kept)
     B, V = logits.shape
     xt, ld = _logits(logits)
-    for t, what in ((u, "u"), (temperature, "temperature"), (top_p, "top_p"), (min_p, "min_p"), (logp, "logp"),
-                    (logp_kept, "logp_kept")):
-        _typed(t, torch.float32, what, B)
-    _typed(top_k, torch.int32, "top_k", B)
-    _typed(token, torch.int64, "token", B)
-    _ok(load().qurl_sample(_ptr(logits), xt, B, V, ld, _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p),
-                           _ptr(u), _ptr(token), _ptr(logp), _ptr(logp_kept), _stream(stream)), "qurl_sample")
+    u_at, t_at, p_at, m_at, lp_at, lk_at = _vec(
+        torch.float32, B, (u, "u"), (temperature, "temperature"), (top_p, "top_p"), (min_p, "min_p"), (logp, "logp"),
+        (logp_kept, "logp_kept"))
+    k_at, = _vec(torch.int32, B, (top_k, "top_k"))
+    token_at, = _vec(torch.int64, B, (token, "token"))
+    _ok(load().qurl_sample(logits.data_ptr(), xt, B, V, ld, t_at, k_at, p_at, m_at, u_at, token_at, lp_at, lk_at,
+                           _stream(stream)), "qurl_sample")
 
 
 def qurl_token_logprob(logits, targets, logp, lse, temperature=1.0, stream=None):
     """Log-probabilities of targets [T] under logits [T, V] (see include/qurl.h)."""
     _here(logits, targets, logp, lse)
-    _dense(targets, logp, lse)
     T, V = logits.shape
     xt, ld = _logits(logits)
-    _typed(targets, torch.int64, "targets", T)
-    _typed(logp, torch.float32, "logp", T)
-    _typed(lse, torch.float32, "lse", T)
-    _ok(load().qurl_token_logprob(_ptr(logits), xt, T, V, ld, _ptr(targets), temperature, _ptr(logp), _ptr(lse),
-                                  _stream(stream)), "qurl_token_logprob")
+    at, = _vec(torch.int64, T, (targets, "targets"))
+    logp_at, lse_at = _vec(torch.float32, T, (logp, "logp"), (lse, "lse"))
+    _ok(load().qurl_token_logprob(logits.data_ptr(), xt, T, V, ld, at, temperature, logp_at, lse_at, _stream(stream)),
+        "qurl_token_logprob")
 
 
 def qurl_token_logprob_grad(logits, targets, lse, g, dlogits, temperature=1.0, scale=1.0, denom=None, stream=None):
     """The logits' gradient of scale * sum_t g[t] logp[t] / denom (see include/qurl.h)."""
     _here(logits, targets, lse, g, dlogits, denom)
-    _dense(targets, lse, g, denom)
-    T, V = logits.shape
+    T, V = shape = logits.shape
     xt, ld = _logits(logits)
-    if dlogits.dtype != logits.dtype or dlogits.shape != logits.shape:
+    if dlogits.dtype is not logits.dtype or dlogits.shape != shape:
         raise ValueError("dlogits has the logits' type and shape")
-    _typed(targets, torch.int64, "targets", T)
-    _typed(lse, torch.float32, "lse", T)
-    _typed(g, torch.float32, "g", T)
-    _typed(denom, torch.float64, "denom", 1)
-    _ok(load().qurl_token_logprob_grad(_ptr(logits), xt, T, V, ld, _ptr(targets), temperature, _ptr(lse), _ptr(g),
-                                       scale, _ptr(denom), _ptr(dlogits), _ld(dlogits), _stream(stream)),
-        "qurl_token_logprob_grad")
+    at, = _vec(torch.int64, T, (targets, "targets"))
+    lse_at, g_at = _vec(torch.float32, T, (lse, "lse"), (g, "g"))
+    n_at, = _vec(torch.float64, 1, (denom, "denom"))
+    _ok(load().qurl_token_logprob_grad(logits.data_ptr(), xt, T, V, ld, at, temperature, lse_at, g_at, scale, n_at,
+                                       dlogits.data_ptr(), _ld(dlogits), _stream(stream)), "qurl_token_logprob_grad")
 
 
 def qurl_check_device_status(stream=None):

@@ -779,17 +779,17 @@ AttnPlan plan_attn(int q_heads, int kv_heads, int head_dim, int num_sms, size_t*
   p.per_part = (group + p.parts - 1) / p.parts;
   const long long heads = static_cast<long long>(kv_heads) * p.parts;
   const long long slots = static_cast<long long>(num_sms) * (head_dim <= 128 ? 2 : 1);
-  // the fewest ranges whose units fill their last round of CTAs to 97%, or the best of up to four rounds
+  // as many ranges as fill the CTAs' first round to 97%, or the best of up to four rounds
   double best = 0.0;
-  for (long long r = 1; r <= 4 * slots / heads + 1; ++r) {
-    const long long u = r * heads, rounds = (u + slots - 1) / slots;
-    const double fill = static_cast<double>(u) / static_cast<double>(rounds * slots);
-    if (fill > best + 1e-9) {
+  for (long long rounds = 1; rounds <= 4 && best < 0.97; ++rounds) {
+    const long long r = rounds * slots / heads;
+    const double fill = static_cast<double>(r * heads) / static_cast<double>(rounds * slots);
+    if (fill > best) {
       best = fill;
       p.ranges = static_cast<int>(r);
     }
-    if (best >= 0.97) break;
   }
+  if (p.ranges < 1) p.ranges = 1;
   const long long units = p.ranges * heads;
   p.grid = static_cast<int>(units < slots ? units : slots);
   const int G = p.per_part <= 5 ? 5 : kMaxG;
