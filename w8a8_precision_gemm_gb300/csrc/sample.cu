@@ -99,9 +99,9 @@ __device__ __forceinline__ float place_logit(u64 p) { return key_value(~static_c
 // What turns a row's logits into weights.
 struct Scale {
   float top;       // the largest logit
-  float chi, clo;  // log2(e) / temperature as a pair
-  float zero;      // exponents up to this weigh less than a unit: 0
-  int bias;        // position of the weights' leading bit, see weight()
+  float chi, clo;  // log2(e) / temperature as a pair; for bf16 logits chi has 16 bits, so x chi is exact
+  float c512;      // 512 log2(e) / temperature
+  int bias;        // position of the weights' leading bit
   bool rel;        // logits of large magnitude: their difference to the top is taken first
 };
 
@@ -109,31 +109,76 @@ constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: adding it rounds to an int
 
 // w as an integer: 2^(x log2(e) / temperature - E + S) with E the integer part of
 // that exponent for the largest logit (in relative rows of x - top).
+//   x log2(e) / temperature = k / 512 + r, |r| <= 2^-10 and a little;  w = 2^(k / 512) (1 + (2^r - 1))
+// finish(): from t = k + magic and r.  2^32 (2^r - 1) = 2^32 (y + y^2 / 2 + y^3 / 6),
+// y = r ln 2, as an integer (the next term is below 2^-43); (w : 0) is shifted
+// down by n, and shifts of 64 and more -- logits so small, -inf and, as n is
+// then negative, what is not a number -- give 0.
+constexpr double kLn2 = 0.69314718055994530942, kUnit = 4294967296.0;
+constexpr float kC1 = static_cast<float>(kUnit * kLn2), kC2 = static_cast<float>(kUnit * kLn2 * kLn2 / 2),
+                kC3 = static_cast<float>(kUnit * kLn2 * kLn2 * kLn2 / 6);
+
+__device__ __forceinline__ u64 finish_weight(float t, float q, const Scale& s, const uint32_t* table) {
+  const int k = static_cast<int>(__float_as_uint(t));  // 0x4B400000 + k
+  const int qi = static_cast<int>(__float_as_uint(q)) - 0x4B400000;
+  const uint32_t tj = table[k & (kTable - 1)];
+  uint32_t w;
+  asm("mad.hi.s32 %0, %1, %2, %1;" : "=r"(w) : "r"(tj), "r"(qi));
+  const int n = s.bias - (k >> 9);
+  u64 v;
+  asm("shr.b64 %0, %1, %2;" : "=l"(v) : "l"(static_cast<u64>(w) << 32), "r"(n));
+  return v;
+}
+
+// One logit (kBf16: of bf16 precision).
+template <bool kBf16>
 __device__ __forceinline__ u64 weight(float x, const Scale& s, const uint32_t* table) {
-  float d = x, dl = 0.0f;
+  float t, r;
   if (s.rel) {  // x - top as an exact pair (two-sum); +inf counts as the largest float
     x = x > FLT_MAX ? FLT_MAX : x;
-    d = __fsub_rn(x, s.top);
+    const float d = __fsub_rn(x, s.top);
     const float bb = __fsub_rn(d, x);
-    dl = __fsub_rn(__fsub_rn(x, __fsub_rn(d, bb)), __fadd_rn(s.top, bb)) * s.chi;
+    const float dl = __fsub_rn(__fsub_rn(x, __fsub_rn(d, bb)), __fadd_rn(s.top, bb));
+    const float ph = __fmul_rn(d, s.chi);
+    const float pl = __fmaf_rn(dl, s.chi, __fmaf_rn(d, s.clo, __fmaf_rn(d, s.chi, -ph)));
+    t = __fmaf_rn(d, s.c512, kMagic);
+    r = __fadd_rn(__fmaf_rn(__fsub_rn(t, kMagic), -1.0f / kTable, ph), pl);
+  } else {
+    const float ph = __fmul_rn(x, s.chi);
+    t = __fmaf_rn(x, s.c512, kMagic);
+    r = __fmaf_rn(__fsub_rn(t, kMagic), -1.0f / kTable, ph);
+    r = kBf16 ? __fmaf_rn(x, s.clo, r) : __fadd_rn(r, __fmaf_rn(x, s.clo, __fmaf_rn(x, s.chi, -ph)));
   }
-  const float ph = __fmul_rn(d, s.chi);
-  float pl = fmaf(d, s.clo, fmaf(d, s.chi, -ph));
-  if (s.rel) pl += dl;
-  // ph + pl = k / 512 + r, |r| <= 2^-10 and a little
-  const float t = fmaf(ph, static_cast<float>(kTable), kMagic);
-  const int k = static_cast<int>(__float_as_uint(t));  // 0x4B400000 + k
-  const float r = fmaf(t - kMagic, -1.0f / kTable, ph) + pl;
-  // 2^32 (2^r - 1) = 2^32 (r ln 2 + (r ln 2)^2 / 2 + (r ln 2)^3 / 6) as an integer: the next term is below 2^-43
-  constexpr double kLn2 = 0.69314718055994530942, kUnit = 4294967296.0;
-  const float c = fmaf(r, fmaf(r, static_cast<float>(kUnit * kLn2 * kLn2 * kLn2 / 6), static_cast<float>(kUnit * kLn2 * kLn2 / 2)),
-                       static_cast<float>(kUnit * kLn2));
-  const int qi = static_cast<int>(__float_as_uint(fmaf(r, c, kMagic))) - 0x4B400000;
-  const uint32_t tj = table[k & (kTable - 1)];
-  const uint32_t w = tj + static_cast<uint32_t>(__mulhi(static_cast<int>(tj), qi));
-  const int n = s.bias - (k >> 9);  // bits to shift (w : 0) down by: 0 .. 63 where the weight is not 0
-  const u64 v = (static_cast<u64>(w) << 32) >> (n & 63);
-  return ph > s.zero ? v : 0;  // (false for what is not a number)
+  const float c = __fmaf_rn(r, __fmaf_rn(r, kC3, kC2), kC1);
+  return finish_weight(t, __fmaf_rn(r, c, kMagic), s, table);
+}
+
+// The same for a vector's logits, two at a time in the paired fp32 instructions.
+template <bool kBf16, int N>
+__device__ __forceinline__ void weights(const float (&x)[N], u64 (&w)[N], const Scale& s, const uint32_t* table) {
+  if (s.rel) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) w[e] = weight<kBf16>(x[e], s, table);
+    return;
+  }
+  const float2 chi = make_float2(s.chi, s.chi), clo = make_float2(s.clo, s.clo), c512 = make_float2(s.c512, s.c512);
+  const float2 mg = make_float2(kMagic, kMagic), nmg = make_float2(-kMagic, -kMagic);
+  const float2 step = make_float2(-1.0f / kTable, -1.0f / kTable);
+  const float2 c1 = make_float2(kC1, kC1), c2 = make_float2(kC2, kC2), c3 = make_float2(kC3, kC3);
+#pragma unroll
+  for (int e = 0; e < N; e += 2) {
+    const float2 v = make_float2(x[e], x[e + 1]);
+    const float2 ph = __fmul2_rn(v, chi);
+    const float2 t = __ffma2_rn(v, c512, mg);
+    float2 r = __ffma2_rn(__fadd2_rn(t, nmg), step, ph);
+    if (kBf16)
+      r = __ffma2_rn(v, clo, r);
+    else
+      r = __fadd2_rn(r, __ffma2_rn(v, clo, __ffma2_rn(v, chi, make_float2(-ph.x, -ph.y))));
+    const float2 q = __ffma2_rn(r, __ffma2_rn(r, __ffma2_rn(r, c3, c2), c1), mg);
+    w[e] = finish_weight(t.x, q.x, s, table);
+    w[e + 1] = finish_weight(t.y, q.y, s, table);
+  }
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -302,7 +347,7 @@ struct Shared {
   float sq[kWarps];
   uint32_t short_n;   // candidates ranked
   int token;
-  float chi, clo;
+  float chi, clo, c512;
   u64 found_before;
 };
 
@@ -349,7 +394,7 @@ __device__ u64 block_scan(u64 v, u64& all, Shared& sh) {
 // The place of the first element, in the order, at which the running measure
 // (1 an element, or its weight) reaches `target` (at least 1); kAll when all of
 // them stay below it.  each(f) calls f(place) for the elements, by the block.
-template <bool kMass, typename Each>
+template <bool kMass, bool kBf16, typename Each>
 __device__ u64 radix_select(Each&& each, const Scale& s, u64 target, Shared& sh) {
   // the bits that all elements share are skipped (a digit that all share would have every thread add to one counter)
   u64 least = kAll, most = 0;
@@ -389,7 +434,7 @@ __device__ u64 radix_select(Each&& each, const Scale& s, u64 target, Shared& sh)
     __syncthreads();
     each([&](u64 p) {
       if ((p & known) != prefix) return;
-      const u64 v = kMass ? weight(place_logit(p), s, sh.table) : 1ull;
+      const u64 v = kMass ? weight<kBf16>(place_logit(p), s, sh.table) : 1ull;
       if (v) atomicAdd(&sh.hist[static_cast<uint32_t>(p >> shift) & digits], v);
     });
     __syncthreads();
@@ -487,6 +532,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
   const int seg = kSeg * ((a.V - 1) / (kSeg * kMaxSegs) + 1);
   const int nseg = (a.V - 1) / seg + 1;
   constexpr int N = Load<T>::N;
+  constexpr bool B16 = N == 8;  // bf16 logits
   const int s0 = static_cast<int>(static_cast<long long>(nseg) * rank / cluster);  // this CTA's segments
   const int s1 = static_cast<int>(static_cast<long long>(nseg) * (rank + 1) / cluster);
   const int warp = tid >> 5, per = seg / (32 * N), steps = (a.V - 1) / (32 * N) + 1;
@@ -512,8 +558,11 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
     constexpr double kLog2e = 1.4426950408889634074;
     constexpr float lh = static_cast<float>(kLog2e), ll = static_cast<float>(kLog2e - static_cast<double>(static_cast<float>(kLog2e)));
     const float ch = __fdiv_rn(lh, pr.temp);
-    sh.chi = ch;
-    sh.clo = __fdiv_rn(fmaf(-ch, pr.temp, lh) + ll, pr.temp);
+    const float cl = __fdiv_rn(__fmaf_rn(-ch, pr.temp, lh) + ll, pr.temp);
+    const float c16 = __uint_as_float(__float_as_uint(ch) & 0xFFFFFF00u);
+    sh.chi = B16 ? c16 : ch;
+    sh.clo = B16 ? __fadd_rn(__fsub_rn(ch, c16), cl) : cl;  // (ch - c16 is exact)
+    sh.c512 = ch * kTable;
     sh.have = 0;
     if (pr.min_p > 0.0f) sh.drop = static_cast<double>(pr.temp) * log(static_cast<double>(pr.min_p));
   }
@@ -560,12 +609,12 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
   s.top = top;
   s.chi = sh.chi;
   s.clo = sh.clo;
+  s.c512 = sh.c512;
   s.rel = !(fabsf(top) * s.chi < 4000.0f);
   const int e0 = s.rel ? 0 : static_cast<int>(floorf(top * s.chi));  // (k >> 9 of the largest logit, or one beside it)
   // k >> 9 carries the magic number's 0x4B400000 >> 9; (w : 0) has its leading bit at 62 and the largest weight
   // at S or S + 1, S = 62 - shift
   s.bias = (0x4B400000 >> 9) + e0 + a.shift;
-  s.zero = (s.rel ? 0.0f : top * s.chi) - (60.0f - a.shift);
   const float extent = fminf(32.0f / (s.chi * 0.69314718f), top - key_value(sh.low));  // -inf logits: the first
   const float binscale = extent > 0.0f ? kBins / extent : 0.0f;
   // (+inf falls into the first step, -inf and what is not a number into the last)
@@ -621,8 +670,10 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
       u64 v = 0;
       row.run(
           [&](const float (&x)[N], int, int) {
+            u64 w[N];
+            weights<B16>(x, w, s, sh.table);
 #pragma unroll
-            for (int e = 0; e < N; ++e) v += weight(x[e], s, sh.table);
+            for (int e = 0; e < N; ++e) v += w[e];
           },
           [&](int sg) {
             v = warp_sum(v);
@@ -647,16 +698,19 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
       };
       if (exact_total) {
         row.all([&](const float (&x)[N], int i, int n) {
+          u64 w[N];
+          weights<B16>(x, w, s, sh.table);
 #pragma unroll
-          for (int e = 0; e < N; ++e) z += weight(x[e], s, sh.table);
+          for (int e = 0; e < N; ++e) z += w[e];
           candidates(x, i, n);
         });
       } else {
         float zf = 0.0f;
+        const float c1 = s.c512 * (1.0f / kTable);  // log2(e) / temperature
         row.all([&](const float (&x)[N], int i, int n) {
           // (what is not a number: 0; +inf, the top: 1)
 #pragma unroll
-          for (int e = 0; e < N; ++e) zf += __saturatef(ex2((x[e] - top) * s.chi));
+          for (int e = 0; e < N; ++e) zf += __saturatef(ex2((x[e] - top) * c1));
           candidates(x, i, n);
         });
         z = __float2ull_rn(zf * 4294967296.0f);
@@ -703,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
   auto finish = [&](int token) {  // two threads, one for each logarithm
     // log w_token - log w_top = (x - top) / temperature, from an exact difference
     const float x = clean(Load<T>::one(row.x + token));
-    const u64 w_top = weight(top, s, sh.table);
+    const u64 w_top = weight<B16>(top, s, sh.table);
     const double d = (static_cast<double>(x) - static_cast<double>(top)) * (static_cast<double>(s.chi) + s.clo) * 0.69314718055994530942;
     if (tid == 0) {
       a.token[b] = token;
@@ -726,7 +780,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
       for (int e = 0; e < 2; ++e) {
         const int i = tid + e * kThreads;
         p[e] = i < n ? sh.list[i] : kAll;
-        w[e] = i < n ? weight(place_logit(p[e]), s, sh.table) : 0;
+        w[e] = i < n ? weight<B16>(place_logit(p[e]), s, sh.table) : 0;
         if (i < n) sh.w[i] = w[e];
       }
       __syncthreads();
@@ -819,8 +873,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
     };
     row.sample(steps >= 256 * cluster ? 8 : 1, [&](const float (&x)[N], int, int n) {
       u64 w[N];
-#pragma unroll
-      for (int e = 0; e < N; ++e) w[e] = weight(x[e], s, sh.table);
+      weights<B16>(x, w, s, sh.table);
 #pragma unroll
       for (int e = 0; e < N; ++e) {
         if (!(x[e] < below) || e >= n) continue;
@@ -861,7 +914,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
             const double total = stage == 0    ? static_cast<double>(a.V)
                                  : exact_total ? static_cast<double>(sh.total)
                                                : static_cast<double>(sh.total) * 0x1p-32 *
-                                                     static_cast<double>(weight(top, s, sh.table));
+                                                     static_cast<double>(weight<B16>(top, s, sh.table));
             const double known = !ranked ? 0.0 : static_cast<double>(stage == 0 ? sh.short_n : sh.have);
             sh.share = static_cast<float>((static_cast<double>(target) - known) / fmax(total - known, 1.0));
             sh.pick_lo = kBins;
@@ -927,8 +980,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
               for (int e = 1; e < N; ++e) most = fmaxf(most, x[e]);
               if (!(most >= lo)) return;
               u64 w[N];
-#pragma unroll
-              for (int e = 0; e < N; ++e) w[e] = weight(x[e], s, sh.table);
+              weights<B16>(x, w, s, sh.table);
 #pragma unroll
               for (int e = 0; e < N; ++e) {
                 v += x[e] > hi ? w[e] : 0;
@@ -1012,11 +1064,10 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
                   before_step = before_step || k[e] < want;
                 }
                 if (before_step) {
+                  u64 w[N];
+                  weights<B16>(x, w, s, sh.table);
 #pragma unroll
-                  for (int e = 0; e < N; ++e) {
-                    const u64 w = weight(x[e], s, sh.table);
-                    v += k[e] < want ? w : 0;
-                  }
+                  for (int e = 0; e < N; ++e) v += k[e] < want ? w[e] : 0;
                 }
 #pragma unroll
                 for (int e = 0; e < N; ++e)
@@ -1049,7 +1100,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
             u64 l = kAll;
             if (n <= kThreads) {  // ranked against each other
               const u64 p = tid < n ? sh.list[tid] : kAll;
-              const u64 w = tid >= n ? 0 : stage == 0 ? 1 : weight(place_logit(p), s, sh.table);
+              const u64 w = tid >= n ? 0 : stage == 0 ? 1 : weight<B16>(place_logit(p), s, sh.table);
               if (tid < n) sh.w[tid] = w;
               if (tid == 0) sh.picked = kAll;
               __syncthreads();
@@ -1061,15 +1112,15 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
               __syncthreads();
               l = sh.picked;
             } else if (stage == 0)
-              l = n <= kList ? radix_select<false>(listed, s, target - before, sh) : radix_select<false>(whole, s, target - before, sh);
+              l = n <= kList ? radix_select<false, B16>(listed, s, target - before, sh) : radix_select<false, B16>(whole, s, target - before, sh);
             else
-              l = n <= kList ? radix_select<true>(listed, s, target - before, sh) : radix_select<true>(whole, s, target - before, sh);
+              l = n <= kList ? radix_select<true, B16>(listed, s, target - before, sh) : radix_select<true, B16>(whole, s, target - before, sh);
             if (l < limit) limit = l;
           }
           if (stage != 2) {  // what the limit leaves
             u64 v = 0;
             auto add = [&](u64 p) {
-              if (p <= limit) v += weight(place_logit(p), s, sh.table);
+              if (p <= limit) v += weight<B16>(place_logit(p), s, sh.table);
             };
             if (n <= kList) listed(add);
             else whole(add);
@@ -1099,7 +1150,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
           [&](const float (&x)[N], int i, int n) {
 #pragma unroll
             for (int e = 0; e < N; ++e)
-              if (x[e] <= hi && x[e] >= least && e < n && place(x[e], i + e) <= limit) v += weight(x[e], s, sh.table);
+              if (x[e] <= hi && x[e] >= least && e < n && place(x[e], i + e) <= limit) v += weight<B16>(x[e], s, sh.table);
           },
           [&](int sg) {
             v = warp_sum(v);
@@ -1112,7 +1163,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
     if (first && quick) {
       for (int i = tid; i < n_last; i += kThreads) {
         const u64 p = sh.list[i];
-        if (p <= limit) atomicAdd(&sh.segs[static_cast<int>(static_cast<uint32_t>(p)) / seg], weight(place_logit(p), s, sh.table));
+        if (p <= limit) atomicAdd(&sh.segs[static_cast<int>(static_cast<uint32_t>(p)) / seg], weight<B16>(place_logit(p), s, sh.table));
       }
       __syncthreads();
     }
@@ -1138,7 +1189,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
       u64 w = 0;
       if (i < end) {
         const float x = Load<T>::one(row.x + i);
-        if (place(x, i) <= limit) w = weight(x, s, sh.table);
+        if (place(x, i) <= limit) w = weight<B16>(x, s, sh.table);
       }
       u64 all;
       c = run + block_scan(w, all, sh);
