@@ -424,8 +424,9 @@ qurl_status qurl_kv_cache_dequant(const void* cache, const float* scale, const i
  * Rows are independent, results identical run to run.  B = 0 is valid.
  * Errors: INVALID_ARG (NULL, a size out of range, q_heads % kv_heads, ld_table <
  * max_blocks, window < 0, scale not finite), UNSUPPORTED (head_dim; B * q_heads
- * or max_blocks * block_size of 2^31 or more), ALIGNMENT, WORKSPACE.  One kernel
- * launch.
+ * of 2^31 or more, max_blocks * block_size above 2^30), ALIGNMENT, WORKSPACE.  One
+ * kernel launch.  If its bounded waits run out (QURL_ERR_TIMEOUT), zero the
+ * workspace before its next use.
  */
 size_t qurl_kv_attn_workspace_size(int B, int q_heads, int kv_heads, int head_dim, int max_blocks, int block_size);
 qurl_status qurl_kv_attn_decode(const void* q, int ldq, int B, int q_heads, int kv_heads, int head_dim,
@@ -467,15 +468,17 @@ qurl_status qurl_residual_rmsnorm_quant(const void* Y, int ldy, const float* gam
  *   logp      = (x_token - max x) / temperature - log sum_v w_v          (all of the row)
  *   logp_kept = the same over the kept weight: what the token was drawn from
  * temperature 0 is greedy: the first of the order, logp that of temperature 1,
- * logp_kept 0.  The weights are held as 62-bit integers (relative error below
- * 2^-29), so a choice does not depend on the order of a sum.
+ * logp_kept 0.  The weights that decide are integers (to a relative 2^-29, in
+ * units of 2^(ceil(log2 V) - 61) of the largest), so a choice does not depend on
+ * the order of a sum; a token of less than a unit is never drawn.
  *   temperature [B] fp32, 0 or in [1e-6, 1e6]; NULL: 1.   top_k [B] int32, <= 0 or >= V: off; NULL: off.
  *   top_p [B] fp32 >= 0, >= 1: off; NULL: off.            min_p [B] fp32 in [0, 1], 0: off; NULL: off.
  *   u [B] fp32 in [0, 1).  token [B] int64.  logp, logp_kept [B] fp32 or NULL.
  * -inf logits are never drawn; NaN counts as -inf, +inf as the largest float.
  * A row with nothing to draw (every logit -inf) gets token -1 and -inf twice; so
  * does a row with a parameter out of range, which latches QURL_ERR_INVALID_ARG
- * in the device status word.  B = 0 is valid.  One kernel launch.
+ * in the device status word.  B = 0 is valid.  Errors: INVALID_ARG, UNSUPPORTED (V
+ * above 2^24), ALIGNMENT.  One kernel launch.
  */
 qurl_status qurl_sample(const void* logits, qurl_ftype x_type, int B, int V, int ld, const float* temperature,
                         const int32_t* top_k, const float* top_p, const float* min_p, const float* u, int64_t* token,
@@ -498,7 +501,8 @@ qurl_status qurl_sample(const void* logits, qurl_ftype x_type, int B, int V, int
  *   themselves (ldd == ld).  Columns V .. ld - 1 are neither read nor written.
  * -inf logits have probability 0; a row of nothing else gives -inf and a zero
  * gradient.  NaN and +inf logits are outside the domain.  temperature in [1e-6, 1e6].
- * T = 0 is valid.  One kernel launch each.
+ * T = 0 is valid.  Errors: INVALID_ARG, UNSUPPORTED (V above 2^30), ALIGNMENT.  One
+ * kernel launch each.
  */
 qurl_status qurl_token_logprob(const void* logits, qurl_ftype x_type, int T, int V, int ld, const int64_t* targets,
                                float temperature, float* logp, float* lse, qurl_stream_t stream);

@@ -35,7 +35,7 @@ ATTN = dict(q=FAKE, ldq=1024, B=2, q_heads=8, kv_heads=2, hd=64, k=FAKE, ks=FAKE
     (dict(block=0), INVALID), (dict(ldt=3), INVALID), (dict(window=-1), INVALID), (dict(scale=float("nan")), INVALID),
     (dict(scale=float("inf")), INVALID), (dict(ldq=504), INVALID), (dict(ldo=504), INVALID),
     (dict(hd=72), UNSUPPORTED), (dict(hd=272, ldq=4096, ldo=4096), UNSUPPORTED),
-    (dict(blocks=1 << 20, ldt=1 << 20, block=1 << 11), UNSUPPORTED), (dict(B=1 << 28), UNSUPPORTED),
+    (dict(blocks=1 << 20, ldt=1 << 20, block=(1 << 10) + 1), UNSUPPORTED), (dict(B=1 << 28), UNSUPPORTED),
     (dict(q=ODD), ALIGNMENT), (dict(k=ODD), ALIGNMENT), (dict(v=ODD), ALIGNMENT), (dict(out=ODD), ALIGNMENT),
     (dict(ws=ODD), ALIGNMENT), (dict(ldq=1028), ALIGNMENT), (dict(ldo=1028), ALIGNMENT), (dict(ks=ODD2), ALIGNMENT),
     (dict(vs=ODD2), ALIGNMENT), (dict(table=ODD2), ALIGNMENT), (dict(lens=ODD2), ALIGNMENT), (dict(lse=ODD2), ALIGNMENT),
@@ -82,7 +82,7 @@ SAMPLE = dict(x=FAKE, type=0, B=2, V=100, ld=104, t=FAKE, k=FAKE, p=FAKE, m=FAKE
     (dict(u=None), INVALID), (dict(token=None), INVALID), (dict(x=ODD), ALIGNMENT), (dict(ld=100), ALIGNMENT),
     (dict(type=1, ld=102), ALIGNMENT), (dict(token=ODD4), ALIGNMENT), (dict(u=ODD2), ALIGNMENT),
     (dict(t=ODD2), ALIGNMENT), (dict(k=ODD2), ALIGNMENT), (dict(p=ODD2), ALIGNMENT), (dict(m=ODD2), ALIGNMENT),
-    (dict(logp=ODD2), ALIGNMENT), (dict(kept=ODD2), ALIGNMENT),
+    (dict(logp=ODD2), ALIGNMENT), (dict(kept=ODD2), ALIGNMENT), (dict(V=(1 << 24) + 1, ld=1 << 25), UNSUPPORTED),
 ])
 def test_sample_validation(L, change, status):
     assert L.qurl_sample(*(SAMPLE | change).values()) == status
@@ -99,6 +99,7 @@ GRAD = dict(x=FAKE, type=0, T=2, V=100, ld=104, targets=FAKE, t=1.0, lse=FAKE, g
     (dict(targets=None), INVALID), (dict(lse=None), INVALID), (dict(t=0.0), INVALID), (dict(t=float("nan")), INVALID),
     (dict(t=-1.0), INVALID), (dict(t=1e7), INVALID), (dict(x=ODD), ALIGNMENT), (dict(ld=100), ALIGNMENT),
     (dict(targets=ODD4), ALIGNMENT), (dict(lse=ODD2), ALIGNMENT),
+    (dict(V=(1 << 30) + 1, ld=(1 << 30) + 8), UNSUPPORTED),
 ])
 def test_logprob_validation(L, change, status):
     assert L.qurl_token_logprob(*(LOGP | change).values()) == status

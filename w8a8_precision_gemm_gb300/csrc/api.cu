@@ -170,6 +170,7 @@ qurl_status check_gemm(const void* Xq, const void* Wq, int M, int N, int K, int 
 // Rows of logits (bf16 or fp32) of V values, row stride ld elements.
 qurl_status check_logits(const void* x, int type, int V, int ld) {
   if (!x || !valid_dim(V) || ld < V || (type != QURL_BF16 && type != QURL_FP32)) return QURL_ERR_INVALID_ARG;
+  if (V > (1 << 30)) return QURL_ERR_UNSUPPORTED;
   const int esize = (type == QURL_FP32) ? 4 : 2;
   if (!aligned16(x) || (static_cast<long long>(ld) * esize) % 16 != 0) return QURL_ERR_ALIGNMENT;
   return QURL_OK;
@@ -915,7 +916,7 @@ qurl_status qurl_kv_attn_decode(const void* q, int ldq, int B, int q_heads, int 
   if (head_dim % 16 != 0 || head_dim > 256) return QURL_ERR_UNSUPPORTED;
   const long long q_dim = static_cast<long long>(q_heads) * head_dim;
   if (ldq < q_dim || ldo < q_dim) return QURL_ERR_INVALID_ARG;
-  if (static_cast<long long>(max_blocks) * block_size >= (1LL << 31) ||
+  if (static_cast<long long>(max_blocks) * block_size > (1LL << 30) ||
       static_cast<long long>(B) * q_heads >= (1LL << 31))
     return QURL_ERR_UNSUPPORTED;
   if (B == 0) return QURL_OK;
@@ -989,6 +990,7 @@ qurl_status qurl_sample(const void* logits, qurl_ftype x_type, int B, int V, int
   if (B == 0) return QURL_OK;
   QURL_TRY(check_logits(logits, x_type, V, ld));
   if (!u || !token) return QURL_ERR_INVALID_ARG;
+  if (V > (1 << 24)) return QURL_ERR_UNSUPPORTED;
   if ((reinterpret_cast<uintptr_t>(token) & 7u) != 0) return QURL_ERR_ALIGNMENT;
   for (const void* p : {static_cast<const void*>(temperature), static_cast<const void*>(top_k),
                         static_cast<const void*>(top_p), static_cast<const void*>(min_p), static_cast<const void*>(u),
