@@ -298,8 +298,15 @@ __device__ __forceinline__ uint32_t remote(const void* p, uint32_t rank) { retur
 __device__ __forceinline__ void remote_add64(uint32_t a, u64 v) {
   asm volatile("red.relaxed.cluster.shared::cluster.add.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
 }
-__device__ __forceinline__ void remote_add32(uint32_t a, uint32_t v) {
-  asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+__device__ __forceinline__ u64 remote_get64(uint32_t a) {
+  u64 v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t remote_get32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
 }
 __device__ __forceinline__ void remote_max32(uint32_t a, uint32_t v) {
   asm volatile("red.relaxed.cluster.shared::cluster.max.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
@@ -355,6 +362,17 @@ __device__ __forceinline__ u64 warp_sum(u64 v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
+}
+
+// Adds to a 64-bit counter in shared memory by its halves, the low one's carry
+// going to the high one: 64-bit shared-memory atomics are loops of compare and
+// swap (11 to 66 ns a warp at 512 to 8 counters and four CTAs an SM; this 3 to 6).
+__device__ __forceinline__ void add64(u64* counter, u64 v) {
+  uint32_t* half = reinterpret_cast<uint32_t*>(counter);
+  const uint32_t lo = static_cast<uint32_t>(v);
+  const uint32_t old = atomicAdd(half, lo);
+  const uint32_t hi = static_cast<uint32_t>(v >> 32) + (old + lo < lo ? 1u : 0u);
+  if (hi != 0) atomicAdd(half + 1, hi);
 }
 
 // Sum over the block; every thread gets it.
@@ -435,7 +453,7 @@ __device__ u64 radix_select(Each&& each, const Scale& s, u64 target, Shared& sh)
     each([&](u64 p) {
       if ((p & known) != prefix) return;
       const u64 v = kMass ? weight<kBf16>(place_logit(p), s, sh.table) : 1ull;
-      if (v) atomicAdd(&sh.hist[static_cast<uint32_t>(p >> shift) & digits], v);
+      if (v) add64(&sh.hist[static_cast<uint32_t>(p >> shift) & digits], v);
     });
     __syncthreads();
     const u64 v = sh.hist[threadIdx.x];
@@ -855,14 +873,23 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
   if (order == kHistogram) {
     // ---- the kept set is larger.  A sample (of what lies below the cut, when the candidates' weight is known)
     const float below = sh.bin ? cut : INFINITY;
-    auto gather = [&](u64* mass_to, uint32_t* count_to) {  // the CTAs' steps into the first one's
-      __syncthreads();
-      for (int k = tid; k < kBins; k += kThreads) {
-        if (sh.mass[k] && (!first || mass_to != sh.mass)) remote_add64(remote(mass_to + k, 0), sh.mass[k]);
-        if (sh.count[k] && (!first || count_to != sh.count)) remote_add32(remote(count_to + k, 0), sh.count[k]);
-      }
+    auto gather = [&](u64* mass_to, uint32_t* count_to) {  // the first CTA: the sums of all CTAs' steps
       if (cluster > 1) cluster_sync();
       else __syncthreads();
+      if (first) {
+        for (int k = tid; k < kBins; k += kThreads) {
+          u64 v = sh.mass[k];
+          uint32_t c = sh.count[k];
+          for (int r = 1; r < cluster; ++r) {
+            v += remote_get64(remote(&sh.mass[k], r));
+            c += remote_get32(remote(&sh.count[k], r));
+          }
+          mass_to[k] = v;
+          count_to[k] = c;
+        }
+        __syncthreads();
+      }
+      // (the others keep theirs until the first CTA's next order)
     };
     auto clear = [&] {
       for (int k = tid; k < kBins; k += kThreads) {
@@ -871,7 +898,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
       }
       __syncthreads();
     };
-    row.sample(steps >= 256 * cluster ? 8 : 1, [&](const float (&x)[N], int, int n) {
+    row.sample(steps >= 128 ? 8 : 1, [&](const float (&x)[N], int, int n) {
       u64 w[N];
       weights<B16>(x, w, s, sh.table);
 #pragma unroll
@@ -879,7 +906,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
         if (!(x[e] < below) || e >= n) continue;
         const int k = bin_of(x[e]);
         atomicAdd(&sh.count[k], 1u);
-        if (w[e]) atomicAdd(&sh.mass[k], w[e]);
+        if (w[e]) add64(&sh.mass[k], w[e]);
       }
     });
     gather(sh.sample_mass, sh.sample_count);
@@ -991,7 +1018,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
                 if (x[e] >= lo && x[e] <= hi && e < n) {
                   const int k = step_of(x[e]);
                   if (stage == 0) atomicAdd(&sh.count[k], 1u);
-                  if (w[e]) atomicAdd(&sh.mass[k], w[e]);
+                  if (w[e]) add64(&sh.mass[k], w[e]);
                 }
             },
             [&](int sg) {
@@ -1163,7 +1190,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
     if (first && quick) {
       for (int i = tid; i < n_last; i += kThreads) {
         const u64 p = sh.list[i];
-        if (p <= limit) atomicAdd(&sh.segs[static_cast<int>(static_cast<uint32_t>(p)) / seg], weight<B16>(place_logit(p), s, sh.table));
+        if (p <= limit) add64(&sh.segs[static_cast<int>(static_cast<uint32_t>(p)) / seg], weight<B16>(place_logit(p), s, sh.table));
       }
       __syncthreads();
     }
