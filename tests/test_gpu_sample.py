@@ -157,6 +157,18 @@ def test_min_p(m):
     check(x, u, t=f32(.5, 2., 5.), k=i32(40, 4000, 0), p=f32(1., .9, .99), m=f32(m, m, m))
 
 
+def test_min_p_that_cuts_nothing_behind_a_large_top_k():
+    """The min-p step then has nothing to do in any CTA of the row's cluster, and the next
+    step follows at once."""
+    x = logits(3, 60000, seed=21, sigma=1.5)
+    u = torch.rand(3, device="cuda", generator=_gen(21))
+    k, m = i32(1000, 4000, 9000), f32(1e-30, 1e-30, 1e-30)
+    token = check(x, u, k=k, m=m)
+    for _ in range(50):
+        assert q.sample(x, u, top_k=k, min_p=m)[0].tolist() == token
+    check(x, u, k=k, p=f32(.9, .99, .999), m=m)
+
+
 def test_ties_go_to_the_lowest_index():
     """Equal logits: the order is by index, the kept weights are exact, so is every border."""
     x = torch.zeros((4, 4096), device="cuda")

@@ -993,7 +993,11 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
           tell(skip ? kDone : kHistogram, 0);
         }
       }
-      if (heard() == kDone) continue;  // nothing to look for in this stage
+      if (heard() == kDone) {  // nothing to look for in this stage (and every thread knows it before the next order)
+        if (cluster > 1) cluster_sync();
+        else __syncthreads();
+        continue;
+      }
       for (int attempt = 0; attempt < 2; ++attempt) {
         const float hi = sh.hi, lo = sh.lo, ref = sh.ref, scale = sh.scale;
         auto step_of = [&](float x) { return min(kBins - 1, static_cast<int>(fminf(fmaxf((ref - x) * scale, 0.0f), 1e6f))); };
