@@ -405,8 +405,8 @@ qurl_status qurl_kv_cache_dequant(const void* cache, const float* scale, const i
  * (the slots of qurl_kv_cache_quant's slot_mapping), j < seq_lens[b], and, with
  * window > 0, j >= seq_lens[b] - window.  A sequence that sees no token (length
  * 0) gets out = 0 and lse = -inf.
- *   q            [B, ldq] bf16, the q_heads * head_dim query columns first (the
- *                fused qkv output itself may be passed).
+ *   q            [B, ldq] bf16, finite, the q_heads * head_dim query columns first
+ *                (the fused qkv output itself may be passed).
  *   caches       as in qurl_kv_cache_quant; head_dim a multiple of 16, at most 256.
  *   block_table  [B, ld_table] int32, max_blocks entries a row; only those that a
  *                sequence's tokens lie in are read.  block_size >= 1.
@@ -442,8 +442,10 @@ qurl_status qurl_kv_attn_decode(const void* q, int ldq, int B, int q_heads, int 
  *   n  = (Y * r_y) * gamma_post                  r_y as in qurl_rmsnorm_quant with eps_post; n = Y without gamma_post
  *   t  = n * gate                                t = n without gate
  *   H_out = bf16_RNE(H + t * residual_scale)     each product and the sum rounded to fp32
- *   v  = (H_out * r) * gamma_folded              then codes and scales as qurl_rmsnorm_quant(H_out) gives them,
- *                                                bit for bit (ms_out [M] fp32 or NULL, likewise)
+ *   v  = (H_out * r) * gamma_folded              then codes and scales as qurl_rmsnorm_quant(H_out) gives them
+ * ms (both norms', H_out's in ms_out [M] fp32 or NULL) by the rule of
+ * qurl_rmsnorm_quant, so equal to its unless the mean lies within ~2^-44 of a
+ * rounding midpoint; the codes and scales are bit for bit those of that ms.
  *   Y, H, H_out  [M, K] bf16, row strides ldy, ldh, ldo; H_out may be H (ldo == ldh).
  *   gamma_post   [K] fp32 or NULL (no norm behind the block).
  *   gate         bf16 rows, stride ldg elements; ldg = 0: one row [K] for every
@@ -493,7 +495,8 @@ qurl_status qurl_sample(const void* logits, qurl_ftype x_type, int B, int V, int
  * qurl_token_logprob_grad takes lse as the forward call wrote it; g is the
  * derivative by logp (qurl_acr_objective's dterm), denom a device double (its
  * stats + 1, the number of valid tokens) or NULL for 1; a denom that is not
- * positive gives zeros.  Sums are fp32.
+ * positive gives zeros.  Sums are fp32, and so are z and lse: z - lse, and with it a
+ * probability, carries about 2^-23 max |z| (large for a temperature far below 1).
  *   targets [T] int64: a negative one is padding (logp = lse = 0, a zero gradient
  *   row whatever lse and g hold); one >= V is treated the same and latches
  *   QURL_ERR_INVALID_ARG in the device status word.

@@ -12,6 +12,7 @@
 #include "internal.h"
 #include "objective.h"
 #include "qurl.h"
+#include "rollout.h"
 
 namespace qurl {
 std::atomic<unsigned long long> g_kernel_launches{0};

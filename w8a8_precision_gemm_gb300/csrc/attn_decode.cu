@@ -45,8 +45,8 @@
 
 #include <cstdint>
 
-#include "internal.h"
 #include "ptx.cuh"
+#include "rollout.h"
 
 namespace qurl {
 namespace {
@@ -122,6 +122,18 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, int* 
     }
   }
   return true;
+}
+
+// The same for MMAs that this thread has issued itself, whatever the status says:
+// none may still be writing TMEM when it is released.
+__device__ __forceinline__ void wait_drain(uint64_t* bar, uint32_t parity, int* status) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      atomicExch(status, kDevTimeout);
+      return;
+    }
+  }
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
@@ -532,8 +544,8 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<G, PANELS>::CTAS)
         }
       }
       if (ok && prev >= 0) ok = outputs(g - 1, prev);
-      umma_commit(&sh.drain);  // no MMA may still be writing TMEM when it is released
-      wait_phase(&sh.drain, 0, a.status);
+      umma_commit(&sh.drain);
+      wait_drain(&sh.drain, 0, a.status);
     }
     __syncwarp();
   } else {

@@ -9,7 +9,6 @@
 #include <atomic>
 #include <cstddef>
 #include <cstdint>
-#include <utility>
 
 namespace qurl {
 
@@ -126,10 +125,10 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
   return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
 }
 
-// launch_pdl for a kernel whose CTAs work in clusters of `cluster` (which divides grid.x).
+// launch_pdl for a kernel whose CTAs work in clusters of two (grid.x even).
 template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl_cluster(void (*kern)(KArgs...), int cluster, dim3 grid, dim3 block, size_t smem,
-                               cudaStream_t st, Args&&... args) {
+cudaError_t launch_pdl_pair(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                            Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
@@ -139,20 +138,13 @@ cudaError_t launch_pdl_cluster(void (*kern)(KArgs...), int cluster, dim3 grid, d
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.x = 2;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   g_kernel_launches.fetch_add(1, std::memory_order_relaxed);
   return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
-}
-
-// ... in clusters of two (grid.x even).
-template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl_pair(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                            Args&&... args) {
-  return launch_pdl_cluster(kern, 2, grid, block, smem, st, std::forward<Args>(args)...);
 }
 
 // quant.cu.  x16 (may be null): also write the INT8 codes as fp16 [M, K]
@@ -179,61 +171,6 @@ cudaError_t launch_kv_cache_quant(const void* QKV, int M, long long ldq, int q_d
 cudaError_t launch_kv_cache_dequant(const void* cache, const float* scale, const long long* slots, int n,
                                     int kv_heads, int head_dim, long long num_slots, void* out, int* status,
                                     cudaStream_t st);
-
-// attn_decode.cu: attention of one new token per sequence over the paged FP8 cache
-// (qurl_kv_attn_decode), and the workspace it needs.
-struct AttnArgs {
-  const __nv_bfloat16* q;
-  long long ldq;
-  int B, q_heads, kv_heads, head_dim;
-  const uint8_t* k_cache;
-  const float* k_scale;
-  const uint8_t* v_cache;
-  const float* v_scale;
-  long long num_slots;
-  const int* block_table;
-  long long ld_table;
-  int max_blocks, block_size;
-  const int* seq_lens;
-  int window;
-  float scale;
-  __nv_bfloat16* out;
-  long long ldo;
-  float* lse;  // null: not wanted
-  void* ws;
-  int* status;
-};
-size_t attn_workspace_bytes(int q_heads, int kv_heads, int head_dim, int num_sms);
-cudaError_t launch_kv_attn_decode(const AttnArgs& a, int num_sms, cudaStream_t st);
-// sample.cu: one token per row of logits from a given uniform number (qurl_sample).
-struct SampleArgs {
-  const void* logits;
-  int B, V;
-  long long ld;
-  const float* temperature;  // null: 1
-  const int* top_k;          // null: off
-  const float* top_p;        // null: off
-  const float* min_p;        // null: off
-  const float* u;
-  long long* token;
-  float* logp;       // null: not wanted
-  float* logp_kept;  // null: not wanted
-  int shift;         // ceil(log2 V) + 1, set by the launch
-  int* status;
-};
-cudaError_t launch_sample(const SampleArgs& a, bool f32, int num_sms, cudaStream_t st);
-// logprob.cu: log-probabilities of given tokens and the logits' gradient.
-cudaError_t launch_token_logprob(const void* X, bool f32, long long T, int V, long long ld, const long long* targets,
-                                 float inv_t, float* logp, float* lse, int num_sms, int* status, cudaStream_t st);
-cudaError_t launch_token_logprob_grad(const void* X, bool f32, long long T, int V, long long ld,
-                                      const long long* targets, float inv_t, const float* lse, const float* g,
-                                      float scale, const double* denom, void* dX, long long ldd, int num_sms,
-                                      int* status, cudaStream_t st);
-// residual.cu: residual update with the norms on both sides and the quantizer behind it.
-cudaError_t launch_residual_rmsnorm_quant(const void* Y, long long ldy, const float* gamma_post, float eps_post,
-                                          const void* gate, long long ldg, float rs, const void* H, long long ldh,
-                                          void* Hout, long long ldo, const float* gamma, float eps, int M, int K,
-                                          int qt, void* Xq, float* sx, float* ms_out, cudaStream_t st);
 
 // How one GEMM call is cut into CTAs.
 struct GemmPlan {

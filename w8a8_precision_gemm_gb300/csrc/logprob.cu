@@ -12,8 +12,8 @@
 
 #include <cstdint>
 
-#include "internal.h"
 #include "ptx.cuh"
+#include "rollout.h"
 
 namespace qurl {
 namespace {

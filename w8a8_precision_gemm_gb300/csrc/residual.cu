@@ -8,19 +8,26 @@
 //   codes, sx = per-token quantization of v
 //
 // Each product and sum is rounded to fp32 as written; r = 1 / sqrt(ms + eps)
-// with ms as in the RMSNorm quantizer.  The second half works on the stored
-// bf16 h', so its codes are bit for bit those of qurl_rmsnorm_quant(h').
+// with ms by the RMSNorm quantizer's rule (the sum of squares as an error-free
+// pair, the mean rounded once).  The second half works on the stored bf16 h', so
+// its codes are those of qurl_rmsnorm_quant(h') (where the two sums' 2^-44 round
+// to the same ms).
 //
-// Bound by HBM: 2 (y) + 2 (h) + 2 (h') + 1 (codes) bytes per value, against
-// 11 for the three passes (norm, update, norm and quantize) it stands for.  One
-// row per CTA, the row kept in registers from its only read to the codes.
+// Bytes: 2 (y) + 2 (h) + 2 (h') + 1 (codes) per value, against 13 for the three
+// passes (norm, update, norm and quantize) it stands for.  One row per CTA, the
+// row kept in registers from its only read to the codes.  8192 x 5120 FP8 with
+// both norms: 70 us, 4.2 TB/s, 0.62 of the copy rate; two dependent block
+// reductions a row (both means and the absmax are chains of barriers that loads of
+// other rows on the SM cover only in part) and the issue slots of about 60
+// instructions a value pair bound it.  64 x 5120 INT8: 10.6 us on the device, the
+// chain of one row.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
 
-#include "internal.h"
 #include "ptx.cuh"
+#include "rollout.h"
 #include "rowquant.cuh"
 
 namespace qurl {

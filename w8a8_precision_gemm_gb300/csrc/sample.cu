@@ -38,8 +38,8 @@
 #include <cfloat>
 #include <cstdint>
 
-#include "internal.h"
 #include "ptx.cuh"
+#include "rollout.h"
 
 namespace qurl {
 namespace {
