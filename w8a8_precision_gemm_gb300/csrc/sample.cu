@@ -338,7 +338,7 @@ struct Shared {
   u64 limit;       // places kept
   u64 scan_total;
   uint32_t top, low;  // ordered keys: largest logit, smallest
-  uint32_t cut;       // ordered key
+  float cuts[8];      // each CTA's estimate of the cut; -inf: none
   uint32_t n;         // first CTA: entries of the list
   uint32_t own_n, own_at;
   int order, bin;     // what to do next, and the step to collect
@@ -558,6 +558,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
                     min(steps, (s0 + (s1 - s0) * warp / kWarps) * per),
                     min(steps, (s0 + (s1 - s0) * (warp + 1) / kWarps) * per)};
   for (int i = tid; i < kTable; i += kThreads) sh.table[i] = g_exp2.v[i];
+  if (tid < 8) sh.cuts[tid] = -INFINITY;
   for (int i = tid; i < kBins; i += kThreads) {
     sh.count[i] = 0;
     sh.mass[i] = 0;
@@ -567,7 +568,6 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
   if (tid == 0) {
     sh.top = 0;
     sh.low = 0xFFFFFFFFu;
-    sh.cut = 0;
     sh.n = 0;
     sh.own_n = 0;
     sh.total = 0;
@@ -642,7 +642,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
   const bool truncated = has_k || has_m || has_p;
   const bool exact_total = !has_k && !has_m;
   // ---- the cut: of n logits above it, spread over t threads at random, t (1 - exp(-n / t)) threads hold one
-  // or more -- so the cut is where that many threads' largest logits lie above it
+  // or more -- so the cut is where that many threads' largest logits lie above it: the mean of the CTAs' estimates
+  // (their highest one would leave less than a top-k of 50 in a row cut into 8)
   if (truncated) {
     if (a.V > kShort) {
       if (own != -INFINITY) atomicAdd(&sh.count[bin_of(own)], 1u);
@@ -657,8 +658,9 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
       sh.count[2 * tid] = sh.count[2 * tid + 1] = 0;
       if (before < want && want <= before + c0 + c1) {
         const int at = 2 * tid + (want <= before + c0 ? 1 : 2);  // its step's lower edge
-        const uint32_t key = order_key(top - static_cast<float>(at) / fmaxf(binscale, 1e-30f));
-        for (int r = 0; r < cluster; ++r) remote_max32(remote(&sh.cut, r), key);
+        const float estimate = top - static_cast<float>(at) / fmaxf(binscale, 1e-30f);
+        for (int r = 0; r < cluster; ++r)
+          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote(&sh.cuts[rank], r)), "f"(estimate) : "memory");
       }
     }
     if (cluster > 1) cluster_sync();
@@ -680,7 +682,18 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
   };
 
   // ---- pass 2: the sum, the candidates, and (nothing cut off) the segments' sums
-  const float cut = sh.cut == 0 ? -INFINITY : key_value(sh.cut);
+  float cut = -INFINITY;
+  {
+    float sum = 0.0f;
+    int n = 0;
+    for (int r = 0; r < cluster; ++r) {
+      const float c = sh.cuts[r];
+      if (c == -INFINITY) continue;
+      sum += c;
+      ++n;
+    }
+    if (n > 0) cut = fminf(sum / static_cast<float>(n), top);
+  }
   {
     const uint32_t r_segs = remote(sh.segs, 0);
     u64 z = 0;
@@ -1238,9 +1251,12 @@ cudaError_t launch_sample(const SampleArgs& a_in, bool f32, int num_sms, cudaStr
   SampleArgs a = a_in;
   a.shift = 1;  // ceil(log2 V) + 1
   while ((1LL << (a.shift - 1)) < a.V) ++a.shift;
-  // CTAs a row: as many as two for every SM leave the batch, each with 2048 logits at least
+  // CTAs a row, each with 2048 logits at least: as many as fill the SMs' four places; twice that with a top-p or min-p,
+  // whose rows need very different work (256 x 131072, CTAs a row 2 | 4: rows of mixed limits 184 | 139 us, top-p 0.95
+  // at temperature 0.8 241 | 191, top-k 50 48 | 58, no limits 65 | 68)
+  const long long room = (a.top_p || a.min_p ? 8LL : 4LL) * num_sms;
   int cluster = 1;
-  while (cluster < 8 && static_cast<long long>(a.B) * cluster * 2 <= 4LL * num_sms && a.V / (cluster * 2) >= 2048) cluster *= 2;
+  while (cluster < 8 && static_cast<long long>(a.B) * cluster * 2 <= room && a.V / (cluster * 2) >= 2048) cluster *= 2;
   auto* kern = f32 ? sample_kernel<float> : sample_kernel<__nv_bfloat16>;
   static bool attr_done[64][2] = {};
   int dev = 0;
