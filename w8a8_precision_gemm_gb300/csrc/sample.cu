@@ -27,11 +27,12 @@
 // and sends the logits above the cut to the cluster's first CTA, which ranks
 // them against each other and draws -- all there is to do unless the kept set is
 // larger.  Then an eighth of the row says between which logits a limit falls; one
-// pass adds up what lies above and cuts the window into 512 steps of count and
-// weight (shared-memory atomics are what a histogram of the whole row would be
-// bound by), the logits of the one step that holds the limit are collected, a
-// radix select among them gives it, and a last pass gives every segment's kept
-// weight.  A limit outside its window is looked for in the whole row.
+// pass adds up what lies above that window and lists what lies in it, a few
+// percent of the row at most.  A thread then takes one of these each: 512 steps of
+// count and weight say in which step the limit falls, the logits of that step are
+// ranked against each other (a radix select where there are many), and every
+// segment's kept weight is known without another pass.  A limit outside its window
+// is looked for in the whole row.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -54,6 +55,7 @@ constexpr int kMaxSegs = 512;    // segments a row is cut into at most
 constexpr int kShort = 512;      // candidates ranked against each other
 constexpr int kAim = 128;        // candidates the cut aims at, more for a large top-k
 constexpr int kList = 1536;      // logits of one step collected for the radix select
+constexpr int kWindow = 4096;    // logits of a CTA in the window: their indices take the room of `list` and `w`
 constexpr int kBins = 512;
 constexpr u64 kAll = ~0ull;
 
@@ -341,6 +343,7 @@ struct Shared {
   float cuts[8];      // each CTA's estimate of the cut; -inf: none
   uint32_t n;         // first CTA: entries of the list
   uint32_t own_n, own_at;
+  uint32_t in_window;
   int order, bin;     // what to do next, and the step to collect
   float hi, lo, ref, scale;  // the window: logits above hi, those down to lo by (ref - x) scale
   u64 picked;
@@ -348,7 +351,8 @@ struct Shared {
   u64 above_count;
   u64 have;           // first CTA: weight of the candidates (0: they were too many)
   double drop;        // temperature ln(min_p)
-  float share;        // of the sample that lies before a limit
+  float before, behind;  // of the sample's measure: before a limit and behind it (negative: not known)
+  uint32_t sampled;      // logits of the sample (first CTA: of all CTAs)
   int found;
   int pick_lo, pick_hi;
   float sq[kWarps];
@@ -357,6 +361,8 @@ struct Shared {
   float chi, clo, c512;
   u64 found_before;
 };
+
+static_assert((kList + kShort) * sizeof(u64) == kWindow * sizeof(int), "the window's indices");
 
 __device__ __forceinline__ u64 warp_sum(u64 v) {
 #pragma unroll
@@ -571,6 +577,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
     sh.n = 0;
     sh.own_n = 0;
     sh.total = 0;
+    sh.sampled = 0;
     sh.token = 0x7FFFFFFF;
     // log2(e) / temperature as a pair
     constexpr double kLog2e = 1.4426950408889634074;
@@ -911,7 +918,9 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
       }
       __syncthreads();
     };
+    uint32_t sampled = 0;
     row.sample(steps >= 128 ? 8 : 1, [&](const float (&x)[N], int, int n) {
+      sampled += max(n, 0);
       u64 w[N];
       weights<B16>(x, w, s, sh.table);
 #pragma unroll
@@ -922,8 +931,12 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
         if (w[e]) add64(&sh.mass[k], w[e]);
       }
     });
+    sampled = __reduce_add_sync(0xFFFFFFFFu, sampled);
+    if ((tid & 31) == 0)
+      asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(remote(&sh.sampled, 0)), "r"(sampled) : "memory");
     gather(sh.sample_mass, sh.sample_count);
 
+    int* window = reinterpret_cast<int*>(sh.list);  // indices of the CTA's logits in the window
     // the limits in turn: top-k, the weight that min-p leaves, top-p
     u64 base = 0;
     int collected = -1;  // the step whose logits the list holds
@@ -944,55 +957,73 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
         } else {
           if (stage == 2 && exact_total) base = sh.total;
           target = stage == 0 ? static_cast<u64>(pr.top_k) : nucleus(pr.top_p, base);
-          // how far down the sample the target lies, give or take 4 sigma of what was counted to there
+          // Where the target may lie, by the sample's steps.  A sum over the sampled logits above a step's edge has
+          // the whole sum's share phi as its mean and less than the sum of their squares as its variance; so does
+          // the sum below the edge, which is the better one where a few large weights lie above.  An edge bounds the
+          // target when either sum says so by 4 sigma (a step's weights are nearly equal; four logits of the largest
+          // weight stand for what the sample may have missed).
           const bool ranked = sh.have != 0;
-          const u64 v0 = stage == 0 ? sh.sample_count[2 * tid] : sh.sample_mass[2 * tid];
-          const u64 v1 = stage == 0 ? sh.sample_count[2 * tid + 1] : sh.sample_mass[2 * tid + 1];
-          u64 all;
-          const u64 c = block_scan(v0 + v1, all, sh);
-          if (tid == 0) {
-            const double total = stage == 0    ? static_cast<double>(a.V)
-                                 : exact_total ? static_cast<double>(sh.total)
-                                               : static_cast<double>(sh.total) * 0x1p-32 *
-                                                     static_cast<double>(weight<B16>(top, s, sh.table));
-            const double known = !ranked ? 0.0 : static_cast<double>(stage == 0 ? sh.short_n : sh.have);
-            sh.share = static_cast<float>((static_cast<double>(target) - known) / fmax(total - known, 1.0));
-            sh.pick_lo = kBins;
-            sh.pick_hi = -1;
-          }
-          __syncthreads();
-          const float share = sh.share;
-          // the estimate's deviation: sqrt(f (1 - f) / n) for n equal weights; for unequal ones n is (sum w)^2 / sum w^2,
-          // taken by steps (a step's weights are nearly equal)
-          float sq = 0.0f;
+          u64 v[2];
+          float sq[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float n = static_cast<float>(sh.sample_count[2 * tid + e]);
-            const float w = static_cast<float>(e ? v1 : v0);
-            if (n > 0.0f) sq += w / n * w;
+            const uint32_t n = sh.sample_count[2 * tid + e];
+            v[e] = stage == 0 ? n : sh.sample_mass[2 * tid + e];
+            const float w = static_cast<float>(v[e]);
+            sq[e] = n > 0 ? w / static_cast<float>(n) * w : 0.0f;
           }
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) sq += __shfl_xor_sync(0xFFFFFFFFu, sq, o);
-          if ((tid & 31) == 0) sh.sq[warp] = sq;
-          __syncthreads();
-          sq = 0.0f;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) sq += sh.sq[w];
-          const float whole = static_cast<float>(all);
-          const float spread = 4.0f * sqrtf(fmaxf(share * (1.0f - share), 0.0f) * sq) + 0.002f * whole;  // (sq = whole^2 / n)
-          const float a0 = fmaxf(share * whole - spread, 0.0f), a1 = share * whole + spread;
-          if (share > 0.0f && all > 0) {
-            // the last pair of steps before a0 is reached, the first after a1
-            if (static_cast<float>(c) <= a0 && a0 <= static_cast<float>(c + v0 + v1)) atomicMax(&sh.pick_hi, 2 * tid);
-            if (static_cast<float>(c) < a1 && a1 <= static_cast<float>(c + v0 + v1)) atomicMin(&sh.pick_lo, 2 * tid + 2);
+          u64 all;
+          const u64 c = block_scan(v[0] + v[1], all, sh);
+          const float w_top = static_cast<float>(weight<B16>(top, s, sh.table));
+          if (tid == 0) {
+            const double total = exact_total ? static_cast<double>(sh.total)
+                                             : static_cast<double>(sh.total) * 0x1p-32 * static_cast<double>(w_top);
+            const double known = !ranked ? 0.0 : static_cast<double>(stage == 0 ? sh.short_n : sh.have);
+            const double phi = static_cast<double>(sh.sampled) / static_cast<double>(a.V);
+            sh.before = static_cast<float>((static_cast<double>(target) - known) * phi);
+            sh.behind = stage == 0 ? -1.0f : static_cast<float>((total - static_cast<double>(target)) * phi);
+            sh.pick_lo = kBins;
+            sh.pick_hi = 0;
           }
+          // squares above the thread's first step, and below its last
+          float up = sq[0] + sq[1], down = up;
+          const int lane = tid & 31;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const float x = __shfl_up_sync(0xFFFFFFFFu, up, o), y = __shfl_down_sync(0xFFFFFFFFu, down, o);
+            if (lane >= o) up += x;
+            if (lane + o < 32) down += y;
+          }
+          if (lane == 31) sh.sq[warp] = up;
+          up -= sq[0] + sq[1];
+          float after = __shfl_down_sync(0xFFFFFFFFu, down, 1);
+          if (lane == 31) after = 0.0f;
           __syncthreads();
-          if (share <= 0.0f && ranked) {  // among the candidates
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) up += sh.sq[w];
+            if (w > warp) after += sh.sq[w];
+          }
+          const float slack = 1e-4f * static_cast<float>(all), c1 = s.c512 * (1.0f / kTable);
+          const float most = stage == 0 ? 1.0f : ranked ? w_top * ex2((cut - top) * c1) : w_top;
+          auto edge_at = [&](int j, u64 above, float sq_above, float sq_below) {
+            const float least = stage == 0 ? 1.0f : w_top * ex2(-static_cast<float>(j) / fmaxf(binscale, 1e-30f) * c1);
+            const float over = static_cast<float>(above), below = static_cast<float>(all - above);
+            const float d0 = 4.0f * sqrtf(sq_above + 4.0f * most * most) + slack;
+            const float d1 = 4.0f * sqrtf(sq_below + 4.0f * least * least) + slack;
+            const bool known = sh.behind >= 0.0f;
+            if (over + d0 <= sh.before || (known && below - d1 >= sh.behind)) atomicMax(&sh.pick_hi, j);
+            if (over - d0 >= sh.before || (known && below + d1 <= sh.behind)) atomicMin(&sh.pick_lo, j);
+          };
+          edge_at(2 * tid, c, up, after + sq[0] + sq[1]);
+          edge_at(2 * tid + 1, c + v[0], up + sq[0], after + sq[1]);
+          __syncthreads();
+          if (sh.before <= 0.0f && ranked) {  // among the candidates
             lo = cut;
             scale = top > cut ? kBins / (top - cut) : 0.0f;
-          } else if (sh.pick_hi >= 0 && binscale > 0.0f) {
+          } else if (sh.pick_hi < sh.pick_lo && binscale > 0.0f) {
             if (sh.pick_hi > 0) hi = top - static_cast<float>(sh.pick_hi) / binscale;
-            else if (ranked) hi = cut;  // (the sample starts below the cut)
+            if (ranked) hi = fminf(hi, cut);  // (the sample starts below the cut)
             if (sh.pick_lo < kBins) lo = top - static_cast<float>(sh.pick_lo) / binscale;
             ref = fminf(hi, top);
             const float range = ref - fmaxf(lo, top - extent);
@@ -1015,28 +1046,41 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
         const float hi = sh.hi, lo = sh.lo, ref = sh.ref, scale = sh.scale;
         auto step_of = [&](float x) { return min(kBins - 1, static_cast<int>(fminf(fmaxf((ref - x) * scale, 0.0f), 1e6f))); };
         if (!first) clear();
+        if (tid == 0) sh.in_window = 0;
+        __syncthreads();
+        // what lies above the window is added up, what lies in it listed: few logits, which threads of their own
+        // then take one each
         u64 n_above = 0, w_above = 0;
         u64 v = 0;
         row.run(
-            [&](const float (&x)[N], int, int n) {
+            [&](const float (&x)[N], int i, int n) {
               float most = x[0];
 #pragma unroll
               for (int e = 1; e < N; ++e) most = fmaxf(most, x[e]);
-              if (!(most >= lo)) return;
-              u64 w[N];
-              weights<B16>(x, w, s, sh.table);
+              uint32_t in = 0;  // by element
+              if (most >= lo) {
+                u64 w[N];
+                weights<B16>(x, w, s, sh.table);
 #pragma unroll
-              for (int e = 0; e < N; ++e) {
-                v += x[e] > hi ? w[e] : 0;
-                n_above += x[e] > hi ? 1 : 0;
-              }
-#pragma unroll
-              for (int e = 0; e < N; ++e)
-                if (x[e] >= lo && x[e] <= hi && e < n) {
-                  const int k = step_of(x[e]);
-                  if (stage == 0) atomicAdd(&sh.count[k], 1u);
-                  if (w[e]) add64(&sh.mass[k], w[e]);
+                for (int e = 0; e < N; ++e) {
+                  v += x[e] > hi ? w[e] : 0;
+                  n_above += x[e] > hi ? 1 : 0;
+                  in |= x[e] >= lo && x[e] <= hi && e < n ? 1u << e : 0;
                 }
+              }
+              if (!__any_sync(0xFFFFFFFFu, in != 0)) return;
+              const int lane = tid & 31;
+              uint32_t at = __popc(in);
+#pragma unroll
+              for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t t = __shfl_up_sync(0xFFFFFFFFu, at, o);
+                if (lane >= o) at += t;
+              }
+              uint32_t from = 0;
+              if (lane == 31) from = atomicAdd(&sh.in_window, at);
+              at += __shfl_sync(0xFFFFFFFFu, from, 31) - __popc(in);
+              for (; in != 0; in &= in - 1, ++at)
+                if (at < kWindow) window[at] = i + __ffs(static_cast<int>(in)) - 1;
             },
             [&](int sg) {
               v = warp_sum(v);
@@ -1048,6 +1092,24 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
             });
         w_above = block_sum(w_above, sh);
         n_above = block_sum(n_above, sh);
+        const uint32_t n_window = sh.in_window;
+        const bool listed_all = n_window <= kWindow;  // (else this CTA reads its part again)
+        auto count_in = [&](float x) {
+          const int k = step_of(x);
+          const u64 w = weight<B16>(x, s, sh.table);
+          if (stage == 0) atomicAdd(&sh.count[k], 1u);
+          if (w) add64(&sh.mass[k], w);
+        };
+        if (listed_all) {
+#pragma unroll 4
+          for (uint32_t j = tid; j < n_window; j += kThreads) count_in(Load<T>::one(row.x + window[j]));
+        } else {
+          row.all([&](const float (&x)[N], int, int n) {
+#pragma unroll 1
+            for (int e = 0; e < min(n, N); ++e)
+              if (x[e] >= lo && x[e] <= hi) count_in(x[e]);
+          });
+        }
         if (tid == 0) {
           remote_add64(remote(&sh.above_mass, 0), w_above);
           remote_add64(remote(&sh.above_count, 0), n_above);
@@ -1093,38 +1155,30 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
         const int want = collected = sh.bin;
         if (want >= 0) {
           // the step's logits, and the segments' weight between the window's upper end and the step
-          u64 v = 0;
-          row.run(
-              [&](const float (&x)[N], int i, int n) {
-                float most = x[0];
-#pragma unroll
-                for (int e = 1; e < N; ++e) most = fmaxf(most, x[e]);
-                if (!(most >= lo)) return;
-                bool before_step = false;
-                int k[N];  // kBins: not in the window
-#pragma unroll
-                for (int e = 0; e < N; ++e) {
-                  k[e] = x[e] >= lo && x[e] <= hi && e < n ? step_of(x[e]) : kBins;
-                  before_step = before_step || k[e] < want;
-                }
-                if (before_step) {
-                  u64 w[N];
-                  weights<B16>(x, w, s, sh.table);
-#pragma unroll
-                  for (int e = 0; e < N; ++e) v += k[e] < want ? w[e] : 0;
-                }
-#pragma unroll
-                for (int e = 0; e < N; ++e)
-                  if (k[e] == want) {
-                    const uint32_t at = atomicAdd(&sh.own_n, 1u);
-                    if (at < kList) sh.own[at] = place(x[e], i + e);
-                  }
-              },
-              [&](int sg) {
-                v = warp_sum(v);
-                if ((tid & 31) == 0) sh.part_segs[sg] = v;
-                v = 0;
-              });
+          for (int sg = s0 + tid; sg < s1; sg += kThreads) sh.part_segs[sg] = 0;
+          __syncthreads();
+          auto sort_in = [&](float x, int i) {
+            const int k = step_of(x);
+            if (k < want) add64(&sh.part_segs[i / seg], weight<B16>(x, s, sh.table));
+            if (k == want) {
+              const uint32_t at = atomicAdd(&sh.own_n, 1u);
+              if (at < kList) sh.own[at] = place(x, i);
+            }
+          };
+          if (listed_all) {
+#pragma unroll 4
+            for (uint32_t j = tid; j < n_window; j += kThreads) {
+              const int i = window[j];
+              sort_in(Load<T>::one(row.x + i), i);
+            }
+          } else {
+            row.all([&](const float (&x)[N], int i, int n) {
+#pragma unroll 1
+              for (int e = 0; e < min(n, N); ++e)
+                if (x[e] >= lo && x[e] <= hi) sort_in(x[e], i + e);
+            });
+          }
+          if (cluster > 1) cluster_sync();  // the first CTA's window is read: `list` takes the step's logits
           send(kList);
         }
         if (cluster > 1) cluster_sync();
