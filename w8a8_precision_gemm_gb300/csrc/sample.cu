@@ -976,12 +976,13 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
           const u64 c = block_scan(v[0] + v[1], all, sh);
           const float w_top = static_cast<float>(weight<B16>(top, s, sh.table));
           if (tid == 0) {
-            const double total = exact_total ? static_cast<double>(sh.total)
-                                             : static_cast<double>(sh.total) * 0x1p-32 * static_cast<double>(w_top);
-            const double known = !ranked ? 0.0 : static_cast<double>(stage == 0 ? sh.short_n : sh.have);
-            const double phi = static_cast<double>(sh.sampled) / static_cast<double>(a.V);
-            sh.before = static_cast<float>((static_cast<double>(target) - known) * phi);
-            sh.behind = stage == 0 ? -1.0f : static_cast<float>((total - static_cast<double>(target)) * phi);
+            const u64 known = !ranked ? 0 : stage == 0 ? sh.short_n : sh.have;
+            const float phi = static_cast<float>(sh.sampled) / static_cast<float>(a.V);
+            sh.before = target > known ? static_cast<float>(target - known) * phi : 0.0f;
+            // (a row's fp32 sum is in units of the largest weight)
+            const float behind = exact_total ? static_cast<float>(sh.total - target)
+                                             : static_cast<float>(sh.total) * 0x1p-32f * w_top - static_cast<float>(target);
+            sh.behind = stage == 0 ? -1.0f : fmaxf(behind, 0.0f) * phi;
             sh.pick_lo = kBins;
             sh.pick_hi = 0;
           }
@@ -1006,17 +1007,24 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
           }
           const float slack = 1e-4f * static_cast<float>(all), c1 = s.c512 * (1.0f / kTable);
           const float most = stage == 0 ? 1.0f : ranked ? w_top * ex2((cut - top) * c1) : w_top;
+          int pick_hi = 0, pick_lo = kBins;
           auto edge_at = [&](int j, u64 above, float sq_above, float sq_below) {
             const float least = stage == 0 ? 1.0f : w_top * ex2(-static_cast<float>(j) / fmaxf(binscale, 1e-30f) * c1);
             const float over = static_cast<float>(above), below = static_cast<float>(all - above);
             const float d0 = 4.0f * sqrtf(sq_above + 4.0f * most * most) + slack;
             const float d1 = 4.0f * sqrtf(sq_below + 4.0f * least * least) + slack;
             const bool known = sh.behind >= 0.0f;
-            if (over + d0 <= sh.before || (known && below - d1 >= sh.behind)) atomicMax(&sh.pick_hi, j);
-            if (over - d0 >= sh.before || (known && below + d1 <= sh.behind)) atomicMin(&sh.pick_lo, j);
+            if (over + d0 <= sh.before || (known && below - d1 >= sh.behind)) pick_hi = max(pick_hi, j);
+            if (over - d0 >= sh.before || (known && below + d1 <= sh.behind)) pick_lo = min(pick_lo, j);
           };
           edge_at(2 * tid, c, up, after + sq[0] + sq[1]);
           edge_at(2 * tid + 1, c + v[0], up + sq[0], after + sq[1]);
+          pick_hi = __reduce_max_sync(0xFFFFFFFFu, pick_hi);
+          pick_lo = __reduce_min_sync(0xFFFFFFFFu, pick_lo);
+          if (lane == 0) {
+            atomicMax(&sh.pick_hi, pick_hi);
+            atomicMin(&sh.pick_lo, pick_lo);
+          }
           __syncthreads();
           if (sh.before <= 0.0f && ranked) {  // among the candidates
             lo = cut;
@@ -1306,11 +1314,14 @@ cudaError_t launch_sample(const SampleArgs& a_in, bool f32, int num_sms, cudaStr
   a.shift = 1;  // ceil(log2 V) + 1
   while ((1LL << (a.shift - 1)) < a.V) ++a.shift;
   // CTAs a row, each with 2048 logits at least: as many as fill the SMs' four places; twice that with a top-p or min-p,
-  // whose rows need very different work (256 x 131072, CTAs a row 2 | 4: rows of mixed limits 184 | 139 us, top-p 0.95
-  // at temperature 0.8 241 | 191, top-k 50 48 | 58, no limits 65 | 68)
-  const long long room = (a.top_p || a.min_p ? 8LL : 4LL) * num_sms;
+  // whose rows need very different work, and parts of 2^16 logits at most, whose windows fit the list (256 x 131072,
+  // us at 1 | 2 | 4 CTAs a row: rows of mixed limits 251 | 135 | 113, top-p 0.95 at temperature 0.8 194 | 167 | 154,
+  // at 1 361 | 184 | 194, top-k 50 46 | 48 | 57, no limits 68 | 64 | 68)
+  const bool uneven = a.top_p || a.min_p;
   int cluster = 1;
-  while (cluster < 8 && static_cast<long long>(a.B) * cluster * 2 <= room && a.V / (cluster * 2) >= 2048) cluster *= 2;
+  while (cluster < 8 && a.V / (cluster * 2) >= 2048 &&
+         (static_cast<long long>(a.B) * cluster * 2 <= (uneven ? 8LL : 4LL) * num_sms || (uneven && a.V / cluster > 65536)))
+    cluster *= 2;
   auto* kern = f32 ? sample_kernel<float> : sample_kernel<__nv_bfloat16>;
   static bool attr_done[64][2] = {};
   int dev = 0;
