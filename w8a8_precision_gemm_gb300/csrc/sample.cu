@@ -21,6 +21,12 @@
 // a whole row only where the choice needs the whole sum (no top-k, no min-p);
 // elsewhere the row's sum, which only logp needs, is a plain fp32 one.
 //
+// 256 rows of 131072 bf16 logits (67 MB, 9.9 us at the copy rate): no limits 64 us
+// (12 the first reading, 21 the exact weights), top-k 50 48, greedy 43, rows of mixed
+// limits 111, top-p 0.95 at temperature 0.6 | 1.0: 110 | 192 (in a wave of 152 rows 13
+// us for the exact sum, 21 for what lies above the window, 25 for what one CTA does
+// between the passes).  One row of 32000: 13 us, the chain of passes.
+//
 // A row is worked on by a cluster of 1 to 8 CTAs, as many as fill the GPU with
 // the batch.  Pass 1 takes the maximum; the threads' own maxima give a cut above
 // which about 128 logits lie.  Pass 2 (the row now comes from L2) takes the sum
