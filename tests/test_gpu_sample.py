@@ -265,3 +265,22 @@ def test_rows_behind_the_batch_and_optional_outputs():
         q.sample(x, u[:2])
     with pytest.raises(ValueError):
         q.sample(x.half(), u)
+
+
+@pytest.mark.parametrize("B", [4096, 4097])
+def test_large_batches_of_differing_rows(B):
+    """Batches of several waves, whose rows are taken in an order of their own up to 4096 rows."""
+    g = _gen(B)
+    r = torch.rand((4, B), device="cuda", generator=g)
+    x = logits(B, 700, seed=B)
+    u, t = r[0], torch.where(r[1] < .1, torch.zeros_like(r[1]), 0.5 + r[1])
+    k = torch.where(r[2] < .4, 0, (r[2] * 600).int()).int()
+    p, m = torch.where(r[3] < .3, torch.ones_like(r[3]), r[3]), torch.where(r[0] < .5, torch.zeros_like(u), r[1] * .01)
+    token, logp, kept = q.sample(x, u, t, k, p, m, want_kept=True)
+    some = torch.randperm(B, generator=torch.Generator().manual_seed(B))[:200].cuda()
+    y = torch.empty((200, 704), dtype=x.dtype, device="cuda")[:, :700]
+    y.copy_(x[some])
+    got = q.sample(y, u[some], t[some], k[some], p[some], m[some], want_kept=True)  # (one wave)
+    for a, b in zip((token, logp, kept), got):
+        assert torch.equal(a[some], b)
+    check(y, u[some], t[some], k[some], p[some], m[some])

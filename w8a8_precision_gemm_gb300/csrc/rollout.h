@@ -75,6 +75,7 @@ struct SampleArgs {
   float* logp;       // null: not wanted
   float* logp_kept;  // null: not wanted
   int shift;         // ceil(log2 V) + 1, set by the launch
+  bool order;        // rows that may take long first, set by the launch
   int* status;
 };
 cudaError_t launch_sample(const SampleArgs& a, bool f32, int num_sms, cudaStream_t st);

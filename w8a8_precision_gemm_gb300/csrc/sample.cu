@@ -23,7 +23,7 @@
 //
 // 256 rows of 131072 bf16 logits (67 MB, 9.9 us at the copy rate): no limits 64 us
 // (12 the first reading, 21 the exact weights), top-k 50 48, greedy 43, rows of mixed
-// limits 111, top-p 0.95 at temperature 0.6 | 1.0: 110 | 192 (in a wave of 152 rows 13
+// limits 98, top-p 0.95 at temperature 0.6 | 1.0: 113 | 196 (in a wave of 152 rows 13
 // us for the exact sum, 21 for what lies above the window, 25 for what one CTA does
 // between the passes).  One row of 32000: 13 us, the chain of passes.
 //
@@ -511,6 +511,30 @@ __device__ __forceinline__ Params params_of(const SampleArgs& a, int b) {
   return p;
 }
 
+// A row whose kept set may be larger than what is ranked on chip: three readings or more instead of two.
+__device__ __forceinline__ bool may_be_long(const SampleArgs& a, int b) {
+  const Params p = params_of(a, b);
+  return p.top_k > kShort / 2 || (p.top_k == 0 && (p.top_p < 1.0f || p.min_p > 0.0f));
+}
+
+// The row that the n-th cluster of the grid takes when those rows go first: a
+// long row that starts in the last wave is what the call would end on.
+__device__ int row_at(const SampleArgs& a, int n, Shared& sh) {
+  const int per = (a.B - 1) / kThreads + 1, r0 = min(a.B, static_cast<int>(threadIdx.x) * per), r1 = min(a.B, r0 + per);
+  int longs = 0;
+  for (int r = r0; r < r1; ++r) longs += may_be_long(a, r);
+  u64 all;
+  const int l = static_cast<int>(block_scan(static_cast<u64>(longs), all, sh));
+  const bool want = n < static_cast<int>(all);  // one of the long rows
+  const int at = want ? n : n - static_cast<int>(all);
+  int before = want ? l : r0 - l;
+  if (before <= at && at < before + (want ? longs : r1 - r0 - longs))
+    for (int r = r0; r < r1; ++r)
+      if (may_be_long(a, r) == want && before++ == at) sh.found = r;
+  __syncthreads();
+  return sh.found;
+}
+
 // floor(f * v) for f in [0, 1); `rest`: whether something was cut off.
 __device__ __forceinline__ u64 fraction(float f, u64 v, bool& rest) {
   const uint32_t b = __float_as_uint(f);
@@ -555,7 +579,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
   griddep_wait();
   griddep_launch_dependents();
   const int tid = threadIdx.x;
-  const int b = blockIdx.x / cluster;
+  int b = blockIdx.x / cluster;
+  if (a.order) b = row_at(a, b, sh);
   const uint32_t rank = cluster_ctarank();
   const bool first = rank == 0;
   const Params pr = params_of(a, b);
@@ -1320,14 +1345,18 @@ cudaError_t launch_sample(const SampleArgs& a_in, bool f32, int num_sms, cudaStr
   a.shift = 1;  // ceil(log2 V) + 1
   while ((1LL << (a.shift - 1)) < a.V) ++a.shift;
   // CTAs a row, each with 2048 logits at least: as many as fill the SMs' four places; twice that with a top-p or min-p,
-  // whose rows need very different work, and parts of 2^16 logits at most, whose windows fit the list (256 x 131072,
-  // us at 1 | 2 | 4 CTAs a row: rows of mixed limits 251 | 135 | 113, top-p 0.95 at temperature 0.8 194 | 167 | 154,
-  // at 1 361 | 184 | 194, top-k 50 46 | 48 | 57, no limits 68 | 64 | 68)
+  // whose rows need very different work, and parts of 40960 logits at most, whose windows fit the list (us at 1 | 2 |
+  // 4 | 8 CTAs a row: 256 x 131072, mixed limits 230 | 134 | 98 | 109, top-p 0.95 at temperature 0.8 194 | 168 | 154 |
+  // 185, top-k 50 46 | 48 | 57 | 83, no limits 68 | 66 | 68 | 80; mixed limits, 128 x 131072 147 | 113 | 92 | 76, 512 x
+  // 32000 121 | 84 | 109 | 178, 700 x 50257 133 | 114 | 160 | 265)
   const bool uneven = a.top_p || a.min_p;
   int cluster = 1;
   while (cluster < 8 && a.V / (cluster * 2) >= 2048 &&
-         (static_cast<long long>(a.B) * cluster * 2 <= (uneven ? 8LL : 4LL) * num_sms || (uneven && a.V / cluster > 65536)))
+         (static_cast<long long>(a.B) * cluster * 2 <= (uneven ? 8LL : 4LL) * num_sms || (uneven && a.V / cluster > 40960)))
     cluster *= 2;
+  // more rows than fit at once: those that may be long first (256 x 131072, mixed limits: 98 us, 111 in row order; the
+  // look at every row's parameters costs a CTA about a microsecond at 256 rows)
+  a.order = uneven && static_cast<long long>(a.B) * cluster > 4LL * num_sms && a.B <= 4096;
   auto* kern = f32 ? sample_kernel<float> : sample_kernel<__nv_bfloat16>;
   static bool attr_done[64][2] = {};
   int dev = 0;
