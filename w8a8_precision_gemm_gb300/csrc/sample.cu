@@ -1346,7 +1346,7 @@ cudaError_t launch_sample(const SampleArgs& a_in, bool f32, int num_sms, cudaStr
   while ((1LL << (a.shift - 1)) < a.V) ++a.shift;
   // CTAs a row, each with 2048 logits at least: as many as fill the SMs' four places; twice that with a top-p or min-p,
   // whose rows need very different work, and parts of 40960 logits at most, whose windows fit the list (us at 1 | 2 |
-  // 4 | 8 CTAs a row: 256 x 131072, mixed limits 230 | 134 | 98 | 109, top-p 0.95 at temperature 0.8 194 | 168 | 154 |
+  // 4 | 8 CTAs a row: 256 x 131072, mixed limits 251 | 134 | 98 | 109, top-p 0.95 at temperature 0.8 194 | 168 | 154 |
   // 185, top-k 50 46 | 48 | 57 | 83, no limits 68 | 66 | 68 | 80; mixed limits, 128 x 131072 147 | 113 | 92 | 76, 512 x
   // 32000 121 | 84 | 109 | 178, 700 x 50257 133 | 114 | 160 | 265)
   const bool uneven = a.top_p || a.min_p;
