@@ -863,9 +863,12 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
           }
         }
       };
-      rank(0);
-      if (n > kThreads) rank(1);
       const u64 ranked = block_sum(w[0] + w[1], sh);
+      const bool too_few = exact_total && n < a.V && ranked < nucleus(pr.top_p, sh.total);  // (only a top-p limits)
+      if (!too_few) {
+        rank(0);
+        if (n > kThreads) rank(1);
+      }
       if (tid == 0) {
         sh.have = ranked;
         sh.short_n = static_cast<uint32_t>(n);
@@ -884,7 +887,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
       } else if (inside) {
         base = block_sum((in[0] ? w[0] : 0) + (in[1] ? w[1] : 0), sh);
       }
-      if (inside) {
+      if (inside && !too_few) {
         const u64 target = has_p ? nucleus(pr.top_p, base) : kAll;
         const u64 have = exact_total ? ranked : base;
         if (!has_p || have >= target || n == a.V) {
