@@ -23,7 +23,7 @@
 //
 // 256 rows of 131072 bf16 logits (67 MB, 9.9 us at the copy rate): no limits 64 us
 // (12 the first reading, 21 the exact weights), top-k 50 48, greedy 43, rows of mixed
-// limits 98, top-p 0.95 at temperature 0.6 | 1.0: 113 | 196 (in a wave of 152 rows 13
+// limits 96, top-p 0.95 at temperature 0.6 | 1.0: 112 | 189 (in a wave of 152 rows 13
 // us for the exact sum, 21 for what lies above the window, 25 for what one CTA does
 // between the passes).  One row of 32000: 13 us, the chain of passes.
 //
@@ -864,8 +864,11 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
         }
       };
       const u64 ranked = block_sum(w[0] + w[1], sh);
-      const bool too_few = exact_total && n < a.V && ranked < nucleus(pr.top_p, sh.total);  // (only a top-p limits)
-      if (!too_few) {
+      // the set that top-k and min-p leave, if it lies above the cut; a top-p alone: of the whole row
+      const u64 lowest = cut == -INFINITY ? kAll : (static_cast<u64>(~order_key(cut)) << 32) | 0xFFFFFFFFull;
+      const bool inside = n == a.V || (exact_total ? ranked >= nucleus(pr.top_p, sh.total)
+                                                   : (has_k && n >= pr.top_k) || (has_m && edge <= lowest));
+      if (inside) {
         rank(0);
         if (n > kThreads) rank(1);
       }
@@ -873,21 +876,12 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
         sh.have = ranked;
         sh.short_n = static_cast<uint32_t>(n);
       }
-      // the set that top-k and min-p leave, if it lies above the cut
-      const u64 lowest = cut == -INFINITY ? kAll : (static_cast<u64>(~order_key(cut)) << 32) | 0xFFFFFFFFull;
-      bool inside = (has_k && n >= pr.top_k) || (has_m && edge <= lowest) || n == a.V;
       bool in[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e)
         in[e] = tid + e * kThreads < n && (!has_k || cnt[e] < static_cast<uint32_t>(pr.top_k)) && p[e] <= edge;
-      u64 base = 0;
-      if (exact_total) {
-        base = sh.total;
-        inside = true;
-      } else if (inside) {
-        base = block_sum((in[0] ? w[0] : 0) + (in[1] ? w[1] : 0), sh);
-      }
-      if (inside && !too_few) {
+      if (inside) {
+        const u64 base = exact_total ? sh.total : block_sum((in[0] ? w[0] : 0) + (in[1] ? w[1] : 0), sh);
         const u64 target = has_p ? nucleus(pr.top_p, base) : kAll;
         const u64 have = exact_total ? ranked : base;
         if (!has_p || have >= target || n == a.V) {
