@@ -21,11 +21,12 @@
 // a whole row only where the choice needs the whole sum (no top-k, no min-p);
 // elsewhere the row's sum, which only logp needs, is a plain fp32 one.
 //
-// 256 rows of 131072 bf16 logits (67 MB, 9.9 us at the copy rate): no limits 64 us
-// (12 the first reading, 21 the exact weights), top-k 50 48, greedy 43, rows of mixed
-// limits 96, top-p 0.95 at temperature 0.6 | 1.0: 112 | 189 (in a wave of 152 rows 13
+// 256 rows of 131072 bf16 logits (67 MB, 9.9 us at the copy rate): no limits 60 us
+// (12 the first reading, 20 the exact weights), top-k 50 48, greedy 43, rows of mixed
+// limits 93, top-p 0.95 at temperature 0.6 | 1.0: 109 | 184 (in a wave of 152 rows 13
 // us for the exact sum, 21 for what lies above the window, 25 for what one CTA does
-// between the passes).  One row of 32000: 13 us, the chain of passes.
+// between the passes).  One row of 32000: 15 us, 31 where the nucleus is large, the
+// chain of passes.
 //
 // A row is worked on by a cluster of 1 to 8 CTAs, as many as fill the GPU with
 // the batch.  Pass 1 takes the maximum; the threads' own maxima give a cut above
@@ -256,11 +257,15 @@ struct Part {
   template <typename F, typename E>
   __device__ __forceinline__ void run(F&& f, E&& end) const {
     uint4 a = load(t0), b = load(t0 + 1);
+    int sg = t0 / per, left = per;
 #pragma unroll 1
     for (int t = t0; t < t1; ++t) {
       const uint4 c = load(t + 2);
       step(t, a, f);
-      if ((t + 1) % per == 0 || t + 1 == t1) end(t / per);
+      if (--left == 0 || t + 1 == t1) {
+        end(sg++);
+        left = per;
+      }
       a = b;
       b = c;
     }
