@@ -19,8 +19,8 @@
 // both norms: 70 us, 4.2 TB/s, 0.62 of the copy rate; two dependent block
 // reductions a row (both means and the absmax are chains of barriers that loads of
 // other rows on the SM cover only in part) and the issue slots of about 60
-// instructions a value pair bound it.  64 x 5120 INT8: 10.6 us on the device, the
-// chain of one row.
+// instructions a value pair bound it.  64 x 5120 INT8, one call after the other in a
+// graph: 4.0 us, the chain of one row (qurl_rmsnorm_quant alone 4.0).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -35,8 +35,9 @@ namespace {
 
 using namespace rq;
 
+constexpr int kSms = 152;      // of the GPU
 constexpr int kNC = 8;        // 16-byte vectors cached per thread
-constexpr int kThreads = 512;  // most threads of a row CTA
+constexpr int kThreads = 512;  // threads of a long row
 
 struct ResidualArgs {
   const __nv_bfloat16* Y;
@@ -236,14 +237,18 @@ cudaError_t launch_residual_rmsnorm_quant(const void* Y, long long ldy, const fl
   a.ms_out = ms_out;
   const int nvec = K / 8;
   auto threads = [&](int nc) { return dim3(static_cast<unsigned>(((nvec + nc - 1) / nc + 31) / 32 * 32)); };
-  // Few rows (less than two an SM): a vector a thread, the shortest chain.  Else
+  // Few rows, all of them at once on the GPU (two an SM, or one of more than 640
+  // vectors): a vector a thread, the shortest chain; 256 rows of 5120 | 8192: 5.0 |
+  // 9.3 us this way, 7.2 | 7.3 the other (8192 is past one row an SM).  Else
   // four vectors a thread: fewer warps wait at each reduction.  8192 x 5120 (FP8,
   // both norms), us at resident CTAs: 1 vector 116 (2), 108 (3); 2 vectors 90 (3),
   // 80 (4); 3 vectors 73 (5); 4 vectors 73 (5), 71 (6), 70 (7), 75 (8); 5 vectors
   // 72 (6), 70 (8).  Persistent CTAs that load the next row into the registers the
   // current one leaves free measured 85 or more: the registers cost more
   // resident rows than the early loads gain.
-  if (M < 304 && nvec <= 1024)
+  if (M <= 2 * kSms && nvec <= 640)
+    return launch_pdl(residual_rmsnorm_quant_kernel<1, true, 640, 2>, dim3(M), threads(1), 0, st, a);
+  if (M <= kSms && nvec <= 1024)
     return launch_pdl(residual_rmsnorm_quant_kernel<1, true, 1024, 1>, dim3(M), threads(1), 0, st, a);
   if (nvec <= 4 * 160) return launch_pdl(residual_rmsnorm_quant_kernel<4, true, 160, 7>, dim3(M), threads(4), 0, st, a);
   if (nvec <= 4 * 256) return launch_pdl(residual_rmsnorm_quant_kernel<4, true, 256, 4>, dim3(M), threads(4), 0, st, a);
