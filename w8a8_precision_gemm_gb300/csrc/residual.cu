@@ -18,8 +18,8 @@
 // row kept in registers from its only read to the codes.  8192 x 5120 FP8 with
 // both norms: 70 us, 4.2 TB/s, 0.62 of the copy rate; two dependent block
 // reductions a row (both means and the absmax are chains of barriers that loads of
-// other rows on the SM cover only in part) and the issue slots of about 60
-// instructions a value pair bound it.  64 x 5120 INT8, one call after the other in a
+// other rows on the SM cover only in part) and the issue slots (84
+// instructions a pair of values, 63% of them taken) bound it.  64 x 5120 INT8, one call after the other in a
 // graph: 4.0 us, the chain of one row (qurl_rmsnorm_quant alone 4.0).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -238,8 +238,8 @@ cudaError_t launch_residual_rmsnorm_quant(const void* Y, long long ldy, const fl
   const int nvec = K / 8;
   auto threads = [&](int nc) { return dim3(static_cast<unsigned>(((nvec + nc - 1) / nc + 31) / 32 * 32)); };
   // Few rows, all of them at once on the GPU (two an SM, or one of more than 640
-  // vectors): a vector a thread, the shortest chain; 256 rows of 5120 | 8192: 5.0 |
-  // 9.3 us this way, 7.2 | 7.3 the other (8192 is past one row an SM).  Else
+  // vectors): a vector a thread, the shortest chain; 304 rows of 5120 5.0 us, 7.2 the
+  // other way; 256 of 8192, past one row an SM, 9.3 and 7.3.  Else
   // four vectors a thread: fewer warps wait at each reduction.  8192 x 5120 (FP8,
   // both norms), us at resident CTAs: 1 vector 116 (2), 108 (3); 2 vectors 90 (3),
   // 80 (4); 3 vectors 73 (5); 4 vectors 73 (5), 71 (6), 70 (7), 75 (8); 5 vectors
