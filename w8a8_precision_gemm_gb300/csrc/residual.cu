@@ -243,7 +243,8 @@ cudaError_t launch_residual_rmsnorm_quant(const void* Y, long long ldy, const fl
   // four vectors a thread: fewer warps wait at each reduction.  8192 x 5120 (FP8,
   // both norms), us at resident CTAs: 1 vector 116 (2), 108 (3); 2 vectors 90 (3),
   // 80 (4); 3 vectors 73 (5); 4 vectors 73 (5), 71 (6), 70 (7), 75 (8); 5 vectors
-  // 72 (6), 70 (8).  Persistent CTAs that load the next row into the registers the
+  // 72 (6), 70 (8).  8192 x 8192 (103 us, 78 without the norm behind the block; 69 at the
+  // copy rate): 4 vectors 118 (3), 103 (4), 109 (5); 5 vectors 105 (4), 112 (5).  Persistent CTAs that load the next row into the registers the
   // current one leaves free measured 85 or more: the registers cost more
   // resident rows than the early loads gain.
   if (M <= 2 * kSms && nvec <= 640)
