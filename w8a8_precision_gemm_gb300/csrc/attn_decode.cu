@@ -40,8 +40,8 @@
 // launch, the same result every run.
 //
 // Measured, 40 query heads over 8 KV heads of 128: 64 sequences of 256 to 8192
-// tokens (about 590 MB) 116 to 119 us, 5.0 TB/s; 4 of 98 k to 131 k tokens (1.0 GB)
-// 172 to 176 us, 5.8 TB/s, 0.85 of the copy rate.  The first tiles are there after 5 us,
+// tokens (about 590 MB) 110 to 119 us, 5.2 TB/s; 4 of 98 k to 131 k tokens (1.0 GB)
+// 169 to 180 us, 5.8 TB/s, 0.85 of the copy rate.  The first tiles are there after 5 us,
 // then the cache streams at 6.3 TB/s; equal units end up to 13 us apart (whoever ends
 // first leaves its share of HBM to the others), the joins take 4 to 5 us more.  One
 // sequence of 300 tokens, 28 heads over 4: 10.6 us.

@@ -23,9 +23,9 @@
 //
 // 256 rows of 131072 bf16 logits (67 MB, 9.9 us at the copy rate): no limits 60 us
 // (12 the first reading, 20 the exact weights), top-k 50 48, greedy 43, rows of mixed
-// limits 93, top-p 0.95 at temperature 0.6 | 1.0: 109 | 184 (in a wave of 152 rows 13
+// limits 93, top-p 0.95 at temperature 0.6 | 1.0: 108 | 182 (in a wave of 152 rows 13
 // us for the exact sum, 21 for what lies above the window, 25 for what one CTA does
-// between the passes).  One row of 32000: 15 us, 31 where the nucleus is large, the
+// between the passes).  One row of 32000: 14 us, 29 where the nucleus is large, the
 // chain of passes.
 //
 // A row is worked on by a cluster of 1 to 8 CTAs, as many as fill the GPU with
@@ -647,12 +647,9 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
     m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
     lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
   }
-  if ((tid & 31) == 0) {
-    const uint32_t km = order_key(m), kl = order_key(lo);
-    for (int r = 0; r < cluster; ++r) {
-      remote_max32(remote(&sh.top, r), km);
-      remote_min32(remote(&sh.low, r), kl);
-    }
+  if ((tid & 31) < cluster) {  // a lane for each CTA
+    remote_max32(remote(&sh.top, tid & 31), order_key(m));
+    remote_min32(remote(&sh.low, tid & 31), order_key(lo));
   }
   if (cluster > 1) cluster_sync();
   else __syncthreads();
@@ -808,20 +805,18 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
     if (static_cast<double>(f) < e) f = nextafterf(f, INFINITY);
     edge = (static_cast<u64>(~order_key(clean(f))) << 32) | 0xFFFFFFFFull;
   }
-  auto tell = [&](int order, int bin) {  // thread 0 of the first CTA
-    for (int r = 0; r < cluster; ++r) {
-      asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(remote(&sh.order, r)), "r"(order) : "memory");
-      asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(remote(&sh.bin, r)), "r"(bin) : "memory");
-      remote_put64(remote(&sh.limit, r), limit);
-    }
+  auto tell = [&](int order, int bin) {  // the first CTA, a thread for each of the cluster's
+    if (tid >= cluster) return;
+    asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(remote(&sh.order, tid)), "r"(order) : "memory");
+    asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(remote(&sh.bin, tid)), "r"(bin) : "memory");
+    remote_put64(remote(&sh.limit, tid), limit);
   };
   auto tell_window = [&](float hi, float lo, float ref, float scale) {  // likewise
-    for (int r = 0; r < cluster; ++r) {
-      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote(&sh.hi, r)), "f"(hi) : "memory");
-      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote(&sh.lo, r)), "f"(lo) : "memory");
-      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote(&sh.ref, r)), "f"(ref) : "memory");
-      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote(&sh.scale, r)), "f"(scale) : "memory");
-    }
+    if (tid >= cluster) return;
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote(&sh.hi, tid)), "f"(hi) : "memory");
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote(&sh.lo, tid)), "f"(lo) : "memory");
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote(&sh.ref, tid)), "f"(ref) : "memory");
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote(&sh.scale, tid)), "f"(scale) : "memory");
   };
   auto heard = [&] {  // every CTA: the first one's order
     if (cluster > 1) cluster_sync();
@@ -919,7 +914,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
     } else if (!truncated) {
       mass = sh.total;
     }
-    if (tid == 0) tell(next, n <= kShort ? 1 : 0);
+    tell(next, n <= kShort ? 1 : 0);
   }
   int order = heard();
 
@@ -1074,9 +1069,9 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
         if (tid == 0) {
           sh.above_mass = 0;
           sh.above_count = 0;
-          if (!skip) tell_window(hi, lo, ref, scale);
-          tell(skip ? kDone : kHistogram, 0);
         }
+        if (!skip) tell_window(hi, lo, ref, scale);
+        tell(skip ? kDone : kHistogram, 0);
       }
       if (heard() == kDone) {  // nothing to look for in this stage (and every thread knows it before the next order)
         if (cluster > 1) cluster_sync();
@@ -1187,10 +1182,10 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
             if (again) {
               sh.above_mass = 0;
               sh.above_count = 0;
-              tell_window(INFINITY, -INFINITY, top, binscale);
             }
-            tell(again ? kHistogram : kCollect, step);
           }
+          if (again) tell_window(INFINITY, -INFINITY, top, binscale);
+          tell(again ? kHistogram : kCollect, step);
         }
         if (heard() == kHistogram) continue;
         const int want = collected = sh.bin;
@@ -1271,7 +1266,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
     }
     // ---- the kept weight of every segment: above the last window, between it and the step, and of the step
     const int n_last = first ? static_cast<int>(sh.n) : 0;
-    if (first && tid == 0) tell(kSums, collected >= 0 && n_last <= kList ? 1 : 0);
+    if (first) tell(kSums, collected >= 0 && n_last <= kList ? 1 : 0);
     order = heard();
     const bool quick = sh.bin == 1;
     limit = sh.limit;
