@@ -421,6 +421,8 @@ qurl_status qurl_kv_cache_dequant(const void* cache, const float* scale, const i
  * Lengths and pages are read on the device: a token whose page is negative or
  * past num_slots is left out, a length past max_blocks * block_size is cut to
  * it, and both latch QURL_ERR_INVALID_ARG in the device status word.
+ * Sums are fp32; the weights that multiply the values carry 12 significant bits,
+ * whatever the value scales of the tokens around them.
  * Rows are independent, results identical run to run.  B = 0 is valid.
  * Errors: INVALID_ARG (NULL, a size out of range, q_heads % kv_heads, ld_table <
  * max_blocks, window < 0, scale not finite), UNSUPPORTED (head_dim; B * q_heads

@@ -258,3 +258,25 @@ def test_small_workspace_is_refused():
     need = q.qurl_kv_attn_workspace_size(1, 2, 1, 64, 1, 16)
     with pytest.raises(q.QurlError, match="WORKSPACE"):
         run(a, ws=torch.zeros(need - 1, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("e", [-18, -20, -24, -30, -60])
+@pytest.mark.parametrize("q_heads,kv_heads,hd", [(10, 2, 128), (7, 1, 128), (5, 1, 256), (8, 1, 192)])
+def test_attended_tokens_of_small_value_scale(q_heads, kv_heads, hd, e):
+    """Each query head attends one token whose value scale is 2^e of its neighbours' (the heads of a group
+    attend different tokens of one tile, each of another scale): what the others weigh, 2^-40 and less, leaves
+    the output to that token where its scale is not below theirs by as much, and to all of them where it is."""
+    a = make([300, 128, 700], q_heads, kv_heads, hd, 16, seed=q_heads)
+    group, part = q_heads // kv_heads, 16 * (hd // 16 // (q_heads // kv_heads))
+    x = torch.zeros((3, kv_heads, group, hd), device="cuda")
+    for b in range(3):
+        for h in range(group):
+            j = int(a["lens"][b]) - 1 - 3 * h
+            slot = int(a["table"][b, j // 16]) * 16 + j % 16
+            x[b, :, h, part * h:part * (h + 1)] = 40.0 * hd ** 0.5 / part / 3.0
+            a["k"][slot] = torch.zeros((kv_heads, hd), device="cuda").to(torch.float8_e4m3fn)
+            a["k"][slot, :, part * h:part * (h + 1)] = torch.full((kv_heads, part), 448.0, device="cuda").to(torch.float8_e4m3fn)
+            a["ks"][slot] = 3.0 / 448
+            a["vs"][slot] *= 2.0 ** (e - h)
+    a["q"] = x.reshape(3, -1).to(torch.bfloat16)
+    check(a)

@@ -15,9 +15,12 @@
 //     q = hi + lo / 16 with hi the e4m3 rounding, lo that of 16 (q - hi).  A bf16
 //     has 8 significant bits and each piece 4, so values within 2^-13 of the
 //     largest are exact and smaller ones off by at most 2^-22 of the largest.
-//   * x_j = p_j vs_j, scaled so that 128 times the tile's largest p bound it, in
-//     three pieces: 12 significant bits, 2^-12 relative, or 2^-25 of the tile's
-//     largest where the last piece underflows.
+//   * x_j = p_j vs_j, scaled by a power of two so that it lies below 256, in three
+//     pieces: 12 significant bits, 2^-12 relative, or an error of 2^-18 where the
+//     last piece underflows (2^-11 in all the tile).  The token that a head attends may
+//     have a far smaller value scale than its neighbours: while the scales lie within
+//     2^6 of each other, one power keeps them in [2, 256); a tile with others in it
+//     takes each head's largest p_j vs_j to [128, 256), from one more maximum a head.
 // Products are exact and sums fp32.  Keys and values are the A operand (M = 128
 // tokens for the scores, M = 128 dimensions for the output, the value tile read
 // transposed), the pieces of all the group's heads the N = 16 or 32 columns of
@@ -184,10 +187,24 @@ __device__ __forceinline__ float2 e4m3x2_value(uint32_t c) {
   return __half22float2(__half2(h));
 }
 
-// 2^n, n in [-126, 127].
+// Barrier of the softmax threads; whether `v` holds in any of them.
+__device__ __forceinline__ bool any_of(bool v) {
+  int r = v ? 1 : 0;
+  asm volatile(
+      "{\n\t.reg .pred a, b;\n\tsetp.ne.s32 a, %0, 0;\n\tbarrier.cta.red.or.pred b, 1, 128, a;\n\tselp.s32 %0, 1, 0, b;\n\t}"
+      : "+r"(r)::"memory");
+  return r != 0;
+}
+
+// 2^n, n in [-126, 128] (2^128: infinity).
 __device__ __forceinline__ float pow2(int n) { return __uint_as_float(static_cast<uint32_t>(n + 127) << 23); }
 // floor(log2 x) of a normal x > 0 (-127 for zero and subnormals).
 __device__ __forceinline__ int exponent(float x) { return static_cast<int>(__float_as_uint(x) >> 23) - 127; }
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));  // (subnormal scales too)
+  return y;
+}
 
 // Matrix descriptor of a tile whose rows are the MMA's K (tokens) and whose 128
 // contiguous bytes are its M (dimensions), 128-byte swizzle: groups of 8 rows
@@ -227,7 +244,8 @@ struct Shared {
   long long tiles_before[kSoftmax + 1];  // tiles before each thread's chunk
   uint32_t valid[3][4];                  // tokens of a stage that count
   float qfac[3][16];                     // per head: what turns a raw score into log2 units
-  alignas(16) float red[2][16][4];       // per-warp maxima of a tile (double-buffered)
+  // per-warp maxima of a tile (double-buffered): scores; where scales lie apart, log2 of the weights, and the scales
+  alignas(16) float red[2][8 + 8 + 1][4];
   alignas(16) float sum[16][4];
   int last;
 };
@@ -574,7 +592,10 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<G, PANELS>::CTAS)
       const int kvh = k.head / p.parts, part = k.head - kvh * p.parts;
       const int h0 = part * p.per_part, nh = min(p.per_part, group - h0);
       float qf[G], m[G], l[G], acc[PANELS][G];
+      int up = 0;                             // value scales in [v_lo, v_hi) times 2^up lie in [2, 256)
+      float v_lo = INFINITY, v_hi = INFINITY;  // (none yet)
       float mt[G], ps[G], back = 0.0f;  // the last tile's maximum, this lane's weight, and scale of its output
+      uint32_t more[2] = {0, 0};        // and, a byte each, the heads' further powers of two
 #pragma unroll
       for (int h = 0; h < G; ++h) {
         m[h] = mt[h] = kNone;
@@ -595,6 +616,10 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<G, PANELS>::CTAS)
           m[h] = mn;
           l[h] = l[h] * r[h] + ps[h] * f[h];
           f[h] *= back;
+        }
+        if ((more[0] | more[1]) != 0) {
+#pragma unroll
+          for (int h = 0; h < G; ++h) f[h] *= pow2(-static_cast<int>(more[h >> 2] >> (8 * (h & 3)) & 0xFFu));
         }
 #pragma unroll
         for (int q = 0; q < PANELS; ++q) {
@@ -630,31 +655,52 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<G, PANELS>::CTAS)
           const float mw = warp_fmax(x[h]);
           if (lane == 0) red[h][warp] = mw;
         }
-        {
-          const float vw = warp_fmax(fabsf(vs));
-          if (lane == 0) red[G][warp] = vw;
-        }
-        int fail = got ? 0 : 1;
-        asm volatile(
-            "{\n\t.reg .pred a, b;\n\tsetp.ne.s32 a, %0, 0;\n\tbarrier.cta.red.or.pred b, 1, 128, a;\n\tselp.s32 %0, 1, 0, b;\n\t}"
-            : "+r"(fail)::"memory");
-        if (fail) {
-          ok = false;
-          break;
+        const float va = fabsf(vs);
+        const bool apart = any_of(!got || (va != 0.0f && (va < v_lo || va >= v_hi)));  // (or a wait that ran out)
+        if (apart) {
+          const float lv = lg2(va), vw = warp_fmax(va);
+          if (lane == 0) red[2 * G][warp] = vw;
+#pragma unroll
+          for (int h = 0; h < G; ++h) {
+            const float yw = warp_fmax(x[h] + lv);
+            if (lane == 0) red[G + h][warp] = yw;
+          }
+          if (any_of(!got)) {
+            ok = false;
+            break;
+          }
         }
         // the previous tile's outputs have long been summed: its weights make room
         if (t > k.t0) got = add_tile(g - 1);
-        const float4 v4 = *reinterpret_cast<const float4*>(red[G]);
-        const float vmax = fmaxf(fmaxf(v4.x, v4.y), fmaxf(v4.z, v4.w));
-        const int up = min(max(7 - exponent(vmax), -120), 120);
+        auto most = [&](int i) {
+          const float4 r4 = *reinterpret_cast<const float4*>(red[i]);
+          return fmaxf(fmaxf(r4.x, r4.y), fmaxf(r4.z, r4.w));
+        };
+        const int e0 = apart ? exponent(most(2 * G)) : 0;
+        if (apart) up = min(max(7 - e0, -120), 120);
         const float vn = vs * pow2(up);
         back = pow2(-up);
+        more[0] = more[1] = 0;
 #pragma unroll
         for (int h = 0; h < G; ++h) {
-          const float4 r4 = *reinterpret_cast<const float4*>(red[h]);
-          mt[h] = fmaxf(fmaxf(fmaxf(r4.x, r4.y), fmaxf(r4.z, r4.w)), kNone);
+          mt[h] = fmaxf(most(h), kNone);
           ps[h] = ex2(x[h] - mt[h]);
           x[h] = ps[h] * vn;
+        }
+        if (apart) {
+          // 2^e more, so that the head's largest p vs is in [128, 256) (to the rounding of its logarithm; scores so large
+          // that a sum with log2 vs loses it keep e = 0)
+#pragma unroll
+          for (int h = 0; h < G; ++h) {
+            const float below = fabsf(mt[h]) < 0x1p22f ? fmaxf(most(G + h) - mt[h], -200.0f) : 200.0f;
+            const int e = min(max(7 - up - __float2int_rd(below), 0), 120);
+            more[h >> 2] |= static_cast<uint32_t>(e) << (8 * (h & 3));
+            x[h] *= pow2(e);
+          }
+          // the next tiles: scales up to twice this one's largest
+          up = min(max(6 - e0, -120), 120);
+          v_lo = pow2(max(e0 - 5, -126));
+          v_hi = pow2(min(e0 + 2, 128));  // (2^128: infinity)
         }
         uint8_t* pt = smem + C::OFF_P + (tid & 15);
         const int ch = tid >> 4;
