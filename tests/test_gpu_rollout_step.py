@@ -170,3 +170,40 @@ def test_decode_steps_then_training(qt):
     err = (d.double() - leaf.grad).abs()
     assert bool(err[ok].le(leaf.grad.abs()[ok] * 2.0 ** -8 * 1.01 + (weight * 2.0 ** -15)[ok]).all())
     assert not bool(d[mask == 0].any())
+
+
+def test_calls_given_a_stream_do_not_touch_the_current_one():
+    """Every operator with stream=: the current stream is busy and its freed memory full of ones, the results on
+    the given stream are those of the current stream alone."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(9)
+    r = lambda *s: torch.randn(s, device="cuda", generator=g)  # noqa: E731
+    n, hid, V, slots = 3, 256, 5000, 4096
+    kc, ks, vc, vs = q.kv_cache(slots, 2, 64)
+    q.qurl_kv_cache_quant(r(slots, 8 * 64).to(torch.bfloat16), 4 * 64, 2, 64, torch.arange(slots, device="cuda"), kc, ks, vc, vs)
+    table = torch.arange(slots // 16, device="cuda", dtype=torch.int32)[None].repeat(n, 1).contiguous()
+    lens = torch.tensor([4000, 17, 2500], dtype=torch.int32, device="cuda")
+    query, h, y = r(n, 4 * 64).to(torch.bfloat16), r(n, hid).to(torch.bfloat16), r(n, hid).to(torch.bfloat16)
+    gain, logits, u, dl = 1 + 0.1 * r(hid), r(n, V), torch.rand(n, device="cuda", generator=g), r(n)
+    target, top_p = torch.tensor([5, -1, 4999], device="cuda"), torch.full_like(u, .9)
+
+    def calls(stream):
+        logp, lse = q.token_logprob(logits, target, stream=stream)
+        return [*q.kv_attn_decode(query, 4, kc, ks, vc, vs, table, 16, lens, want_lse=True, stream=stream),
+                *q.residual_rmsnorm_quant(h, y, gain, q.INT8, stream=stream),
+                *q.sample(logits, u, top_p=top_p, want_kept=True, stream=stream), logp, lse,
+                q.token_logprob_grad(logits, target, lse, dl, stream=stream)]
+
+    want = calls(None)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for _ in range(3):
+        dirt = [torch.full((1 << k,), 255, dtype=torch.uint8, device="cuda") for k in range(6, 24)]
+        torch.cuda.synchronize()
+        del dirt
+        torch.cuda._sleep(1 << 27)
+        got = calls(s)
+        s.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    torch.cuda.synchronize()

@@ -131,3 +131,66 @@ def test_binding_takes_device_tensors_only():
     with pytest.raises(ValueError):
         q.kv_attn_decode(h, 1, c, s, c, s, torch.zeros(2, 1, dtype=torch.int32), 2, torch.zeros(2, dtype=torch.int32),
                          ws=torch.zeros(16, dtype=torch.uint8))
+
+
+class _Streams:
+    """Stands in for torch.cuda.stream: which stream an allocation belongs to."""
+
+    def __init__(self, monkeypatch):
+        self.now, self.seen = ["current"], []
+        outer = self
+
+        class Use:
+            def __init__(self, s):
+                self.s = s
+
+            def __enter__(self):
+                outer.now.append(self.s)
+
+            def __exit__(self, *exc):
+                outer.now.pop()
+
+        monkeypatch.setattr(torch.cuda, "stream", Use)
+        for name in ("empty", "zeros", "empty_strided"):
+            make = getattr(torch, name)
+            monkeypatch.setattr(torch, name, lambda *a, make=make, **k: (self.seen.append(self.now[-1]), make(*a, **k))[1])
+
+
+@pytest.mark.parametrize("positional", [False, True])
+def test_allocations_belong_to_the_stream_of_the_call(monkeypatch, positional):
+    """What a helper allocates is allocated for the stream that its kernel runs on."""
+    bf, B, K = torch.bfloat16, 2, 16
+    x, h, u, t = torch.zeros(B, 16), torch.zeros(B, K, dtype=bf), torch.zeros(B), torch.zeros(B, dtype=torch.int64)
+    cache, scale = torch.zeros(4, 1, 16, dtype=torch.uint8), torch.ones(4, 1)
+    table, lens, one = torch.zeros(B, 1, dtype=torch.int32), torch.zeros(B, dtype=torch.int32), torch.ones(B)
+    codes, w = torch.zeros(B, K, dtype=torch.int8), torch.zeros(B, K)
+    q4 = (torch.zeros(B, K // 2, dtype=torch.uint8), torch.zeros(B, 1, dtype=torch.uint8), one)
+    calls = [
+        (q.kv_attn_decode, (h, 1, cache, scale, cache, scale, table, 2, lens, None, 0, True, None)),
+        (q.residual_rmsnorm_quant, (h, h, torch.ones(K), q.INT8, None, None, 1.0, 1e-6, 1e-6, False)),
+        (q.sample, (x, u, None, None, None, None, True)),
+        (q.token_logprob, (x, t, 1.0)),
+        (q.token_logprob_grad, (x, t, u, u, 1.0, 1.0, None, False)),
+        (q.prepare_weights, (w, q.INT8, 1.5, torch.ones(K), True)),
+        (q.quant_act, (h, q.INT8, 1.0)),
+        (q.rmsnorm_quant, (h, torch.ones(K), q.INT8, 1e-6, True)),
+        (q.silu_mul_quant, (h, q.INT8, 1.0, True)),
+        (q.linear, (codes, one, codes, one, q.INT8, None)),
+        (q.gemm_acc, (codes, codes, q.INT8, None)),
+        (q.count_diff, (codes, codes)),
+        (q.nvfp4_quant, (h, 1.0)),
+        (q.nvfp4_linear, (q4, q4, None)),
+        (q.nvfp4_gemm_acc, (q4, q4, None)),
+        (q.acr_objective, (one, one, one, one, torch.ones(B, dtype=torch.uint8), 0.2, 2.0, True, True, True, None)),
+    ]
+    for name in dir(q):  # the C ABI: nothing is launched here
+        if name.startswith("qurl_") and not name.endswith("_size"):
+            monkeypatch.setattr(q, name, lambda *a, **k: None)
+    streams = _Streams(monkeypatch)
+    for f, args in calls:
+        streams.seen.clear()
+        f(*args, "s") if positional else f(*args, stream="s")
+        assert streams.seen and set(streams.seen) == {"s"}, f.__name__
+        streams.seen.clear()
+        f(*args)
+        assert streams.seen and set(streams.seen) == {"current"}, f.__name__

@@ -18,6 +18,7 @@ per-token activation INT8 / FP8 quantization, s = 1.5 (section "损失函数 /
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 import threading
@@ -139,6 +140,23 @@ def _ptr(t):
 def _stream(stream=None):
     # (the raw handle of torch.cuda.current_stream(), without the Stream object it is wrapped in)
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) if stream is None else stream.cuda_stream
+
+
+def _for_stream(f):
+    """Helpers that allocate: with a stream given (their last parameter), what they
+    allocate, zero and return belongs to it, so no other stream's work is still
+    using the memory and none is handed it while the call runs."""
+    last = f.__code__.co_argcount - 1
+
+    @functools.wraps(f)
+    def call(*args, **kw):
+        stream = args[last] if len(args) > last else kw.get("stream")
+        if stream is None:
+            return f(*args, **kw)
+        with torch.cuda.stream(stream):
+            return f(*args, **kw)
+
+    return call
 
 
 def _ok(rc: int, where: str):
@@ -486,6 +504,7 @@ def code_dtype(qt):
     return torch.int8 if qt == INT8 else torch.float8_e4m3fn
 
 
+@_for_stream
 def prepare_weights(W, qt, s=1.5, gamma=None, keep_scaled=True, stream=None):
     """UAQ fold + per-channel quantization.  Returns (Wq, sw, gamma', W')."""
     N, K = W.shape
@@ -498,6 +517,7 @@ def prepare_weights(W, qt, s=1.5, gamma=None, keep_scaled=True, stream=None):
     return Wq, sw, gf, Ws
 
 
+@_for_stream
 def quant_act(X, qt, pre_scale=1.0, stream=None):
     M, K = X.shape
     Xq = torch.empty((M, K), dtype=code_dtype(qt), device=X.device)
@@ -506,6 +526,7 @@ def quant_act(X, qt, pre_scale=1.0, stream=None):
     return Xq, sx
 
 
+@_for_stream
 def rmsnorm_quant(X, gamma_folded, qt, eps=1e-6, want_ms=False, stream=None):
     M, K = X.shape
     Xq = torch.empty((M, K), dtype=code_dtype(qt), device=X.device)
@@ -515,6 +536,7 @@ def rmsnorm_quant(X, gamma_folded, qt, eps=1e-6, want_ms=False, stream=None):
     return (Xq, sx, ms) if want_ms else (Xq, sx)
 
 
+@_for_stream
 def silu_mul_quant(GU, qt, pre_scale=1.0, want_h=False, stream=None):
     M, I2 = GU.shape
     Xq = torch.empty((M, I2 // 2), dtype=code_dtype(qt), device=GU.device)
@@ -532,6 +554,7 @@ def workspace(M, N, K, qt, device="cuda"):
     return torch.zeros(max(nbytes, 16), dtype=torch.uint8, device=device) if nbytes else None
 
 
+@_for_stream
 def linear(Xq, sx, Wq, sw, qt, ws=None, stream=None):
     M, N = Xq.shape[0], Wq.shape[0]
     Y = torch.empty((M, N), dtype=torch.bfloat16, device=Xq.device)
@@ -539,6 +562,7 @@ def linear(Xq, sx, Wq, sw, qt, ws=None, stream=None):
     return Y
 
 
+@_for_stream
 def gemm_acc(Xq, Wq, qt, ws=None, stream=None):
     M, N = Xq.shape[0], Wq.shape[0]
     acc = torch.empty((M, N), dtype=torch.int32 if qt == INT8 else torch.float32, device=Xq.device)
@@ -553,6 +577,7 @@ def kv_attn_workspace(B, q_heads, kv_heads, head_dim, max_blocks, block_size, de
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
+@_for_stream
 def kv_attn_decode(q, q_heads, k_cache, k_scale, v_cache, v_scale, block_table, block_size, seq_lens, scale=None,
                    window=0, want_lse=False, ws=None, stream=None):
     """Attention of one new token per sequence over the paged FP8 cache.  scale
@@ -568,6 +593,7 @@ def kv_attn_decode(q, q_heads, k_cache, k_scale, v_cache, v_scale, block_table, 
     return (out, lse) if want_lse else out
 
 
+@_for_stream
 def residual_rmsnorm_quant(H, Y, gamma_folded, qt, gamma_post=None, gate=None, residual_scale=1.0, eps=1e-6,
                            eps_post=1e-6, inplace=False, stream=None):
     """The residual update, its norms and the quantizer behind them.  Returns
@@ -581,6 +607,7 @@ def residual_rmsnorm_quant(H, Y, gamma_folded, qt, gamma_post=None, gate=None, r
     return H_out, Xq, sx
 
 
+@_for_stream
 def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, want_kept=False, stream=None):
     """The next token of each row from uniform numbers u.  Returns (token int64
     [B], logp [B]), with want_kept also logp_kept [B]."""
@@ -592,6 +619,7 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, want
     return (token, logp, kept) if want_kept else (token, logp)
 
 
+@_for_stream
 def token_logprob(logits, targets, temperature=1.0, stream=None):
     """Log-probabilities of the targets.  Returns (logp [T], lse [T]); the
     gradient call takes lse."""
@@ -602,6 +630,7 @@ def token_logprob(logits, targets, temperature=1.0, stream=None):
     return logp, lse
 
 
+@_for_stream
 def token_logprob_grad(logits, targets, lse, g, temperature=1.0, scale=1.0, denom=None, inplace=False, stream=None):
     """The logits' gradient of scale * sum_t g[t] logp[t] / denom; with inplace, in the logits' place."""
     d = logits if inplace else torch.empty_strided(logits.shape, logits.stride(), dtype=logits.dtype,
@@ -610,6 +639,7 @@ def token_logprob_grad(logits, targets, lse, g, temperature=1.0, scale=1.0, deno
     return d
 
 
+@_for_stream
 def count_diff(a, b, stream=None) -> torch.Tensor:
     c = torch.empty(1, dtype=torch.int64, device=a.device)
     qurl_count_diff(a, b, c, stream)
@@ -630,6 +660,7 @@ def qurl_detach_wide_weights(Wq):
     _ok(load().qurl_detach_wide_weights(_ptr(Wq)), "qurl_detach_wide_weights")
 
 
+@_for_stream
 def wide_weights(Wq, stream=None) -> torch.Tensor:
     """Allocate, fill and attach the fp16 copy of INT8 codes Wq.  The returned
     tensor holds a reference to Wq and detaches the copy when it is freed, so
@@ -677,6 +708,7 @@ def qurl_nvfp4_gemm_acc(x, w, acc, workspace, stream=None):
         "qurl_nvfp4_gemm_acc")
 
 
+@_for_stream
 def nvfp4_quant(X, pre_scale=1.0, stream=None):
     """Allocating wrapper: returns (q4 uint8 [R, K/2], sblk uint8 [R, K/16], g fp32 [R])."""
     R, K = X.shape
@@ -687,6 +719,7 @@ def nvfp4_quant(X, pre_scale=1.0, stream=None):
     return q4, sb, g
 
 
+@_for_stream
 def nvfp4_wide_weights(w, stream=None) -> torch.Tensor:
     """Allocate, fill and attach the fp16 copy of 4-bit weight rows w = (q4, sblk, g);
     detached when the returned tensor is freed (it holds a reference to q4)."""
@@ -704,6 +737,7 @@ def nvfp4_workspace(M, N, K, device="cuda") -> torch.Tensor:
     return torch.empty(max(qurl_nvfp4_workspace_size(M, N, K), 16), dtype=torch.uint8, device=device)
 
 
+@_for_stream
 def nvfp4_linear(x, w, ws=None, stream=None):
     M, N = x[0].shape[0], w[0].shape[0]
     ws = nvfp4_workspace(M, N, x[0].shape[1] * 2, x[0].device) if ws is None else ws
@@ -712,6 +746,7 @@ def nvfp4_linear(x, w, ws=None, stream=None):
     return Y
 
 
+@_for_stream
 def nvfp4_gemm_acc(x, w, ws=None, stream=None):
     M, N = x[0].shape[0], w[0].shape[0]
     ws = nvfp4_workspace(M, N, x[0].shape[1] * 2, x[0].device) if ws is None else ws
@@ -732,6 +767,7 @@ def acr_workspace(device="cuda") -> torch.Tensor:
     return torch.zeros(int(load().qurl_acr_workspace_size()), dtype=torch.uint8, device=device)
 
 
+@_for_stream
 def acr_objective(logp, logp_prox, logp_behav, adv, mask, eps=0.2, C=2.0, adaptive=True, want_term=False,
                   want_dterm=True, workspace=None, stream=None):
     """The ACR token objective (qurl_acr_objective).  Returns (stats fp64 [6] in
