@@ -413,8 +413,9 @@ qurl_status qurl_kv_cache_dequant(const void* cache, const float* scale, const i
  *   seq_lens     [B] int32, the new token's included once its key is cached;
  *                negative counts as 0.
  *   out          [B, ldo] bf16.     lse [B, q_heads] fp32 or NULL.
- *   workspace    qurl_kv_attn_workspace_size(...) bytes for the same arguments (a
- *                larger batch's or table's serves a smaller one), 16-byte aligned,
+ *   workspace    qurl_kv_attn_workspace_size(...) bytes for the same arguments, or
+ *                more (the size goes by the heads; one workspace serves layouts of
+ *                other heads too where it is large enough), 16-byte aligned,
  *                ZERO-FILLED before its first use: it holds counters that every
  *                call leaves zero.  Calls that may run at the same time need
  *                separate workspaces.

@@ -280,3 +280,18 @@ def test_attended_tokens_of_small_value_scale(q_heads, kv_heads, hd, e):
             a["vs"][slot] *= 2.0 ** (e - h)
     a["q"] = x.reshape(3, -1).to(torch.bfloat16)
     check(a)
+
+
+def test_workspace_of_another_head_layout():
+    """A workspace serves any layout it is large enough for, whatever layouts ran on it before: sequences over
+    many ranges leave partial sums everywhere, then a layout whose counters lie elsewhere joins in groups."""
+    big = make([1664, 8064], 32, 32, 128, 16, seed=41)
+    others = [make([40000, 1], 4, 1, 64, 64, seed=42), make([9000], 2, 1, 256, 64, seed=43),
+              make([6000, 300], 28, 4, 128, 16, seed=44)]
+    sizes = [q.qurl_kv_attn_workspace_size(a["q"].shape[0], a["q_heads"], a["k"].shape[1], a["k"].shape[2],
+                                           a["table"].shape[1], a["block"]) for a in [big] + others]
+    ws = torch.zeros(max(sizes), dtype=torch.uint8, device="cuda")
+    for a in others:
+        check(a, run(a, ws=ws))
+        check(big, run(big, ws=ws))
+        check(a, run(a, ws=ws))

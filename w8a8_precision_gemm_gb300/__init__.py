@@ -571,8 +571,9 @@ def gemm_acc(Xq, Wq, qt, ws=None, stream=None):
 
 
 def kv_attn_workspace(B, q_heads, kv_heads, head_dim, max_blocks, block_size, device="cuda") -> torch.Tensor:
-    """Scratch for kv_attn_decode calls of at most this size: zero-filled once
-    (its counters), left ready for reuse by every call."""
+    """Scratch for kv_attn_decode calls of this head layout, any batch and table:
+    zero-filled once (its counters), left ready for reuse by every call, one of
+    another layout included where it is large enough (a smaller one is refused)."""
     n = qurl_kv_attn_workspace_size(B, q_heads, kv_heads, head_dim, max_blocks, block_size)
     return torch.zeros(n, dtype=torch.uint8, device=device)
 

@@ -835,6 +835,13 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<G, PANELS>::CTAS)
   }
 }
 
+// The workspace's counters: room for those of any layout, so that no layout's partial sums lie where another's
+// counters do.  Several ranges (one needs no counter) have at most four rounds of two CTAs an SM as units, and
+// each unit has three.
+size_t counter_bytes(int num_sms) {
+  return (static_cast<size_t>(num_sms) * 2 * 4 * 3 * sizeof(unsigned) + 255) & ~static_cast<size_t>(255);
+}
+
 // Equal parts of a group of at most 8 query heads.
 constexpr int kMaxG = 8;
 
@@ -859,8 +866,7 @@ AttnPlan plan_attn(int q_heads, int kv_heads, int head_dim, int num_sms, size_t*
   const long long units = p.ranges * heads;
   p.grid = static_cast<int>(units < slots ? units : slots);
   const int G = p.per_part <= 5 ? 5 : kMaxG;
-  const size_t counters = (static_cast<size_t>(units) * 12 + 255) & ~static_cast<size_t>(255);
-  *bytes = counters + static_cast<size_t>(2 * units) * G * (head_dim + 2) * 4;
+  *bytes = counter_bytes(num_sms) + static_cast<size_t>(2 * units) * G * (head_dim + 2) * 4;
   return p;
 }
 
@@ -894,9 +900,8 @@ size_t attn_workspace_bytes(int q_heads, int kv_heads, int head_dim, int num_sms
 cudaError_t launch_kv_attn_decode(const AttnArgs& a, int num_sms, cudaStream_t st) {
   size_t bytes = 0;
   AttnPlan p = plan_attn(a.q_heads, a.kv_heads, a.head_dim, num_sms, &bytes);
-  const size_t units = static_cast<size_t>(p.ranges) * a.kv_heads * p.parts;
   p.counter = reinterpret_cast<unsigned*>(a.ws);
-  p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + ((units * 12 + 255) & ~static_cast<size_t>(255)));
+  p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + counter_bytes(num_sms));
   if (a.head_dim <= 128) return p.per_part <= 5 ? launch_inst<5, 1>(a, p, st) : launch_inst<kMaxG, 1>(a, p, st);
   return p.per_part <= 5 ? launch_inst<5, 2>(a, p, st) : launch_inst<kMaxG, 2>(a, p, st);
 }
