@@ -221,3 +221,15 @@ def test_columns_behind_a_row_stay():
         q.token_logprob(x, t[:3])
     with pytest.raises(ValueError):
         q.token_logprob_grad(x, t, lse, g, denom=torch.ones(1, device="cuda"))
+
+
+def test_rows_split_over_clusters():
+    """Few rows of every length that is split over 2, 4 or 8 CTAs, padding rows (whose CTAs leave at once) beside
+    them, again and again."""
+    for T, V in ((1, 8192), (2, 16384), (3, 40000), (7, 32768), (19, 65536), (38, 33000), (150, 8200)):
+        x, t, g = make(T, V, torch.bfloat16, seed=T)
+        t[1::3] = -1
+        logp, lse, _ = check(x, t, g)
+        for _ in range(20):
+            again = q.token_logprob(x, t)
+            assert torch.equal(again[0], logp) and torch.equal(again[1], lse)

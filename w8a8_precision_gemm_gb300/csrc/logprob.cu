@@ -107,6 +107,7 @@ __global__ void __launch_bounds__(kThreads, MINB) token_logprob_kernel(const T* 
     }
     return;
   }
+  if (cluster > 1) cluster_arrive();  // (the target is the cluster's: all of it or nothing of it comes here)
   const T* row = X + static_cast<long long>(t) * ld;
   const float xt = Vec<T>::one(row + target);
   const float c = kLog2e * inv_t;
@@ -142,6 +143,7 @@ __global__ void __launch_bounds__(kThreads, MINB) token_logprob_kernel(const T* 
       a = join(a, {__shfl_xor_sync(0xFFFFFFFFu, a.m, o), __shfl_xor_sync(0xFFFFFFFFu, a.s, o)}, c);
   }
   if (cluster > 1) {
+    cluster_wait();  // the first CTA runs: its shared memory may be written (the row's reading hides the wait)
     if (threadIdx.x == 0) {
       const uint32_t at = cluster_map(&slice[rank], 0);
       asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(a.m) : "memory");

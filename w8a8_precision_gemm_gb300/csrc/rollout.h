@@ -35,6 +35,13 @@ cudaError_t launch_pdl_cluster(void (*kern)(KArgs...), int cluster, dim3 grid, d
   return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
 }
 
+#ifdef __CUDACC__
+// The halves of a cluster barrier that orders no memory: every thread of the
+// cluster's CTAs arrives, and has arrived once one of them returns from the wait.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+#endif
+
 // attn_decode.cu: attention of one new token per sequence over the paged FP8 cache
 // (qurl_kv_attn_decode), and the workspace it needs.
 struct AttnArgs {
