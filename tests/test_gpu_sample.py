@@ -284,3 +284,13 @@ def test_large_batches_of_differing_rows(B):
     for a, b in zip((token, logp, kept), got):
         assert torch.equal(a[some], b)
     check(y, u[some], t[some], k[some], p[some], m[some])
+
+
+@pytest.mark.parametrize("V", [7, 600, 5000, 60000])
+def test_negative_zero_parameters(V):
+    """-0 lies in every parameter's range and is 0."""
+    z, n = f32(0., 0., 0.), f32(-0., -0., -0.)
+    x = logits(3, V, seed=V)
+    for kw in (dict(u=n), dict(u=n, p=n), dict(u=f32(.5, .9, .1), p=n), dict(u=n, t=n), dict(u=n, m=n, k=i32(0, 3, 900))):
+        token = check(x, **kw)
+        assert token == check(x, **{a: z if b is n else b for a, b in kw.items()})

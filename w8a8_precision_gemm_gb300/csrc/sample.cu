@@ -500,9 +500,9 @@ __device__ __forceinline__ Params params_of(const SampleArgs& a, int b) {
   Params p;
   p.temp = a.temperature ? a.temperature[b] : 1.0f;
   p.top_k = a.top_k ? a.top_k[b] : 0;
-  p.top_p = a.top_p ? a.top_p[b] : 1.0f;
+  p.top_p = (a.top_p ? a.top_p[b] : 1.0f) + 0.0f;  // (-0, which lies in the range, becomes 0: fraction() takes bits)
   p.min_p = a.min_p ? a.min_p[b] : 0.0f;
-  p.u = a.u[b];
+  p.u = a.u[b] + 0.0f;
   p.valid = (p.temp == 0.0f || (p.temp >= 1e-6f && p.temp <= 1e6f)) && p.top_p >= 0.0f && p.min_p >= 0.0f &&
             p.min_p <= 1.0f && p.u >= 0.0f && p.u < 1.0f;
   if (p.top_k < 0 || p.top_k >= a.V) p.top_k = 0;
@@ -540,7 +540,7 @@ __device__ int row_at(const SampleArgs& a, int n, Shared& sh) {
   return sh.found;
 }
 
-// floor(f * v) for f in [0, 1); `rest`: whether something was cut off.
+// floor(f * v) for f in [0, 1), not -0; `rest`: whether something was cut off.
 __device__ __forceinline__ u64 fraction(float f, u64 v, bool& rest) {
   const uint32_t b = __float_as_uint(f);
   rest = false;
