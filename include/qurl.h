@@ -47,7 +47,9 @@
  *     throw and never abort.
  *   - Device-side failures (a bounded wait inside a kernel that ran out, ~1 s)
  *     are latched in a per-device status word; qurl_check_device_status()
- *     synchronises the stream and returns (and clears) it.
+ *     synchronises the stream and returns (and clears) it.  An index or a
+ *     parameter that a kernel read and found out of range is latched too, and
+ *     changes nothing in the calls that follow.
  *   - Alignment: every pointer passed as a tensor must be 16-byte aligned and
  *     every row stride must be a multiple of 16 bytes; K must be a multiple
  *     of 16.  Violations return QURL_ERR_ALIGNMENT / QURL_ERR_UNSUPPORTED.
@@ -567,7 +569,8 @@ qurl_status qurl_acr_objective(const float* logp, const float* logp_prox, const 
 
 /* Synchronise `stream`, then return and clear the device status word of the
  * current device (QURL_OK, QURL_ERR_TIMEOUT from a kernel's bounded wait, or
- * QURL_ERR_INVALID_ARG from an index a kernel found out of range), or
+ * QURL_ERR_INVALID_ARG from an index or a parameter that a kernel found out of
+ * range; the timeout where both were latched), or
  * QURL_ERR_CUDA if the synchronisation itself failed. */
 qurl_status qurl_check_device_status(qurl_stream_t stream);
 

@@ -207,3 +207,37 @@ def test_calls_given_a_stream_do_not_touch_the_current_one():
         for a, b in zip(got, want):
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("mode", [0, 1, 2])
+@pytest.mark.parametrize("qt", [q.INT8, q.FP8_E4M3])
+def test_a_latched_parameter_leaves_later_calls_alone(qt, mode):
+    """A page, a target or a parameter out of range is reported at the next look at the status; the calls between,
+    each with other rows, compute what they compute without it, the linears that hand over inside their kernel
+    among them."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    for M, N, K in ((16, 4096, 4096), (64, 4608, 3584), (64, 512, 18944)):
+        W = torch.randn((N, K), device="cuda", generator=g) * 0.02
+        Wq, sw, _, _ = q.prepare_weights(W, qt, keep_scaled=False)
+        X = torch.randn((8, M, K), device="cuda", generator=g).to(torch.bfloat16)
+        ws = q.workspace(M, N, K, qt)
+        xq, sx = torch.empty((M, K), dtype=q.code_dtype(qt), device="cuda"), torch.empty(M, device="cuda")
+        logits = torch.randn((4, 1024), device="cuda", generator=g)
+        u = torch.tensor([.5, 1.5, .5, .5], device="cuda")
+        out = torch.full((2, 8, M, N), 7.0, dtype=torch.bfloat16, device="cuda")
+        before = q.qurl_set_fused_decode(mode)
+        try:
+            for k in (0, 1):
+                if k:
+                    q.sample(logits, u)  # u = 1.5 is out of range
+                for x, y in zip(X, out[k]):
+                    q.qurl_quant_act_linear(x, 1.5, Wq, sw, qt, y, xq, sx, ws)
+                if k:
+                    with pytest.raises(q.QurlError) as e:
+                        q.qurl_check_device_status()
+                    assert e.value.status == 1  # QURL_ERR_INVALID_ARG
+                q.qurl_check_device_status()
+        finally:
+            q.qurl_set_fused_decode(before)
+        assert torch.equal(out[0], out[1]) and not bool(ws[-256:].any())

@@ -25,8 +25,10 @@ std::atomic<int> g_fused_decode{1};    // 0 never, 1 where it pays, 2 always: se
 
 namespace {
 
-// Per-device status word: kernels latch a bounded-wait timeout here.
-__device__ int g_qurl_status;
+// Per-device status words: kernels latch a bounded-wait timeout in the first,
+// which the waits of later kernels look at, and an index or a parameter out of
+// range in the second, which none looks at.
+__device__ int g_qurl_status[2];
 
 constexpr int kMaxDevices = 64;
 
@@ -1079,12 +1081,13 @@ qurl_status qurl_check_device_status(qurl_stream_t stream) {
   DevState* dev = nullptr;
   QURL_TRY(device_state(&dev));
   QURL_CUDA(cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)));
-  int v = 0;
-  QURL_CUDA(cudaMemcpy(&v, dev->status, sizeof(int), cudaMemcpyDeviceToHost));
-  if (v != 0) {
-    const int zero = 0;
-    QURL_CUDA(cudaMemcpy(dev->status, &zero, sizeof(int), cudaMemcpyHostToDevice));
-    return v == qurl::kDevTimeout ? QURL_ERR_TIMEOUT : v == qurl::kDevBadIndex ? QURL_ERR_INVALID_ARG : QURL_ERR_CUDA;
+  int v[2] = {0, 0};
+  QURL_CUDA(cudaMemcpy(v, dev->status, sizeof(v), cudaMemcpyDeviceToHost));
+  if (v[0] != 0 || v[1] != 0) {
+    const int zero[2] = {0, 0};
+    QURL_CUDA(cudaMemcpy(dev->status, zero, sizeof(zero), cudaMemcpyHostToDevice));
+    if (v[0] != 0) return v[0] == qurl::kDevTimeout ? QURL_ERR_TIMEOUT : QURL_ERR_CUDA;
+    return QURL_ERR_INVALID_ARG;
   }
   return QURL_OK;
 }

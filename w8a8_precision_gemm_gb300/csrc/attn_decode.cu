@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<G, PANELS>::CTAS)
         const int b = tid * chunk + i;
         if (b >= a.B) break;
         n += span_of(a, b).tiles;
-        if (blockIdx.x == 0 && __ldg(a.seq_lens + b) > room) atomicCAS(a.status, kDevOk, kDevBadIndex);
+        if (blockIdx.x == 0 && __ldg(a.seq_lens + b) > room) latch_bad_index(a.status);
       }
       long long c = n;
 #pragma unroll
@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<G, PANELS>::CTAS)
           const int blk = j / a.block_size;
           const int page = __ldg(table + blk);
           const long long slot = static_cast<long long>(page) * a.block_size + (j - blk * a.block_size);
-          if (page < 0 || slot >= a.num_slots) atomicCAS(a.status, kDevOk, kDevBadIndex);
+          if (page < 0 || slot >= a.num_slots) latch_bad_index(a.status);
           else at = slot * a.kv_heads + kvh;
         }
         if (g >= C::STAGES && !wait_phase(&sh.empty[st], ((g / C::STAGES) & 1) ^ 1, a.status)) ok = false;

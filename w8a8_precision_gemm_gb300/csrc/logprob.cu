@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kThreads, MINB) token_logprob_kernel(const T* 
     if (threadIdx.x == 0 && rank == 0) {
       logp[t] = 0.0f;
       lse_out[t] = 0.0f;
-      if (target >= V) atomicCAS(status, kDevOk, kDevBadIndex);
+      if (target >= V) latch_bad_index(status);
     }
     return;
   }
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 4)
     const T* row = X + t * ld;
     T* out = dX + t * ldd;
     const long long target = targets[t];
-    if (target >= V && threadIdx.x == 0) atomicCAS(status, kDevOk, kDevBadIndex);
+    if (target >= V && threadIdx.x == 0) latch_bad_index(status);
     const float l = lse[t];
     float w = target >= 0 && target < V && l != -INFINITY ? w0 * g[t] : 0.0f;
     const bool live = w != 0.0f;  // (else zeros, whatever the row and lse hold)

@@ -21,6 +21,7 @@
 
 #include "internal.h"
 #include "ptx.cuh"
+#include "rollout.h"
 #include "rowquant.cuh"
 
 namespace qurl {
@@ -317,7 +318,7 @@ __global__ void count_diff_kernel(const uint8_t* __restrict__ a, const uint8_t* 
 // one row with the FP8 rule -- the per-token rule applied to each attention
 // head -- and the codes and the scale are written to the token's cache slot.
 // A negative slot (padding) writes nothing; a slot >= num_slots writes
-// nothing and latches kDevBadIndex.
+// nothing and is reported (latch_bad_index).
 __global__ void __launch_bounds__(256) kv_cache_quant_kernel(const __nv_bfloat16* __restrict__ QKV, int M,
                                                              long long ldq, int q_dim, int kv_heads, int head_dim,
                                                              const long long* __restrict__ slots,
@@ -336,7 +337,7 @@ __global__ void __launch_bounds__(256) kv_cache_quant_kernel(const __nv_bfloat16
   const long long slot = __ldg(slots + m);
   if (slot < 0) return;
   if (slot >= num_slots) {
-    if (lane == 0) atomicCAS(status, kDevOk, kDevBadIndex);
+    if (lane == 0) latch_bad_index(status);
     return;
   }
   const int nvec = head_dim >> 3;
@@ -371,7 +372,7 @@ __global__ void __launch_bounds__(256) kv_cache_dequant_kernel(const uint8_t* __
   const int j = static_cast<int>(idx - i * per_row);
   const long long slot = __ldg(slots + i);
   if (slot < 0 || slot >= num_slots) {
-    atomicCAS(status, kDevOk, kDevBadIndex);
+    latch_bad_index(status);
     return;
   }
   const int h = (j * 8) / head_dim;

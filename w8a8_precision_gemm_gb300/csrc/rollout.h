@@ -36,6 +36,11 @@ cudaError_t launch_pdl_cluster(void (*kern)(KArgs...), int cluster, dim3 grid, d
 }
 
 #ifdef __CUDACC__
+// An index or a parameter that a kernel read and found out of range: reported by
+// the next look at the status, in the word that no wait looks at (a wait that ends
+// for it would break the handoff of a fused linear, whose counters then stay).
+__device__ __forceinline__ void latch_bad_index(int* status) { atomicExch(status + 1, kDevBadIndex); }
+
 // The halves of a cluster barrier that orders no memory: every thread of the
 // cluster's CTAs arrives, and has arrived once one of them returns from the wait.
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }

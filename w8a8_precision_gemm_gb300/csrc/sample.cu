@@ -656,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a,
   const float top = key_value(sh.top);
   if (!pr.valid || top == -INFINITY) {  // (the same in every CTA of the cluster)
     if (first && tid == 0) {
-      if (!pr.valid) atomicCAS(a.status, kDevOk, kDevBadIndex);
+      if (!pr.valid) latch_bad_index(a.status);
       a.token[b] = -1;
       if (a.logp) a.logp[b] = -INFINITY;
       if (a.logp_kept) a.logp_kept[b] = -INFINITY;
