@@ -407,8 +407,9 @@ qurl_status qurl_kv_cache_dequant(const void* cache, const float* scale, const i
  * (the slots of qurl_kv_cache_quant's slot_mapping), j < seq_lens[b], and, with
  * window > 0, j >= seq_lens[b] - window.  A sequence that sees no token (length
  * 0) gets out = 0 and lse = -inf.
- *   q            [B, ldq] bf16, finite, the q_heads * head_dim query columns first
- *                (the fused qkv output itself may be passed).
+ *   q            [B, ldq] bf16, finite (and so the scores in fp32), the q_heads *
+ *                head_dim query columns first (the fused qkv output itself may be
+ *                passed).
  *   caches       as in qurl_kv_cache_quant; head_dim a multiple of 16, at most 256.
  *   block_table  [B, ld_table] int32, max_blocks entries a row; only those that a
  *                sequence's tokens lie in are read.  block_size >= 1.

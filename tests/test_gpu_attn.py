@@ -295,3 +295,23 @@ def test_workspace_of_another_head_layout():
         check(a, run(a, ws=ws))
         check(big, run(big, ws=ws))
         check(a, run(a, ws=ws))
+
+
+def test_scores_of_any_size():
+    """Scores far below any that a mask would have: a softmax takes only their differences."""
+    a = make([1, 2, 200], 5, 1, 64, 16, seed=31)
+    a["k"].copy_(torch.full(a["k"].shape, 448.0, device="cuda").to(torch.float8_e4m3fn))
+    a["ks"].fill_(1.0 / 448)
+    a["q"].fill_(2.0 ** 100)
+    a["scale"] = -1.0
+    o, l = run(a)
+    # eight roundings of 2^-24: the key's scale, log2(e) and ln(2) as constants, and the four products and the sum
+    # between the raw score and lse
+    assert bool((l.double() / (-64 * 2.0 ** 100) - 1).abs().le(2.0 ** -21).all())
+    for b, n in enumerate((1, 2, 200)):
+        j = torch.arange(n, device="cuda")
+        slot = a["table"][b].long()[j // 16] * 16 + j % 16
+        v = a["v"].view(torch.uint8)[slot, 0].view(torch.float8_e4m3fn).double() * a["vs"][slot].double()
+        want, mag = v.mean(0), v.abs().mean(0)
+        d = (o[b].double().view(5, 64) - want).abs()
+        assert bool(d.le(want.abs() * 2.0 ** -8 + mag * 2.0 ** -11).all()), b

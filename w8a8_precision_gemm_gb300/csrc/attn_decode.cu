@@ -54,6 +54,7 @@
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <cstdint>
 
 #include "ptx.cuh"
@@ -69,7 +70,7 @@ constexpr int kThreads = kSoftmax + kLoaders + 32;  // and the MMA warp
 // Tiles per range at least: a tile more costs a unit about 0.75 us, joining partial sums about 3.
 constexpr int kMinTiles = 4;
 constexpr int kJoin = 12;        // partial sums that one unit joins; of more, groups of that many are joined first
-constexpr float kNone = -1e30f;  // a maximum over no tokens (log2 units)
+constexpr float kNone = -FLT_MAX;  // a maximum over no tokens: no score lies below it
 
 constexpr int round16(int n) { return (n + 15) / 16 * 16; }
 
