@@ -501,7 +501,8 @@ qurl_status qurl_sample(const void* logits, qurl_ftype x_type, int B, int V, int
  * qurl_token_logprob_grad takes lse as the forward call wrote it; g is the
  * derivative by logp (qurl_acr_objective's dterm), denom a device double (its
  * stats + 1, the number of valid tokens) or NULL for 1; a denom that is not
- * positive gives zeros.  Sums are fp32, and so are z and lse: z - lse, and with it a
+ * positive gives zeros, as a scale of 0 does.  scale / temperature / denom is taken
+ * in fp32 in that order.  Sums are fp32, and so are z and lse: z - lse, and with it a
  * probability, carries about 2^-23 max |z| (large for a temperature far below 1).
  *   targets [T] int64: a negative one is padding (logp = lse = 0, a zero gradient
  *   row whatever lse and g hold); one >= V is treated the same and latches

@@ -233,3 +233,13 @@ def test_rows_split_over_clusters():
         for _ in range(20):
             again = q.token_logprob(x, t)
             assert torch.equal(again[0], logp) and torch.equal(again[1], lse)
+
+
+def test_denominator_that_counts_nothing():
+    """No valid token: zeros, whatever the derivative holds."""
+    x, t, g = make(4, 1000, torch.bfloat16, seed=12)
+    _, lse = q.token_logprob(x, t)
+    g[0], g[1] = INF, float("nan")
+    for n in (0.0, -1.0, float("nan")):
+        d = q.token_logprob_grad(x, t, lse, g, denom=torch.tensor([n], dtype=torch.float64, device="cuda"))
+        assert not bool(d.any())

@@ -189,8 +189,8 @@ __global__ void __launch_bounds__(kThreads, 4)
     const long long target = targets[t];
     if (target >= V && threadIdx.x == 0) latch_bad_index(status);
     const float l = lse[t];
-    float w = target >= 0 && target < V && l != -INFINITY ? w0 * g[t] : 0.0f;
-    const bool live = w != 0.0f;  // (else zeros, whatever the row and lse hold)
+    const float w = target >= 0 && target < V && l != -INFINITY && w0 != 0.0f ? w0 * g[t] : 0.0f;
+    const bool live = w != 0.0f;  // (else zeros, whatever the row, lse and, in a row or call that does not count, g hold)
     for (int i = static_cast<int>(static_cast<long long>(nvec) * part / parts) + threadIdx.x; i < v1; i += kThreads) {
       float x[N];
       Vec<T>::unpack(reinterpret_cast<const uint4*>(row)[i], x);
