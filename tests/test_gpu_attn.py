@@ -315,3 +315,31 @@ def test_scores_of_any_size():
         want, mag = v.mean(0), v.abs().mean(0)
         d = (o[b].double().view(5, 64) - want).abs()
         assert bool(d.le(want.abs() * 2.0 ** -8 + mag * 2.0 ** -11).all()), b
+
+
+def test_behind_a_timeout_of_another_kernel():
+    """A GEMM's wait has run out and is not looked at yet: the attention behind it may give up, but what it stores
+    is right; with the status read and the workspace zeroed it runs as ever."""
+    a = make([3000, 10, 0, 777], 10, 2, 128, 16, seed=51)
+    ws = q.kv_attn_workspace(4, 10, 2, 128, a["table"].shape[1], 16)
+    want = run(a, ws=ws)
+    X, W = torch.randn((16, 256), device="cuda").to(torch.bfloat16), torch.randn((512, 256), device="cuda")
+    Wq, sw, _, _ = q.prepare_weights(W, q.FP8_E4M3, keep_scaled=False)
+    Xq, sx = q.quant_act(X, q.FP8_E4M3)
+    gws = q.workspace(16, 512, 256, q.FP8_E4M3)
+    out, lse = torch.full_like(want[0], 7.0), torch.full_like(want[1], 7.0)
+    q.qurl_check_device_status()
+    q.qurl_debug_inject_timeout()
+    q.linear(Xq, sx, Wq, sw, q.FP8_E4M3, gws)
+    q.qurl_kv_attn_decode(a["q"], 10, a["k"], a["ks"], a["v"], a["vs"], a["table"], 16, a["lens"], a["scale"], out, ws,
+                          lse=lse)
+    with pytest.raises(q.QurlError) as e:
+        q.qurl_check_device_status()
+    assert e.value.status == 6  # QURL_ERR_TIMEOUT
+    per_head = out.view(4, 10, 128)
+    left = (per_head == 7.0).all(-1)
+    assert bool((left | (per_head == want[0].view(4, 10, 128)).all(-1)).all())
+    assert bool(((lse == 7.0) | (lse == want[1])).all())
+    ws.zero_()
+    got = run(a, ws=ws)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

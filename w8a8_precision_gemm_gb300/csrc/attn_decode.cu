@@ -607,6 +607,7 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<G, PANELS>::CTAS)
       // adds tile i's output columns
       auto add_tile = [&](int i) {
         const bool got = wait_phase(&sh.ofull, i & 1, a.status);
+        __syncwarp();  // (lanes leave the wait each by itself; the loads below are the warp's)
         tc_fence_after();
         float f[G], r[G];
 #pragma unroll
@@ -633,10 +634,11 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<G, PANELS>::CTAS)
         tc_fence_before();
         return got;
       };
+      bool summed = true;  // no wait for an output has run out: told to the others at the next vote
       for (int t = k.t0; t < k.t1; ++t, ++g) {
         const int st = g % C::STAGES;
-        bool got = wait_phase(&sh.full[st], (g / C::STAGES) & 1, a.status) &&
-                   wait_phase(&sh.sfull[g & 1], (g >> 1) & 1, a.status);
+        const bool got = summed && wait_phase(&sh.full[st], (g / C::STAGES) & 1, a.status) &&
+                         wait_phase(&sh.sfull[g & 1], (g >> 1) & 1, a.status);
         tc_fence_after();
         if (t == k.t0) {
 #pragma unroll
@@ -672,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<G, PANELS>::CTAS)
           }
         }
         // the previous tile's outputs have long been summed: its weights make room
-        if (t > k.t0) got = add_tile(g - 1);
+        if (t > k.t0) summed = add_tile(g - 1);
         auto most = [&](int i) {
           const float4 r4 = *reinterpret_cast<const float4*>(red[i]);
           return fmaxf(fmaxf(r4.x, r4.y), fmaxf(r4.z, r4.w));
@@ -726,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<G, PANELS>::CTAS)
         mbar_arrive(&sh.pfull);
       }
       if (!ok) break;
-      bool got = add_tile(g - 1);
+      summed = add_tile(g - 1) && summed;
       // sums over the lanes (tokens)
 #pragma unroll
       for (int h = 0; h < G; ++h) {
@@ -734,7 +736,10 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<G, PANELS>::CTAS)
         for (int o = 16; o > 0; o >>= 1) l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], o);
         if (lane == 0) sh.sum[h][warp] = l[h];
       }
-      named_barrier(1, kSoftmax);
+      if (any_of(!summed)) {  // nothing is stored, joined or counted
+        ok = false;
+        break;
+      }
 #pragma unroll
       for (int h = 0; h < G; ++h) l[h] = (sh.sum[h][0] + sh.sum[h][1]) + (sh.sum[h][2] + sh.sum[h][3]);
       const int qh = kvh * group + h0;
@@ -825,7 +830,6 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<G, PANELS>::CTAS)
           if (lse && tid == 0) lse[h] = l[h] > 0.0f ? (m[h] + log2f(l[h])) * 0.693147180559945309f : -INFINITY;
         }
       }
-      (void)got;
     }
   }
   tc_fence_before();
