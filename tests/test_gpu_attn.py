@@ -343,3 +343,11 @@ def test_behind_a_timeout_of_another_kernel():
     ws.zero_()
     got = run(a, ws=ws)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("q_heads,kv_heads,hd", [(7, 1, 144), (8, 1, 256), (16, 1, 192), (20, 1, 256), (12, 2, 240), (5, 1, 160)])
+def test_wide_heads_over_many_ranges(q_heads, kv_heads, hd):
+    """Heads of two panels, up to eight query heads a unit, sequences joined from two ranges and from groups of
+    them."""
+    check(make([5000, 1, 700, 0, 333], q_heads, kv_heads, hd, 16, seed=hd))
+    check(make([15000, 9000, 20011], q_heads, kv_heads, hd, 64, seed=hd + 1))

@@ -122,3 +122,11 @@ def test_wrong_tensors_are_refused():
         q.residual_rmsnorm_quant(h, y[:2], gamma, q.INT8)
     with pytest.raises(ValueError):
         q.residual_rmsnorm_quant(h.float(), y, gamma, q.INT8)
+
+
+@pytest.mark.parametrize("M,K", [(1, 5136), (3, 5136), (152, 8192), (153, 8192), (304, 5120), (305, 5120), (152, 5376),
+                                 (400, 7168), (400, 8192), (305, 8176), (2, 8208)])
+def test_widths_at_the_edges_of_the_variants(M, K):
+    """Rows of one vector a thread and of four, at the widths and batches where the choice changes."""
+    check(M, K, q.INT8, seed=M)
+    check(M, K, q.FP8_E4M3, post=False, gate="one", seed=K, inplace=True)
