@@ -294,3 +294,15 @@ def test_negative_zero_parameters(V):
     for kw in (dict(u=n), dict(u=n, p=n), dict(u=f32(.5, .9, .1), p=n), dict(u=n, t=n), dict(u=n, m=n, k=i32(0, 3, 900))):
         token = check(x, **kw)
         assert token == check(x, **{a: z if b is n else b for a, b in kw.items()})
+
+
+@pytest.mark.parametrize("V", [262144, 262145, 300001, (1 << 20) + 3, 1 << 24])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_vocabularies_of_longer_segments(V, dtype):
+    """Past 2^18 logits a segment holds more than 512; 2^24 is the most."""
+    B = 2 if V < 1 << 24 else 1
+    x, u = logits(B, V, dtype, seed=V & 1023), torch.rand(B, device="cuda", generator=_gen(V & 1023))
+    check(x, u)
+    check(x, u, k=i32(50, 7)[:B], p=f32(.9, .5)[:B])
+    check(x, u, t=f32(.8, 1.1)[:B], p=f32(.95, .999)[:B])
+    check(x, u, k=i32(5000, 100000)[:B], m=f32(1e-4, 0.)[:B], p=f32(.99, .9)[:B])
