@@ -981,7 +981,7 @@ qurl_status qurl_residual_rmsnorm_quant(const void* Y, int ldy, const float* gam
   DevState* dev = nullptr;
   QURL_TRY(device_state(&dev));
   QURL_CUDA(qurl::launch_residual_rmsnorm_quant(Y, ldy, gamma_post, eps_post, gate, ldg, residual_scale, H, ldh, H_out,
-                                                ldo, gamma_folded, eps, M, K, qt, Xq, sx, ms_out,
+                                                ldo, gamma_folded, eps, M, K, qt, Xq, sx, ms_out, dev->num_sms,
                                                 reinterpret_cast<cudaStream_t>(stream)));
   return QURL_OK;
 }

@@ -35,7 +35,6 @@ namespace {
 
 using namespace rq;
 
-constexpr int kSms = 152;      // of the GPU
 constexpr int kNC = 8;        // 16-byte vectors cached per thread
 constexpr int kThreads = 512;  // threads of a long row
 
@@ -215,7 +214,7 @@ __global__ void __launch_bounds__(MAXT, MINB) residual_rmsnorm_quant_kernel(cons
 cudaError_t launch_residual_rmsnorm_quant(const void* Y, long long ldy, const float* gamma_post, float eps_post,
                                           const void* gate, long long ldg, float rs, const void* H, long long ldh,
                                           void* Hout, long long ldo, const float* gamma, float eps, int M, int K,
-                                          int qt, void* Xq, float* sx, float* ms_out, cudaStream_t st) {
+                                          int qt, void* Xq, float* sx, float* ms_out, int num_sms, cudaStream_t st) {
   ResidualArgs a{};
   a.Y = reinterpret_cast<const __nv_bfloat16*>(Y);
   a.H = reinterpret_cast<const __nv_bfloat16*>(H);
@@ -247,9 +246,9 @@ cudaError_t launch_residual_rmsnorm_quant(const void* Y, long long ldy, const fl
   // copy rate): 4 vectors 118 (3), 103 (4), 109 (5); 5 vectors 105 (4), 112 (5).  Persistent CTAs that load the next row into the registers the
   // current one leaves free measured 85 or more: the registers cost more
   // resident rows than the early loads gain.
-  if (M <= 2 * kSms && nvec <= 640)
+  if (M <= 2 * num_sms && nvec <= 640)
     return launch_pdl(residual_rmsnorm_quant_kernel<1, true, 640, 2>, dim3(M), threads(1), 0, st, a);
-  if (M <= kSms && nvec <= 1024)
+  if (M <= num_sms && nvec <= 1024)
     return launch_pdl(residual_rmsnorm_quant_kernel<1, true, 1024, 1>, dim3(M), threads(1), 0, st, a);
   if (nvec <= 4 * 160) return launch_pdl(residual_rmsnorm_quant_kernel<4, true, 160, 7>, dim3(M), threads(4), 0, st, a);
   if (nvec <= 4 * 256) return launch_pdl(residual_rmsnorm_quant_kernel<4, true, 256, 4>, dim3(M), threads(4), 0, st, a);

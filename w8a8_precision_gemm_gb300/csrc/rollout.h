@@ -104,6 +104,6 @@ cudaError_t launch_token_logprob_grad(const void* X, bool f32, long long T, int 
 cudaError_t launch_residual_rmsnorm_quant(const void* Y, long long ldy, const float* gamma_post, float eps_post,
                                           const void* gate, long long ldg, float rs, const void* H, long long ldh,
                                           void* Hout, long long ldo, const float* gamma, float eps, int M, int K,
-                                          int qt, void* Xq, float* sx, float* ms_out, cudaStream_t st);
+                                          int qt, void* Xq, float* sx, float* ms_out, int num_sms, cudaStream_t st);
 
 }  // namespace qurl
