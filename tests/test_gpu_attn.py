@@ -351,3 +351,24 @@ def test_wide_heads_over_many_ranges(q_heads, kv_heads, hd):
     them."""
     check(make([5000, 1, 700, 0, 333], q_heads, kv_heads, hd, 16, seed=hd))
     check(make([15000, 9000, 20011], q_heads, kv_heads, hd, 64, seed=hd + 1))
+
+
+def test_offsets_past_32_bits():
+    """Pages at both ends of caches of more than 2^32 bytes."""
+    block, kvh, hd = 16, 8, 256
+    pages = (2 ** 32 // (kvh * hd * block)) + 40
+    g = _gen(61)
+    kc, ks, vc, vs = q.kv_cache(pages * block, kvh, hd)
+    small = make([300, 77], 16, kvh, hd, block, seed=61, pages=60)
+    per = small["table"].shape[1]
+    table = torch.stack([pages - 1 - torch.arange(per), pages - 1 - per - torch.arange(per)]).int().cuda()
+    table[1, :2] = torch.tensor([3, 1])
+    slot = lambda t: (t.long()[..., None] * block + torch.arange(block, device="cuda")).reshape(-1)  # noqa: E731
+    for big, name in ((kc, "k"), (vc, "v")):
+        big.view(torch.uint8)[slot(table)] = small[name].view(torch.uint8)[slot(small["table"])]
+    for big, name in ((ks, "ks"), (vs, "vs")):
+        big[slot(table)] = small[name][slot(small["table"])]
+    want = run(small)
+    check(small, want)
+    got = run(small | dict(k=kc, ks=ks, v=vc, vs=vs, table=table))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
