@@ -372,3 +372,19 @@ def test_offsets_past_32_bits():
     check(small, want)
     got = run(small | dict(k=kc, ks=ks, v=vc, vs=vs, table=table))
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("peak", [0.0, 1.0, 4.0, 12.0])
+def test_attended_tokens_without_a_value(peak):
+    """The tokens that every head attends have a value scale of 0, as have others at random: what is left comes
+    from weights far below the largest."""
+    a = make([300, 128, 5, 700], 10, 2, 128, 16, seed=71)
+    g = _gen(72)
+    a["vs"].masked_fill_(torch.rand(a["vs"].shape, device="cuda", generator=g) < 0.3, 0.0)
+    a["q"].fill_(peak / 8)
+    for b in range(4):
+        for j in (0, int(a["lens"][b]) // 2):
+            slot = int(a["table"][b, j // 16]) * 16 + j % 16
+            a["k"][slot] = torch.full((2, 128), 448.0, device="cuda").to(torch.float8_e4m3fn)
+            a["vs"][slot] = 0.0
+    check(a)

@@ -20,7 +20,8 @@
 //     last piece underflows (2^-11 in all the tile).  The token that a head attends may
 //     have a far smaller value scale than its neighbours: while the scales lie within
 //     2^6 of each other, one power keeps them in [2, 256); a tile with others in it
-//     takes each head's largest p_j vs_j to [128, 256), from one more maximum a head.
+//     takes p_j against a reference below the largest score, so that each head's
+//     largest p_j vs_j is in [128, 256), from one more maximum a head.
 // Products are exact and sums fp32.  Keys and values are the A operand (M = 128
 // tokens for the scores, M = 128 dimensions for the output, the value tile read
 // transposed), the pieces of all the group's heads the N = 16 or 32 columns of
@@ -233,6 +234,47 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, int b) {
   return {first, len, (len - first + kTile - 1) / kTile};
 }
 
+// The power of two that takes scales below 2^(top + 1) below 256.
+__device__ __forceinline__ int scale_power(int top) { return min(max(7 - top, -120), 120); }
+__device__ __forceinline__ float most(const float (&v)[4]) {
+  const float4 q = *reinterpret_cast<const float4*>(v);
+  return fmaxf(fmaxf(q.x, q.y), fmaxf(q.z, q.w));
+}
+
+// A tile whose value scales lie far apart, by the softmax threads behind the vote that found it: takes each head's
+// score maximum in `red` to a reference 2^e below it, such that its largest p vs lies in [128, 256) (to the rounding
+// of its logarithm; scores so large that a sum with log2 vs loses it stay as they are).  Sums and outputs go by the
+// reference, whatever it is.  Returns the power that bounds the tile's scales with one to spare, or kFailed.  (Called,
+// not inlined: inlined it cost the other tiles 2%.)
+constexpr int kFailed = 1 << 20;
+template <int G>
+struct PerHead {
+  float v[G];
+};
+template <int G>
+__device__ __noinline__ int lower_references(float (*red)[4], PerHead<G> x, float va, bool got) {
+  const int tid = threadIdx.x, warp = tid >> 5;
+  const float lv = lg2(va), vw = warp_fmax(va);
+  if ((tid & 31) == 0) red[2 * G][warp] = vw;
+#pragma unroll
+  for (int h = 0; h < G; ++h) {
+    const float yw = warp_fmax(x.v[h] + lv);
+    if ((tid & 31) == 0) red[G + h][warp] = yw;
+  }
+  if (any_of(!got)) return kFailed;
+  const int top = exponent(most(red[2 * G])) + 1;
+  if (tid < G) {
+    const float mx = most(red[tid]);
+    if (fabsf(mx) < 0x1p22f) {
+      const int e = 7 - scale_power(top) - __float2int_rd(fmaxf(most(red[G + tid]) - mx, -200.0f));
+      *reinterpret_cast<float4*>(red[tid]) =
+          make_float4(mx - static_cast<float>(min(max(e, 0), 100)), -INFINITY, -INFINITY, -INFINITY);
+    }
+  }
+  named_barrier(1, kSoftmax);
+  return top;
+}
+
 struct Shared {
   uint64_t full[3], empty[3];  // a stage's rows have landed / its MMAs have read them
   uint64_t sfull[2];           // scores of a tile are in TMEM
@@ -249,6 +291,7 @@ struct Shared {
   alignas(16) float red[2][8 + 8 + 1][4];
   alignas(16) float sum[16][4];
   int last;
+  int failed;  // a wait for an output has run out
 };
 
 // a / b of small results: 32-bit where both fit (64-bit divisions took a microsecond of the call's start).
@@ -397,6 +440,7 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<G, PANELS>::CTAS)
       sh.tiles_before[tid + 1] = c;
     }
     if (tid == 0) {
+      sh.failed = 0;
       sh.tiles_before[0] = 0;
       sh.chunk = chunk;
     }
@@ -593,10 +637,15 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<G, PANELS>::CTAS)
       const int kvh = k.head / p.parts, part = k.head - kvh * p.parts;
       const int h0 = part * p.per_part, nh = min(p.per_part, group - h0);
       float qf[G], m[G], l[G], acc[PANELS][G];
-      int up = 0;                             // value scales in [v_lo, v_hi) times 2^up lie in [2, 256)
+      // value scales in [v_lo, v_hi) times 2^up lie in [2, 256)
+      int up = 0;
       float v_lo = INFINITY, v_hi = INFINITY;  // (none yet)
-      float mt[G], ps[G], back = 0.0f;  // the last tile's maximum, this lane's weight, and scale of its output
-      uint32_t more[2] = {0, 0};        // and, a byte each, the heads' further powers of two
+      auto window = [&](int top) {             // scales below 2^(top + 1)
+        up = scale_power(top);
+        v_lo = top < -113 ? INFINITY : pow2(top - 6);  // (scales so small that 2^up would pass fp32: none)
+        v_hi = pow2(min(top + 1, 128));
+      };
+      float mt[G], ps[G], back = 0.0f;  // the last tile's reference, this lane's weight, and scale of its output
 #pragma unroll
       for (int h = 0; h < G; ++h) {
         m[h] = mt[h] = kNone;
@@ -606,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<G, PANELS>::CTAS)
       }
       // adds tile i's output columns
       auto add_tile = [&](int i) {
-        const bool got = wait_phase(&sh.ofull, i & 1, a.status);
+        if (!wait_phase(&sh.ofull, i & 1, a.status)) sh.failed = 1;
         __syncwarp();  // (lanes leave the wait each by itself; the loads below are the warp's)
         tc_fence_after();
         float f[G], r[G];
@@ -619,10 +668,6 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<G, PANELS>::CTAS)
           l[h] = l[h] * r[h] + ps[h] * f[h];
           f[h] *= back;
         }
-        if ((more[0] | more[1]) != 0) {
-#pragma unroll
-          for (int h = 0; h < G; ++h) f[h] *= pow2(-static_cast<int>(more[h >> 2] >> (8 * (h & 3)) & 0xFFu));
-        }
 #pragma unroll
         for (int q = 0; q < PANELS; ++q) {
           float o[C::NP];
@@ -632,17 +677,18 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<G, PANELS>::CTAS)
             acc[q][h] = acc[q][h] * r[h] + f[h] * fmaf(o[2 * G + h], 0x1p-8f, fmaf(o[G + h], 0x1p-4f, o[h]));
         }
         tc_fence_before();
-        return got;
       };
-      bool summed = true;  // no wait for an output has run out: told to the others at the next vote
       for (int t = k.t0; t < k.t1; ++t, ++g) {
         const int st = g % C::STAGES;
-        const bool got = summed && wait_phase(&sh.full[st], (g / C::STAGES) & 1, a.status) &&
+        const bool got = wait_phase(&sh.full[st], (g / C::STAGES) & 1, a.status) &&
                          wait_phase(&sh.sfull[g & 1], (g >> 1) & 1, a.status);
         tc_fence_after();
         if (t == k.t0) {
 #pragma unroll
           for (int h = 0; h < G; ++h) qf[h] = h < nh ? sh.qfac[seg % C::STAGES][h] : 0.0f;
+          // the segment's first token says where its scales may lie: 2^3 below its own to 2^3 above
+          const float v0 = fabsf(scales[st * 2 * kTile + kTile]);
+          if (v0 > 0.0f) window(exponent(v0) + 3);
         }
         float s[C::NS];
         __syncwarp();
@@ -659,51 +705,27 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<G, PANELS>::CTAS)
           if (lane == 0) red[h][warp] = mw;
         }
         const float va = fabsf(vs);
-        const bool apart = any_of(!got || (va != 0.0f && (va < v_lo || va >= v_hi)));  // (or a wait that ran out)
-        if (apart) {
-          const float lv = lg2(va), vw = warp_fmax(va);
-          if (lane == 0) red[2 * G][warp] = vw;
+        const bool apart = any_of(!got || (valid && (va < v_lo || va >= v_hi)));  // (or a wait that ran out)
+        if (__builtin_expect(apart, 0)) {
+          PerHead<G> xs;
 #pragma unroll
-          for (int h = 0; h < G; ++h) {
-            const float yw = warp_fmax(x[h] + lv);
-            if (lane == 0) red[G + h][warp] = yw;
-          }
-          if (any_of(!got)) {
+          for (int h = 0; h < G; ++h) xs.v[h] = x[h];
+          const int top = lower_references<G>(red, xs, va, got);
+          if (top == kFailed) {
             ok = false;
             break;
           }
+          window(top);  // for the next tiles too
         }
         // the previous tile's outputs have long been summed: its weights make room
-        if (t > k.t0) summed = add_tile(g - 1);
-        auto most = [&](int i) {
-          const float4 r4 = *reinterpret_cast<const float4*>(red[i]);
-          return fmaxf(fmaxf(r4.x, r4.y), fmaxf(r4.z, r4.w));
-        };
-        const int e0 = apart ? exponent(most(2 * G)) : 0;
-        if (apart) up = min(max(7 - e0, -120), 120);
+        if (t > k.t0) add_tile(g - 1);
         const float vn = vs * pow2(up);
         back = pow2(-up);
-        more[0] = more[1] = 0;
 #pragma unroll
         for (int h = 0; h < G; ++h) {
-          mt[h] = fmaxf(most(h), kNone);
+          mt[h] = fmaxf(most(red[h]), kNone);
           ps[h] = ex2(x[h] - mt[h]);
           x[h] = ps[h] * vn;
-        }
-        if (apart) {
-          // 2^e more, so that the head's largest p vs is in [128, 256) (to the rounding of its logarithm; scores so large
-          // that a sum with log2 vs loses it keep e = 0)
-#pragma unroll
-          for (int h = 0; h < G; ++h) {
-            const float below = fabsf(mt[h]) < 0x1p22f ? fmaxf(most(G + h) - mt[h], -200.0f) : 200.0f;
-            const int e = min(max(7 - up - __float2int_rd(below), 0), 120);
-            more[h >> 2] |= static_cast<uint32_t>(e) << (8 * (h & 3));
-            x[h] *= pow2(e);
-          }
-          // the next tiles: scales up to twice this one's largest
-          up = min(max(6 - e0, -120), 120);
-          v_lo = pow2(max(e0 - 5, -126));
-          v_hi = pow2(min(e0 + 2, 128));  // (2^128: infinity)
         }
         uint8_t* pt = smem + C::OFF_P + (tid & 15);
         const int ch = tid >> 4;
@@ -728,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<G, PANELS>::CTAS)
         mbar_arrive(&sh.pfull);
       }
       if (!ok) break;
-      summed = add_tile(g - 1) && summed;
+      add_tile(g - 1);
       // sums over the lanes (tokens)
 #pragma unroll
       for (int h = 0; h < G; ++h) {
@@ -736,7 +758,8 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<G, PANELS>::CTAS)
         for (int o = 16; o > 0; o >>= 1) l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], o);
         if (lane == 0) sh.sum[h][warp] = l[h];
       }
-      if (any_of(!summed)) {  // nothing is stored, joined or counted
+      named_barrier(1, kSoftmax);
+      if (sh.failed != 0) {  // nothing is stored, joined or counted
         ok = false;
         break;
       }
@@ -827,7 +850,10 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<G, PANELS>::CTAS)
 #pragma unroll
           for (int q = 0; q < PANELS; ++q)
             if (q * 128 + tid < hd) out[static_cast<long long>(h) * hd + q * 128 + tid] = __float2bfloat16_rn(acc[q][h] * inv);
-          if (lse && tid == 0) lse[h] = l[h] > 0.0f ? (m[h] + log2f(l[h])) * 0.693147180559945309f : -INFINITY;
+          if (lse && tid == 0) {
+            const int k = exponent(l[h]);  // (the reference m may lie far below the largest score)
+            lse[h] = l[h] > 0.0f ? ((m[h] + static_cast<float>(k)) + log2f(l[h] * pow2(-k))) * 0.693147180559945309f : -INFINITY;
+          }
         }
       }
     }
