@@ -431,8 +431,9 @@ qurl_status qurl_kv_cache_dequant(const void* cache, const float* scale, const i
  * Errors: INVALID_ARG (NULL, a size out of range, q_heads % kv_heads, ld_table <
  * max_blocks, window < 0, scale not finite), UNSUPPORTED (head_dim; B * q_heads
  * of 2^31 or more, max_blocks * block_size above 2^30), ALIGNMENT, WORKSPACE.  One
- * kernel launch.  If its bounded waits run out (QURL_ERR_TIMEOUT), zero the
- * workspace before its next use.
+ * kernel launch.  If its bounded waits run out, or a timeout of an earlier kernel
+ * was still latched when it ran (QURL_ERR_TIMEOUT), zero the workspace before its
+ * next use.
  */
 size_t qurl_kv_attn_workspace_size(int B, int q_heads, int kv_heads, int head_dim, int max_blocks, int block_size);
 qurl_status qurl_kv_attn_decode(const void* q, int ldq, int B, int q_heads, int kv_heads, int head_dim,
@@ -478,7 +479,10 @@ qurl_status qurl_residual_rmsnorm_quant(const void* Y, int ldy, const float* gam
  * temperature 0 is greedy: the first of the order, logp that of temperature 1,
  * logp_kept 0.  The weights that decide are integers (to a relative 2^-29, in
  * units of 2^(ceil(log2 V) - 61) of the largest), so a choice does not depend on
- * the order of a sum; a token of less than a unit is never drawn.
+ * the order of a sum; a token of less than a unit is never drawn.  logp and
+ * logp_kept come from the same sums, to an ulp of fp32; with a top_k, a min_p or
+ * temperature 0 the sum over all of the row, which logp alone has, is one of fp32
+ * exponentials (2^-21, and 2^-24 for each of up to V / 256 additions in a row).
  *   temperature [B] fp32, 0 or in [1e-6, 1e6]; NULL: 1.   top_k [B] int32, <= 0 or >= V: off; NULL: off.
  *   top_p [B] fp32 >= 0, >= 1: off; NULL: off.            min_p [B] fp32 in [0, 1], 0: off; NULL: off.
  *   u [B] fp32 in [0, 1).  token [B] int64.  logp, logp_kept [B] fp32 or NULL.

@@ -14,7 +14,8 @@
 //   * q, scaled by a power of two so that its largest value is in [128, 256):
 //     q = hi + lo / 16 with hi the e4m3 rounding, lo that of 16 (q - hi).  A bf16
 //     has 8 significant bits and each piece 4, so values within 2^-13 of the
-//     largest are exact and smaller ones off by at most 2^-22 of the largest.
+//     largest are exact and smaller ones off by at most 2^-21 of the largest (half
+//     lo's smallest step, 2^-14, beside 128).
 //   * x_j = p_j vs_j, scaled by a power of two so that it lies below 256, in three
 //     pieces: 12 significant bits, 2^-12 relative, or an error of 2^-18 where the
 //     last piece underflows (2^-11 in all the tile).  The token that a head attends may
@@ -43,12 +44,16 @@
 // head) joins them in range order (a sequence over many ranges in groups): one
 // launch, the same result every run.
 //
-// Measured, 40 query heads over 8 KV heads of 128: 64 sequences of 256 to 8192
-// tokens (about 590 MB) 110 to 119 us, 5.2 TB/s; 4 of 98 k to 131 k tokens (1.0 GB)
-// 169 to 180 us, 5.8 TB/s, 0.85 of the copy rate.  The first tiles are there after 5 us,
-// then the cache streams at 6.3 TB/s; equal units end up to 13 us apart (whoever ends
-// first leaves its share of HBM to the others), the joins take 4 to 5 us more.  One
-// sequence of 300 tokens, 28 heads over 4: 10.6 us.
+// Measured on the device, 40 query heads over 8 KV heads of 128: 64 sequences of 256
+// to 8192 tokens (about 590 MB) 107 to 120 us (other lengths, other times), 5.2 TB/s; 4
+// of 98 k to 131 k tokens (1.0 GB) 172 to 176 us, 5.8 TB/s, 0.85 of the copy rate; value
+// scales spread over 2^10 in every tile 2 to 4% more.  The first tiles are there after
+// 5 us, then the cache streams at 6.3 TB/s; equal units end up to 16 us apart (whoever
+// ends first leaves its share of HBM to the others), the joins take 4 to 5 us more.  64
+// query heads over 4 (two parts, each of which reads the keys and values): 126 us of
+// 43 at the copy rate.  One sequence of 300 tokens, 28 heads over 4: 10.8 us, of which 3.6 to
+// the first tile (lengths, table, rows: one after the other), 1.3 a tile, nothing to
+// join, 2.5 to the end.
 // Taking units from a shared counter in shorter ranges was slower (more joins).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -16,11 +16,14 @@
 // Bytes: 2 (y) + 2 (h) + 2 (h') + 1 (codes) per value, against 13 for the three
 // passes (norm, update, norm and quantize) it stands for.  One row per CTA, the
 // row kept in registers from its only read to the codes.  8192 x 5120 FP8 with
-// both norms: 70 us, 4.2 TB/s, 0.62 of the copy rate; two dependent block
+// both norms: 70 us, 4.2 TB/s, 0.62 of the copy rate; three dependent block
 // reductions a row (both means and the absmax are chains of barriers that loads of
 // other rows on the SM cover only in part) and the issue slots (84
-// instructions a pair of values, 63% of them taken) bound it.  64 x 5120 INT8, one call after the other in a
-// graph: 4.0 us, the chain of one row (qurl_rmsnorm_quant alone 4.0).
+// instructions a pair of values, 63% of them taken) bound it.  64 x 5120 INT8, one
+// call after the other in a graph: 4.0 us, the chain of one row (qurl_rmsnorm_quant
+// alone 4.0).  Rows of more than 8192 (a CTA of 512 threads, the rest of the row read
+// again): 8192 x 27648 INT8 529 us with both norms, 433 without the one behind the
+// block (234 at the copy rate), 64 x 27648 10.6 and 8.8.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -238,14 +241,16 @@ cudaError_t launch_residual_rmsnorm_quant(const void* Y, long long ldy, const fl
   auto threads = [&](int nc) { return dim3(static_cast<unsigned>(((nvec + nc - 1) / nc + 31) / 32 * 32)); };
   // Few rows, all of them at once on the GPU (two an SM, or one of more than 640
   // vectors): a vector a thread, the shortest chain; 304 rows of 5120 5.0 us, 7.2 the
-  // other way; 256 of 8192, past one row an SM, 9.3 and 7.3.  Else
-  // four vectors a thread: fewer warps wait at each reduction.  8192 x 5120 (FP8,
+  // other way; 256 of 8192, past one row an SM, 9.3 and 7.3.  (640 threads is where the
+  // variant of two an SM was built and measured; between that and 1024 it was not.)
+  // Else four vectors a thread: fewer warps wait at each reduction.  8192 x 5120 (FP8,
   // both norms), us at resident CTAs: 1 vector 116 (2), 108 (3); 2 vectors 90 (3),
   // 80 (4); 3 vectors 73 (5); 4 vectors 73 (5), 71 (6), 70 (7), 75 (8); 5 vectors
-  // 72 (6), 70 (8).  8192 x 8192 (103 us, 78 without the norm behind the block; 69 at the
-  // copy rate): 4 vectors 118 (3), 103 (4), 109 (5); 5 vectors 105 (4), 112 (5).  Persistent CTAs that load the next row into the registers the
-  // current one leaves free measured 85 or more: the registers cost more
-  // resident rows than the early loads gain.
+  // 72 (6), 70 (8).  8192 x 8192 (103 to 107 us, 77 without the norm behind the block;
+  // 69 at the copy rate): 4 vectors 118 (3), 103 (4), 109 (5); 5 vectors 105 (4), 112
+  // (5).  Persistent CTAs that load the next row into the registers the current one
+  // leaves free measured 85 or more: the registers cost more resident rows than the
+  // early loads gain.
   if (M <= 2 * num_sms && nvec <= 640)
     return launch_pdl(residual_rmsnorm_quant_kernel<1, true, 640, 2>, dim3(M), threads(1), 0, st, a);
   if (M <= num_sms && nvec <= 1024)

@@ -21,12 +21,15 @@
 // a whole row only where the choice needs the whole sum (no top-k, no min-p);
 // elsewhere the row's sum, which only logp needs, is a plain fp32 one.
 //
-// 256 rows of 131072 bf16 logits (67 MB, 9.9 us at the copy rate): no limits 60 us
-// (12 the first reading, 20 the exact weights), top-k 50 48, greedy 43, rows of mixed
-// limits 93, top-p 0.95 at temperature 0.6 | 1.0: 108 | 182 (in a wave of 152 rows 13
-// us for the exact sum, 21 for what lies above the window, 25 for what one CTA does
-// between the passes).  One row of 32000: 14 us, 29 where the nucleus is large, the
-// chain of passes.
+// 256 rows of 131072 bf16 logits (67 MB, 9.9 us at the copy rate): no limits 57 to 59 us,
+// top-k 50 48, greedy 43, rows of mixed limits 88 to 92, top-p 0.95 at temperature 0.6 |
+// 1.0: 109 | 181 (in a wave of 152 rows 13 us for the exact sum, 21 for what lies above
+// the window, 25 for what one CTA does between the passes).  Without limits, stamped:
+// the CTAs end the first reading after 10 to 27 us (512 of them on 152 SMs, so some SMs
+// read for three and some for four), know the maximum 2 to 5 later, take 15 to 22 for
+// the exact weights and 4 for the search; greedy 10 to 21, 3 to 6, 8, and 5 to 8 for
+// the ranking.  One row of 32000: 14 us, 29 where the nucleus is large, the chain of
+// passes.
 //
 // A row is worked on by a cluster of 1 to 8 CTAs, as many as fill the GPU with
 // the batch.  Pass 1 takes the maximum; the threads' own maxima give a cut above
@@ -1352,15 +1355,15 @@ cudaError_t launch_sample(const SampleArgs& a_in, bool f32, int num_sms, cudaStr
   while ((1LL << (a.shift - 1)) < a.V) ++a.shift;
   // CTAs a row, each with 2048 logits at least: as many as fill the SMs' four places; twice that with a top-p or min-p,
   // whose rows need very different work, and parts of 40960 logits at most, whose windows fit the list (us at 1 | 2 |
-  // 4 | 8 CTAs a row: 256 x 131072, mixed limits 251 | 134 | 98 | 109, top-p 0.95 at temperature 0.8 194 | 168 | 154 |
-  // 185, top-k 50 46 | 48 | 57 | 83, no limits 68 | 66 | 68 | 80; mixed limits, 128 x 131072 147 | 113 | 92 | 76, 512 x
-  // 32000 121 | 84 | 109 | 178, 700 x 50257 133 | 114 | 160 | 265)
+  // 4 | 8 CTAs a row: 256 x 131072, mixed limits 228 | 130 | 90 | 104, top-p 0.95 at temperature 0.8 181 | 157 | 146 |
+  // 173, top-k 50 46 | 47 | 57 | 81, no limits 59 | 57 | 61 | 73, greedy 42 | 42 | 50 | 70; mixed limits, 128 x 131072
+  // 198 | 105 | 88 | 75, 512 x 32000 111 | 79 | 104 | 172, 700 x 50257 130 | 113 | 155 | 251)
   const bool uneven = a.top_p || a.min_p;
   int cluster = 1;
   while (cluster < 8 && a.V / (cluster * 2) >= 2048 &&
          (static_cast<long long>(a.B) * cluster * 2 <= (uneven ? 8LL : 4LL) * num_sms || (uneven && a.V / cluster > 40960)))
     cluster *= 2;
-  // more rows than fit at once: those that may be long first (256 x 131072, mixed limits: 98 us, 111 in row order; the
+  // more rows than fit at once: those that may be long first (256 x 131072, mixed limits, when it was built: 98 us, 111 in row order; the
   // look at every row's parameters costs a CTA about a microsecond at 256 rows)
   a.order = uneven && static_cast<long long>(a.B) * cluster > 4LL * num_sms && a.B <= 4096;
   auto* kern = f32 ? sample_kernel<float> : sample_kernel<__nv_bfloat16>;
