@@ -17,13 +17,13 @@ x20, W ~ N(0,0.02), gamma ~ 1 + N(0,0.1).  The step streams 976 MB of weights
 (each projection's weights come back only after the other three's, >= 450 MB,
 have passed through the 129 MB L2).
 
-Reported beside it (not part of `value`): the 7B-class decode chain (M = 64 and
+Reported beside it, as a JSON line on stderr (not part of `value`): the 7B-class decode chain (M = 64 and
 256), the 7B-class chain at M = 512 and 4096 with the code flips of a weight
 update W' -> W' + dW' for s = 1 and s = 1.5, every GEMM and quantizer on its
 own against its roofline, the per-RL-step weight re-quantization, the ACR
 token objective, the tensor-rate probes, the FP8 KV-cache quantizer, the 4-bit
-(NVFP4) variant of the linear, the end-to-end number through the C ABI with
-host buffers and the CPU oracle as a baseline.
+(NVFP4) variant of the linear; in the line on stdout, the end-to-end number
+through the C ABI with host buffers and the CPU oracle as a baseline.
 
     python bench.py [--gpus N] [--steps K] [--warmup W] [--impl ours|reference]
 """
@@ -107,6 +107,16 @@ def traffic_from_profile(path, sources):
     if fields.get("kernel_sources_sha256_16", "").split()[0:1] != [h.hexdigest()[:16]]:
         return None
     return int(fields["dram_bytes_per_launch"])
+
+
+DETAIL = ("per_gemm", "per_quant", "decode_7b", "chain_7b", "weight_requant", "acr_objective", "tensor_routes",
+          "kv_cache_fp8", "nvfp4_w4a4")
+
+
+def split_record(line):
+    """(the benchmark's record, the tables beside it): the record goes to stdout as one line of a few KB, which
+    whoever keeps only the end of the output still has in whole (the tables made it 22 KB); they go to stderr."""
+    return {k: v for k, v in line.items() if k not in DETAIL}, {k: line[k] for k in DETAIL if k in line}
 
 
 def alg_bytes(M, K, N):
@@ -1017,7 +1027,9 @@ def run_ours(args):
                                 "cores": min(ref.nthreads, args.ref_tokens), "kind": "oracle",
                                 "sample": ref.describe(dt)}
     if rank == 0:
-        print(json.dumps(line), flush=True)
+        record, detail = split_record(line)
+        print(json.dumps({"detail": detail}), file=sys.stderr, flush=True)
+        print(json.dumps(record), flush=True)
     return 0
 
 

@@ -31,3 +31,15 @@ def test_clock_summary_throttle_and_unsampled():
 def test_job_throughput_single_rank():
     v, ms = bench.job_throughput(2.0e12, 4.0, 1)
     assert ms == 4.0 and abs(v - 5.0e14) < 1.0
+
+
+def test_record_on_stdout_is_short():
+    """The tables beside the record (20 KB) are not part of its line."""
+    import json
+
+    tables = {k: {"x": [1.0] * 500} for k in bench.DETAIL}
+    line = {"metric": bench.METRIC, "value": 1.0, "e2e": {"value": 1.0}, "clocks": {}, "gpu_launches": 3,
+            "config": {"workload": bench.WORKLOAD}} | tables
+    record, detail = bench.split_record(line)
+    assert detail == tables and not set(record) & set(detail) and record | detail == line
+    assert len(json.dumps(record)) < 4096
