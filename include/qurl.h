@@ -425,8 +425,9 @@ qurl_status qurl_kv_cache_dequant(const void* cache, const float* scale, const i
  * Lengths and pages are read on the device: a token whose page is negative or
  * past num_slots is left out, a length past max_blocks * block_size is cut to
  * it, and both latch QURL_ERR_INVALID_ARG in the device status word.
- * Sums are fp32; the weights that multiply the values carry 12 significant bits,
- * whatever the value scales of the tokens around them.
+ * Sums are fp32.  A weight softmax(s)_j * v_scale is within 2^-12 of its value, or
+ * 2^-19 of the largest of the 128 tokens around it (2^-24 where their scales are
+ * within a factor of two), whatever those tokens' scales.
  * Rows are independent, results identical run to run.  B = 0 is valid.
  * Errors: INVALID_ARG (NULL, a size out of range, q_heads % kv_heads, ld_table <
  * max_blocks, window < 0, scale not finite), UNSUPPORTED (head_dim; B * q_heads

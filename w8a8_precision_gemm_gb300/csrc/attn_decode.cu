@@ -51,9 +51,9 @@
 // 5 us, then the cache streams at 6.3 TB/s; equal units end up to 16 us apart (whoever
 // ends first leaves its share of HBM to the others), the joins take 4 to 5 us more.  64
 // query heads over 4 (two parts, each of which reads the keys and values): 126 us of
-// 43 at the copy rate.  One sequence of 300 tokens, 28 heads over 4: 10.8 us, of which 3.6 to
-// the first tile (lengths, table, rows: one after the other), 1.3 a tile, nothing to
-// join, 2.5 to the end.
+// 43 at the copy rate.  One sequence of 300 tokens, 28 heads over 4: 10.8 us, of which
+// 3.6 to the first tile (lengths, table, rows: one after the other), 1.3 a tile,
+// nothing to join, 2.5 to the end.
 // Taking units from a shared counter in shorter ranges was slower (more joins).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -691,9 +691,9 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<G, PANELS>::CTAS)
         if (t == k.t0) {
 #pragma unroll
           for (int h = 0; h < G; ++h) qf[h] = h < nh ? sh.qfac[seg % C::STAGES][h] : 0.0f;
-          // the segment's first token says where its scales may lie: 2^3 below its own to 2^3 above
+          // the segment's first token says where its scales may lie: 2^5 below its own to twice that
           const float v0 = fabsf(scales[st * 2 * kTile + kTile]);
-          if (v0 > 0.0f) window(exponent(v0) + 3);
+          if (v0 > 0.0f) window(exponent(v0) + 1);
         }
         float s[C::NS];
         __syncwarp();
