@@ -78,6 +78,8 @@ typedef enum {
 
 typedef enum { QURL_INT8 = 0, QURL_FP8_E4M3 = 1 } qurl_qtype;
 typedef enum { QURL_BF16 = 0, QURL_FP32 = 1 } qurl_ftype;
+/* How the pairs of a rotary position lie in a head: (i, i + rot_dim / 2), or (2 i, 2 i + 1). */
+typedef enum { QURL_ROPE_HALF = 0, QURL_ROPE_INTERLEAVED = 1 } qurl_rope_layout;
 
 /* cudaStream_t without including the CUDA headers. */
 typedef struct CUstream_st* qurl_stream_t;
@@ -394,6 +396,89 @@ qurl_status qurl_kv_cache_quant(const void* qkv, int M, int ldq, int q_dim, int 
  */
 qurl_status qurl_kv_cache_dequant(const void* cache, const float* scale, const int64_t* slots, int n, int kv_heads,
                                   int head_dim, long long num_slots, void* out, qurl_stream_t stream);
+
+/*
+ * Rotary positions.  The first rot_dim values of each head are rot_dim / 2 pairs
+ * (a, b), (i, i + rot_dim / 2) or neighbours (`layout`); pair i of a token at position
+ * p is turned by the angle p inv_freq[i]:
+ *   a' = factor (a cos - b sin),   b' = factor (a sin + b cos)
+ * and the rest of the head stays.  inverse = 1 turns the other way (sin negated): with
+ * the same factor it is the transpose, the gradient of the rotation with respect to X.
+ * Arithmetic is fp32; the angle is taken modulo a turn in fixed point, within 2^-31 of a
+ * turn and |p inv_freq| 2^-52 radians for any position.  Frequencies scaled for long contexts and the
+ * factor that goes with them are the caller's (the Python binding's rope_frequencies
+ * gives the usual ones).
+ *   X, out     [M, heads * head_dim] of x_type (bf16 or fp32), row strides ldx, ldo; out may be X
+ *              (ldo == ldx) and must not overlap it otherwise.  Columns past the heads
+ *              are neither read nor written.  Query and key heads that lie side
+ *              by side may be passed as one.
+ *   positions  [M] int32, any sign.    inv_freq [rot_dim / 2] fp64, finite: radians a position.
+ *   rot_dim    even, at most head_dim; head_dim a multiple of 16, at most 256.
+ * M = 0 is valid.  Errors: INVALID_ARG (NULL, a size or a stride out of range, factor not
+ * finite), UNSUPPORTED (head_dim), ALIGNMENT.  One kernel launch.
+ */
+qurl_status qurl_rope(const void* X, qurl_ftype x_type, int M, int ldx, int heads, int head_dim,
+                      const int32_t* positions, const double* inv_freq, int rot_dim, qurl_rope_layout layout,
+                      float factor, int inverse, void* out, int ldo, qurl_stream_t stream);
+
+/*
+ * qurl_rope of the queries and keys of the fused qkv output together with
+ * qurl_kv_cache_quant: the queries are rotated into q_out, the keys are rotated and, in
+ * fp32 as they come out of the rotation, quantized into the cache, the values are
+ * quantized as they are.  A token with a negative slot (padding) writes no key and no value; its query
+ * is rotated all the same.  A head whose largest magnitude is below 2^-140 is stored as zeros.
+ *   qkv    [M, ldq] bf16: q_heads, kv_heads and kv_heads heads of head_dim columns.
+ *   q_out  [M, ldo] bf16, ldo >= q_heads * head_dim; may be qkv (ldo == ldq), whose
+ *          keys and values stay, and must not overlap it otherwise.
+ *   slot_mapping and the caches as in qurl_kv_cache_quant, the rest as in qurl_rope.
+ * A slot past the cache is reported and written nowhere, as there.  Two tokens of a call
+ * must not have the same slot.  M = 0 is valid.  Errors as qurl_rope.  One kernel launch.
+ */
+qurl_status qurl_rope_kv_cache_quant(const void* qkv, int M, int ldq, int q_heads, int kv_heads, int head_dim,
+                                     const int32_t* positions, const double* inv_freq, int rot_dim,
+                                     qurl_rope_layout layout, float factor, void* q_out, int ldo,
+                                     const int64_t* slot_mapping, long long num_slots, void* k_cache, float* k_scale,
+                                     void* v_cache, float* v_scale, qurl_stream_t stream);
+
+/*
+ * Pages of the paged cache, handed out and taken back on the GPU.  The free pages are the first
+ * *n_free entries of free_pages [num_pages]; pages are taken from its end and given
+ * back to its end.  A page belongs to one request; request b's pages are the entries
+ * of its row of block_table [B, ld_table] (max_blocks of them), block k holding the tokens at
+ * positions k block_size .. k block_size + block_size - 1.
+ *
+ * qurl_kv_append places new_lens[b] new tokens behind the cached_lens[b] ones of each
+ * request.  The pages they reach first are taken from the list, in the order of
+ * requests and blocks, and written to the table (no other entry is); the tokens of all requests
+ * in a row, in order, make the step's rows:
+ *   slot_mapping [M] int64, positions [M] int32   each row's slot and position; rows behind
+ *                                                 the last token: -1 and 0
+ *   cu_new [B + 1]       int32, the first row of each request, and the number of rows
+ *   seq_lens [B]         int32, cached_lens + new_lens; may be cached_lens
+ *   n_free_out           *n_free less the pages taken; may be n_free.  Where the list is
+ *                        too short the last pages are missing: -1 in the table and in the
+ *                        slots of their tokens, and n_free_out is minus the number missing
+ * Lengths are read on the device; negative ones count as 0.  Requests longer than max_blocks *
+ * block_size and rows past M are cut (the lengths and cu_new say so), and a *n_free past num_pages counts as
+ * num_pages; these latch QURL_ERR_INVALID_ARG in the device status word.
+ *
+ * qurl_kv_release gives back the pages of the blocks behind the first keep_lens[b] of
+ * lens[b] tokens (keep_lens NULL: all of a request's), in the order of requests and
+ * blocks; a negative entry has no page to give.  *n_free_out (may be n_free) is the
+ * new number; a negative *n_free counts as 0.  The table is only read.  Pages past num_pages and lengths past
+ * the table are cut and reported as above.
+ *
+ * B up to 16384, max_blocks * block_size up to 2^30, B * max_blocks below 2^31 (UNSUPPORTED otherwise); B
+ * and M may be 0.  Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT (slot_mapping 8 bytes,
+ * the others 4).  One kernel launch each.
+ */
+qurl_status qurl_kv_append(const int32_t* cached_lens, const int32_t* new_lens, int B, int32_t* block_table,
+                           int ld_table, int max_blocks, int block_size, const int32_t* free_pages, int num_pages,
+                           const int32_t* n_free, int32_t* n_free_out, int M, int64_t* slot_mapping,
+                           int32_t* positions, int32_t* cu_new, int32_t* seq_lens, qurl_stream_t stream);
+qurl_status qurl_kv_release(const int32_t* lens, const int32_t* keep_lens, int B, const int32_t* block_table,
+                            int ld_table, int max_blocks, int block_size, int32_t* free_pages, int num_pages,
+                            const int32_t* n_free, int32_t* n_free_out, qurl_stream_t stream);
 
 /*
  * Attention of one new token per sequence over the FP8 cache that

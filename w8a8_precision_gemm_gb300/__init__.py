@@ -19,6 +19,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import os
 import re
 import threading
@@ -32,6 +33,8 @@ INT8 = 0
 FP8_E4M3 = 1
 BF16 = 0
 FP32 = 1
+ROPE_HALF = 0
+ROPE_INTERLEAVED = 1
 
 STATUS = {0: "QURL_OK", 1: "QURL_ERR_INVALID_ARG", 2: "QURL_ERR_UNSUPPORTED", 3: "QURL_ERR_ALIGNMENT",
           4: "QURL_ERR_WORKSPACE", 5: "QURL_ERR_CUDA", 6: "QURL_ERR_TIMEOUT"}
@@ -100,6 +103,10 @@ def load() -> ctypes.CDLL:
             "qurl_kv_cache_dequant": [P, P, P, i, i, i, ctypes.c_longlong, P, P],
             "qurl_kv_attn_decode": [P, i, i, i, i, i, P, P, P, P, ctypes.c_longlong, P, i, i, i, P, i, f, P, i, P, P,
                                     z, P],
+            "qurl_rope": [P, i, i, i, i, i, P, P, i, i, f, i, P, i, P],
+            "qurl_rope_kv_cache_quant": [P, i, i, i, i, i, P, P, i, i, f, P, i, P, ctypes.c_longlong, P, P, P, P, P],
+            "qurl_kv_append": [P, P, i, P, i, i, i, P, i, P, P, i, P, P, P, P, P],
+            "qurl_kv_release": [P, P, i, P, i, i, i, P, i, P, P, P],
             "qurl_residual_rmsnorm_quant": [P, i, P, f, P, i, f, P, i, P, i, P, f, i, i, i, P, P, P, P],
             "qurl_sample": [P, i, i, i, i, P, P, P, P, P, P, P, P, P],
             "qurl_token_logprob": [P, i, i, i, i, P, f, P, P, P],
@@ -384,6 +391,105 @@ def qurl_kv_attn_decode(q, q_heads, k_cache, k_scale, v_cache, v_scale, block_ta
         "qurl_kv_attn_decode")
 
 
+def _rotation(M, head_dim, positions, inv_freq):
+    """(rot_dim, addresses of positions and inv_freq)."""
+    rot = 2 * inv_freq.numel()
+    if not 0 < rot <= head_dim:
+        raise ValueError("inv_freq has between 1 and head_dim / 2 values")
+    at, = _vec(torch.int32, M, (positions, "positions"))
+    freq, = _vec(torch.float64, rot // 2, (inv_freq, "inv_freq"))
+    return rot, at, freq
+
+
+def _apart(x, out):
+    """out is x itself, or shares no memory with it as far as the views' own elements tell."""
+    if out.data_ptr() == x.data_ptr():
+        return
+    end = lambda t: t.data_ptr() + t.element_size() * (1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride())))  # noqa: E731
+    if x.numel() and out.numel() and x.data_ptr() < end(out) and out.data_ptr() < end(x) \
+            and x.untyped_storage().data_ptr() == out.untyped_storage().data_ptr():
+        # (columns of one matrix, side by side)
+        ld, size = x.stride(0), x.element_size()
+        gap = (out.data_ptr() - x.data_ptr()) // size % ld if ld else 0
+        if x.dtype is not out.dtype or out.stride(0) != ld or gap < x.shape[1] or gap + out.shape[1] > ld:
+            raise ValueError("out overlaps the input")
+
+
+def qurl_rope(X, heads, head_dim, positions, inv_freq, out, layout=ROPE_HALF, factor=1.0, inverse=False, stream=None):
+    """Rotary positions of the first `heads` heads of each row of X (see include/qurl.h)."""
+    _here(X, positions, inv_freq, out)
+    M = X.shape[0]
+    if X.dtype not in (torch.bfloat16, torch.float32) or out.dtype is not X.dtype or out.shape[0] != M:
+        raise ValueError("X and out are both bf16 or both fp32, [M, ...]")
+    ldx, ldo = _ld(X), _ld(out)
+    if min(X.shape[1], out.shape[1]) < heads * head_dim:
+        raise ValueError("X and out have heads * head_dim columns at least")
+    _apart(X[:, :heads * head_dim], out[:, :heads * head_dim])
+    rot, at, freq = _rotation(M, head_dim, positions, inv_freq)
+    _ok(load().qurl_rope(X.data_ptr(), FP32 if X.dtype is torch.float32 else BF16, M, ldx, heads, head_dim, at, freq,
+                         rot, layout, factor, 1 if inverse else 0, out.data_ptr(), ldo, _stream(stream)), "qurl_rope")
+
+
+def qurl_rope_kv_cache_quant(qkv, q_heads, positions, inv_freq, q_out, slot_mapping, k_cache, k_scale, v_cache,
+                             v_scale, layout=ROPE_HALF, factor=1.0, stream=None):
+    """Rotary positions of queries and keys, and the FP8 quantization of keys and values into the cache (see
+    include/qurl.h)."""
+    _here(qkv, positions, inv_freq, q_out, slot_mapping, k_cache, k_scale, v_cache, v_scale)
+    num_slots, kv_heads, head_dim = shape = k_cache.shape
+    M, columns = qkv.shape
+    if (v_cache.shape != shape or k_cache.element_size() != 1 or v_cache.element_size() != 1
+            or not k_cache.is_contiguous() or not v_cache.is_contiguous()):
+        raise ValueError("caches are contiguous, 8-bit, [slots, kv_heads, head_dim]")
+    if qkv.dtype is not torch.bfloat16 or q_out.dtype is not torch.bfloat16 or q_out.shape[0] != M:
+        raise ValueError("qkv and q_out are bf16 [M, ...]")
+    if columns < (q_heads + 2 * kv_heads) * head_dim or q_out.shape[1] < q_heads * head_dim:
+        raise ValueError("qkv has the columns of q_heads + 2 kv_heads heads, q_out those of q_heads")
+    ldq, ldo = _ld(qkv), _ld(q_out)
+    _apart(qkv[:, :(q_heads + 2 * kv_heads) * head_dim], q_out[:, :q_heads * head_dim])
+    rot, at, freq = _rotation(M, head_dim, positions, inv_freq)
+    ks, vs = _vec(torch.float32, num_slots * kv_heads, (k_scale, "k_scale"), (v_scale, "v_scale"))
+    slots, = _vec(torch.int64, M, (slot_mapping, "slot_mapping"))
+    _ok(load().qurl_rope_kv_cache_quant(qkv.data_ptr(), M, ldq, q_heads, kv_heads, head_dim, at, freq, rot, layout,
+                                        factor, q_out.data_ptr(), ldo, slots, num_slots, k_cache.data_ptr(), ks,
+                                        v_cache.data_ptr(), vs, _stream(stream)), "qurl_rope_kv_cache_quant")
+
+
+def _pages(B, block_table, free_pages):
+    """(rows' stride, blocks a request) of a table, after the checks that it and the list of free pages share."""
+    if block_table.dtype is not torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table is int32 [B, blocks]")
+    if free_pages.dtype is not torch.int32 or not free_pages.is_contiguous():
+        raise ValueError("free_pages is int32, contiguous")
+    blocks = block_table.shape[1]
+    return (_ld(block_table) if blocks else 0), blocks
+
+
+def qurl_kv_append(cached_lens, new_lens, block_table, block_size, free_pages, n_free, n_free_out, slot_mapping,
+                   positions, cu_new, seq_lens, stream=None):
+    """Slots, positions and pages for a step's new tokens (see include/qurl.h)."""
+    _here(cached_lens, new_lens, block_table, free_pages, n_free, n_free_out, slot_mapping, positions, cu_new, seq_lens)
+    B, M = cached_lens.numel(), slot_mapping.numel()
+    ld, blocks = _pages(B, block_table, free_pages)
+    cached, new, lens = _vec(torch.int32, B, (cached_lens, "cached_lens"), (new_lens, "new_lens"), (seq_lens, "seq_lens"))
+    n, n_out = _vec(torch.int32, 1, (n_free, "n_free"), (n_free_out, "n_free_out"))
+    cu, = _vec(torch.int32, B + 1, (cu_new, "cu_new"))
+    pos, = _vec(torch.int32, M, (positions, "positions"))
+    slots, = _vec(torch.int64, M, (slot_mapping, "slot_mapping"))
+    _ok(load().qurl_kv_append(cached, new, B, block_table.data_ptr(), ld, blocks, block_size, free_pages.data_ptr(),
+                              free_pages.numel(), n, n_out, M, slots, pos, cu, lens, _stream(stream)), "qurl_kv_append")
+
+
+def qurl_kv_release(lens, block_table, block_size, free_pages, n_free, n_free_out, keep_lens=None, stream=None):
+    """Pages given back to the list of free ones (see include/qurl.h)."""
+    _here(lens, block_table, free_pages, n_free, n_free_out, keep_lens)
+    B = lens.numel()
+    ld, blocks = _pages(B, block_table, free_pages)
+    at, keep = _vec(torch.int32, B, (lens, "lens"), (keep_lens, "keep_lens"))
+    n, n_out = _vec(torch.int32, 1, (n_free, "n_free"), (n_free_out, "n_free_out"))
+    _ok(load().qurl_kv_release(at, keep, B, block_table.data_ptr(), ld, blocks, block_size, free_pages.data_ptr(),
+                               free_pages.numel(), n, n_out, _stream(stream)), "qurl_kv_release")
+
+
 def qurl_residual_rmsnorm_quant(H, Y, gamma_folded, qt, H_out, Xq, sx, gamma_post=None, gate=None, residual_scale=1.0,
                                 eps=1e-6, eps_post=1e-6, ms_out=None, stream=None):
     """H_out = H + residual_scale * gate * RMSNorm(Y), then RMSNorm and per-token
@@ -592,6 +698,99 @@ def kv_attn_decode(q, q_heads, k_cache, k_scale, v_cache, v_scale, block_table, 
     qurl_kv_attn_decode(q, q_heads, k_cache, k_scale, v_cache, v_scale, block_table, block_size, seq_lens,
                         hd ** -0.5 if scale is None else scale, out, ws, window, lse, stream)
     return (out, lse) if want_lse else out
+
+
+def kv_pages(num_pages, device="cuda"):
+    """A list of num_pages free pages, the lowest handed out first: (free_pages, n_free)."""
+    return (torch.arange(num_pages - 1, -1, -1, dtype=torch.int32, device=device),
+            torch.full((1,), num_pages, dtype=torch.int32, device=device))
+
+
+@_for_stream
+def kv_append(cached_lens, new_lens, block_table, block_size, free_pages, n_free, num_tokens, n_free_out=None,
+              stream=None):
+    """Places a step's new tokens, num_tokens rows at most, taking the pages they need; block_table and
+    n_free (or n_free_out) are updated.  Returns (slot_mapping, positions, cu_new, seq_lens)."""
+    B, dev = cached_lens.numel(), cached_lens.device
+    slots = torch.empty(num_tokens, dtype=torch.int64, device=dev)
+    pos = torch.empty(num_tokens, dtype=torch.int32, device=dev)
+    cu = torch.empty(B + 1, dtype=torch.int32, device=dev)
+    lens = torch.empty(B, dtype=torch.int32, device=dev)
+    qurl_kv_append(cached_lens, new_lens, block_table, block_size, free_pages, n_free,
+                   n_free if n_free_out is None else n_free_out, slots, pos, cu, lens, stream)
+    return slots, pos, cu, lens
+
+
+def kv_release(lens, block_table, block_size, free_pages, n_free, keep_lens=None, n_free_out=None, stream=None):
+    """Gives the pages behind the first keep_lens tokens back; free_pages and n_free (or n_free_out) are updated."""
+    qurl_kv_release(lens, block_table, block_size, free_pages, n_free, n_free if n_free_out is None else n_free_out,
+                    keep_lens, stream)
+
+
+def rope_frequencies(rot_dim, base=10000.0, scaling=None, factor=1.0, original_len=0, low_turns=1.0, high_turns=32.0,
+                     device="cuda"):
+    """Radians a position of each of a head's rot_dim / 2 pairs, base ** (-2 i / rot_dim), and the factor on the
+    rotated values: (inv_freq fp64 on the device, float).  For contexts `factor` times as long as original_len, the
+    one trained on, scaling is
+      "linear"  every frequency divided by factor;
+      "base"    the base raised so that the slowest pair is divided by factor and the fastest stays;
+      "ramp"    pairs that make fewer than low_turns turns over original_len divided by factor, those of more than
+                high_turns kept, a linear ramp in the turns between;
+      "yarn"    the same with a ramp in the pair's index, the ends rounded outwards to whole pairs, and the rotated
+                values multiplied by 1 + 0.1 ln(factor)."""
+    if rot_dim <= 0 or rot_dim % 2 or not base > 0 or not factor > 0:
+        raise ValueError("rot_dim is even and positive, base and factor are positive")
+    i = torch.arange(0, rot_dim, 2, dtype=torch.float64) / rot_dim
+    freq, scale = base ** -i, 1.0
+    if scaling == "linear":
+        freq = freq / factor
+    elif scaling == "base":
+        if rot_dim > 2:
+            freq = (base * factor ** (rot_dim / (rot_dim - 2))) ** -i
+    elif scaling in ("ramp", "yarn"):
+        if original_len <= 0 or not 0 < low_turns < high_turns:
+            raise ValueError("scaling by turns takes original_len and 0 < low_turns < high_turns")
+        if scaling == "ramp":
+            keep = (original_len * freq / (2 * math.pi) - low_turns) / (high_turns - low_turns)
+        else:
+            # the pair that makes a number of turns over original_len
+            pair = lambda turns: rot_dim * math.log(original_len / (2 * math.pi * turns)) / (2 * math.log(base))  # noqa: E731
+            low, high = max(math.floor(pair(high_turns)), 0), min(math.ceil(pair(low_turns)), rot_dim - 1)
+            keep = 1 - (torch.arange(rot_dim // 2, dtype=torch.float64) - low) / max(high - low, 0.001)
+            scale = 1.0 + 0.1 * math.log(factor) if factor > 1 else 1.0
+        keep = keep.clamp(0.0, 1.0)
+        freq = freq * keep + freq / factor * (1 - keep)
+    elif scaling is not None:
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return freq.to(device), scale
+
+
+@_for_stream
+def rope(X, heads, positions, inv_freq, head_dim=None, layout=ROPE_HALF, factor=1.0, inverse=False, inplace=False,
+         stream=None):
+    """Rotary positions of X [M, heads * head_dim]; inverse gives the gradient's rotation.  head_dim defaults to the
+    columns over heads."""
+    hd = X.shape[1] // heads if head_dim is None else head_dim
+    if head_dim is None and X.shape[1] != heads * hd:
+        raise ValueError("X has heads * head_dim columns (give head_dim for wider rows)")
+    if inplace:
+        out = X
+    else:
+        out = torch.empty((X.shape[0], heads * hd), dtype=X.dtype, device=X.device)
+    qurl_rope(X, heads, hd, positions, inv_freq, out, layout, factor, inverse, stream)
+    return out
+
+
+@_for_stream
+def rope_kv_cache_quant(qkv, q_heads, positions, inv_freq, slot_mapping, k_cache, k_scale, v_cache, v_scale,
+                        layout=ROPE_HALF, factor=1.0, inplace=False, stream=None):
+    """Rotates queries and keys of the fused qkv output and quantizes keys and values into the cache.  Returns the
+    queries [M, q_heads * head_dim]; with inplace they stay in qkv, which is returned."""
+    q_out = qkv if inplace else torch.empty((qkv.shape[0], q_heads * k_cache.shape[2]), dtype=torch.bfloat16,
+                                            device=qkv.device)
+    qurl_rope_kv_cache_quant(qkv, q_heads, positions, inv_freq, q_out, slot_mapping, k_cache, k_scale, v_cache, v_scale,
+                             layout, factor, stream)
+    return q_out
 
 
 @_for_stream

@@ -171,6 +171,29 @@ qurl_status check_gemm(const void* Xq, const void* Wq, int M, int N, int K, int 
 }
 
 // Rows of logits (bf16 or fp32) of V values, row stride ld elements.
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// The table and the list of free pages of qurl_kv_append and qurl_kv_release.
+qurl_status check_pages(int B, const void* table, int ld_table, int max_blocks, int block_size, const void* free_pages,
+                        int num_pages, const void* n_free, const void* n_free_out) {
+  if (B < 0 || max_blocks < 0 || block_size <= 0 || ld_table < max_blocks || num_pages < 0 || !n_free || !n_free_out ||
+      (num_pages > 0 && !free_pages) || (B > 0 && max_blocks > 0 && !table))
+    return QURL_ERR_INVALID_ARG;
+  if (B > qurl::kMaxRequests || static_cast<long long>(max_blocks) * block_size > (1LL << 30) ||
+      static_cast<long long>(B) * max_blocks >= (1LL << 31))
+    return QURL_ERR_UNSUPPORTED;
+  if (!aligned4(table) || !aligned4(free_pages) || !aligned4(n_free) || !aligned4(n_free_out)) return QURL_ERR_ALIGNMENT;
+  return QURL_OK;
+}
+
+qurl_status check_rope(int M, int heads, int head_dim, int rot_dim, int layout, float factor) {
+  if (M < 0 || heads <= 0 || head_dim <= 0 || rot_dim <= 0 || rot_dim > head_dim || rot_dim % 2 != 0 ||
+      (layout != QURL_ROPE_HALF && layout != QURL_ROPE_INTERLEAVED) || !std::isfinite(factor))
+    return QURL_ERR_INVALID_ARG;
+  if (head_dim % 16 != 0 || head_dim > 256) return QURL_ERR_UNSUPPORTED;
+  return QURL_OK;
+}
+
 qurl_status check_logits(const void* x, int type, int V, int ld) {
   if (!x || !valid_dim(V) || ld < V || (type != QURL_BF16 && type != QURL_FP32)) return QURL_ERR_INVALID_ARG;
   if (V > (1 << 30)) return QURL_ERR_UNSUPPORTED;
@@ -960,6 +983,145 @@ qurl_status qurl_kv_attn_decode(const void* q, int ldq, int B, int q_heads, int 
   a.ws = workspace;
   a.status = dev->status;
   QURL_CUDA(qurl::launch_kv_attn_decode(a, dev->num_sms, reinterpret_cast<cudaStream_t>(stream)));
+  return QURL_OK;
+}
+
+qurl_status qurl_kv_append(const int32_t* cached_lens, const int32_t* new_lens, int B, int32_t* block_table,
+                           int ld_table, int max_blocks, int block_size, const int32_t* free_pages, int num_pages,
+                           const int32_t* n_free, int32_t* n_free_out, int M, int64_t* slot_mapping,
+                           int32_t* positions, int32_t* cu_new, int32_t* seq_lens, qurl_stream_t stream) {
+  QURL_TRY(check_pages(B, block_table, ld_table, max_blocks, block_size, free_pages, num_pages, n_free, n_free_out));
+  if (M < 0 || !cu_new || (B > 0 && (!cached_lens || !new_lens || !seq_lens)) || (M > 0 && (!slot_mapping || !positions)))
+    return QURL_ERR_INVALID_ARG;
+  if (!aligned4(cached_lens) || !aligned4(new_lens) || !aligned4(positions) || !aligned4(cu_new) ||
+      !aligned4(seq_lens) || (reinterpret_cast<uintptr_t>(slot_mapping) & 7u) != 0)
+    return QURL_ERR_ALIGNMENT;
+  DevState* dev = nullptr;
+  QURL_TRY(device_state(&dev));
+  qurl::KvAppendArgs a{};
+  a.cached = cached_lens;
+  a.fresh = new_lens;
+  a.B = B;
+  a.table = block_table;
+  a.ld_table = ld_table;
+  a.max_blocks = max_blocks;
+  a.block_size = block_size;
+  a.free_pages = free_pages;
+  a.capacity = num_pages;
+  a.n_free = n_free;
+  a.n_free_out = n_free_out;
+  a.M = M;
+  a.slots = reinterpret_cast<long long*>(slot_mapping);
+  a.positions = positions;
+  a.cu = cu_new;
+  a.seq_lens = seq_lens;
+  a.status = dev->status;
+  QURL_CUDA(qurl::launch_kv_append(a, reinterpret_cast<cudaStream_t>(stream)));
+  return QURL_OK;
+}
+
+qurl_status qurl_kv_release(const int32_t* lens, const int32_t* keep_lens, int B, const int32_t* block_table,
+                            int ld_table, int max_blocks, int block_size, int32_t* free_pages, int num_pages,
+                            const int32_t* n_free, int32_t* n_free_out, qurl_stream_t stream) {
+  QURL_TRY(check_pages(B, block_table, ld_table, max_blocks, block_size, free_pages, num_pages, n_free, n_free_out));
+  if (B > 0 && !lens) return QURL_ERR_INVALID_ARG;
+  if (!aligned4(lens) || !aligned4(keep_lens)) return QURL_ERR_ALIGNMENT;
+  DevState* dev = nullptr;
+  QURL_TRY(device_state(&dev));
+  qurl::KvReleaseArgs a{};
+  a.lens = lens;
+  a.keep = keep_lens;
+  a.B = B;
+  a.table = block_table;
+  a.ld_table = ld_table;
+  a.max_blocks = max_blocks;
+  a.block_size = block_size;
+  a.free_pages = free_pages;
+  a.capacity = num_pages;
+  a.n_free = n_free;
+  a.n_free_out = n_free_out;
+  a.status = dev->status;
+  QURL_CUDA(qurl::launch_kv_release(a, reinterpret_cast<cudaStream_t>(stream)));
+  return QURL_OK;
+}
+
+qurl_status qurl_rope(const void* X, qurl_ftype x_type, int M, int ldx, int heads, int head_dim,
+                      const int32_t* positions, const double* inv_freq, int rot_dim, qurl_rope_layout layout, float factor,
+                      int inverse, void* out, int ldo, qurl_stream_t stream) {
+  QURL_TRY(check_rope(M, heads, head_dim, rot_dim, layout, factor));
+  if (x_type != QURL_BF16 && x_type != QURL_FP32) return QURL_ERR_INVALID_ARG;
+  if (inverse != 0 && inverse != 1) return QURL_ERR_INVALID_ARG;
+  const long long cols = static_cast<long long>(heads) * head_dim;
+  if (ldx < cols || ldo < cols) return QURL_ERR_INVALID_ARG;
+  if (M == 0) return QURL_OK;
+  if (!X || !out || !positions || !inv_freq || (out == X && ldo != ldx)) return QURL_ERR_INVALID_ARG;
+  const long long size = x_type == QURL_FP32 ? 4 : 2;
+  if (!aligned16(X) || !aligned16(out) || (ldx * size) % 16 != 0 || (ldo * size) % 16 != 0 || !aligned4(positions) ||
+      (reinterpret_cast<uintptr_t>(inv_freq) & 7u) != 0)
+    return QURL_ERR_ALIGNMENT;
+  DevState* dev = nullptr;
+  QURL_TRY(device_state(&dev));
+  qurl::RopeArgs a{};
+  a.x = X;
+  a.ldx = ldx;
+  a.out = out;
+  a.ldo = ldo;
+  a.M = M;
+  a.heads = heads;
+  a.head_dim = head_dim;
+  a.rot = rot_dim;
+  a.interleaved = layout == QURL_ROPE_INTERLEAVED;
+  a.inverse = inverse != 0;
+  a.positions = positions;
+  a.inv_freq = inv_freq;
+  a.factor = factor;
+  a.status = dev->status;
+  QURL_CUDA(qurl::launch_rope(a, x_type == QURL_FP32, false, dev->num_sms, reinterpret_cast<cudaStream_t>(stream)));
+  return QURL_OK;
+}
+
+qurl_status qurl_rope_kv_cache_quant(const void* qkv, int M, int ldq, int q_heads, int kv_heads, int head_dim,
+                                     const int32_t* positions, const double* inv_freq, int rot_dim, qurl_rope_layout layout,
+                                     float factor, void* q_out, int ldo, const int64_t* slot_mapping,
+                                     long long num_slots, void* k_cache, float* k_scale, void* v_cache,
+                                     float* v_scale, qurl_stream_t stream) {
+  QURL_TRY(check_rope(M, q_heads, head_dim, rot_dim, layout, factor));
+  if (kv_heads <= 0 || num_slots < 0) return QURL_ERR_INVALID_ARG;
+  const long long q_dim = static_cast<long long>(q_heads) * head_dim, kv_dim = static_cast<long long>(kv_heads) * head_dim;
+  if (ldq < q_dim + 2 * kv_dim || ldo < q_dim) return QURL_ERR_INVALID_ARG;
+  if (M == 0) return QURL_OK;
+  if (!qkv || !positions || !inv_freq || !q_out || !slot_mapping || !k_cache || !k_scale || !v_cache || !v_scale ||
+      (q_out == qkv && ldo != ldq))
+    return QURL_ERR_INVALID_ARG;
+  if (!aligned16(qkv) || !aligned16(q_out) || (static_cast<long long>(ldq) * 2) % 16 != 0 ||
+      (static_cast<long long>(ldo) * 2) % 16 != 0 || !aligned16(k_cache) || !aligned16(v_cache) || !aligned4(positions) ||
+      (reinterpret_cast<uintptr_t>(inv_freq) & 7u) != 0 || (reinterpret_cast<uintptr_t>(slot_mapping) & 7u) != 0 ||
+      !aligned4(k_scale) || !aligned4(v_scale))
+    return QURL_ERR_ALIGNMENT;
+  DevState* dev = nullptr;
+  QURL_TRY(device_state(&dev));
+  qurl::RopeArgs a{};
+  a.x = qkv;
+  a.ldx = ldq;
+  a.out = q_out;
+  a.ldo = ldo;
+  a.M = M;
+  a.heads = q_heads;
+  a.head_dim = head_dim;
+  a.rot = rot_dim;
+  a.interleaved = layout == QURL_ROPE_INTERLEAVED;
+  a.positions = positions;
+  a.inv_freq = inv_freq;
+  a.factor = factor;
+  a.kv_heads = kv_heads;
+  a.slots = reinterpret_cast<const long long*>(slot_mapping);
+  a.num_slots = num_slots;
+  a.k_cache = reinterpret_cast<uint8_t*>(k_cache);
+  a.k_scale = k_scale;
+  a.v_cache = reinterpret_cast<uint8_t*>(v_cache);
+  a.v_scale = v_scale;
+  a.status = dev->status;
+  QURL_CUDA(qurl::launch_rope(a, false, true, dev->num_sms, reinterpret_cast<cudaStream_t>(stream)));
   return QURL_OK;
 }
 

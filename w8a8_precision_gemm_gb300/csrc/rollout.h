@@ -73,6 +73,68 @@ struct AttnArgs {
 size_t attn_workspace_bytes(int q_heads, int kv_heads, int head_dim, int num_sms);
 cudaError_t launch_kv_attn_decode(const AttnArgs& a, int num_sms, cudaStream_t st);
 
+// pages.cu: pages for a step's new tokens (qurl_kv_append), and pages given back
+// (qurl_kv_release).
+constexpr int kMaxRequests = 16384;  // the lengths' prefix sums lie in shared memory
+struct KvAppendArgs {
+  const int* cached;
+  const int* fresh;
+  int B;
+  int* table;
+  long long ld_table;
+  int max_blocks, block_size;
+  const int* free_pages;
+  int capacity;
+  const int* n_free;
+  int* n_free_out;
+  int M;
+  long long* slots;
+  int* positions;
+  int* cu;
+  int* seq_lens;
+  int* status;
+};
+cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t st);
+struct KvReleaseArgs {
+  const int* lens;
+  const int* keep;  // null: 0
+  int B;
+  const int* table;
+  long long ld_table;
+  int max_blocks, block_size;
+  int* free_pages;
+  int capacity;
+  const int* n_free;
+  int* n_free_out;
+  int* status;
+};
+cudaError_t launch_kv_release(const KvReleaseArgs& a, cudaStream_t st);
+
+// rope.cu: rotary positions, alone or with the quantization into the cache.
+struct RopeArgs {
+  const void* x;
+  long long ldx;
+  void* out;  // may be x
+  long long ldo;
+  long long M;
+  int heads, head_dim, rot;  // rotated heads (cache: query heads, then kv_heads keys and kv_heads values)
+  bool interleaved, inverse;
+  const int* positions;
+  const double* inv_freq;
+  float factor;
+  int group;  // lanes per head, set by the launch
+  // with the cache
+  int kv_heads;
+  const long long* slots;
+  long long num_slots;
+  uint8_t* k_cache;
+  float* k_scale;
+  uint8_t* v_cache;
+  float* v_scale;
+  int* status;
+};
+cudaError_t launch_rope(const RopeArgs& a, bool f32, bool cache, int num_sms, cudaStream_t st);
+
 // sample.cu: one token per row of logits from a given uniform number (qurl_sample).
 struct SampleArgs {
   const void* logits;
