@@ -529,6 +529,44 @@ qurl_status qurl_kv_attn_decode(const void* q, int ldq, int B, int q_heads, int 
                                 float* lse, void* workspace, size_t ws_bytes, qurl_stream_t stream);
 
 /*
+ * Causal attention of several new tokens per sequence over the same cache (a prompt, a
+ * chunk of one behind cached tokens, draft tokens to be verified; single tokens and
+ * sequences without any may be among them), once the new tokens' keys and values are in it.  Sequence
+ * b's new tokens are rows cu_new[b] .. cu_new[b + 1] - 1 of q, the last of its seq_lens[b] tokens: row
+ * cu_new[b] + i stands at position p = seq_lens[b] - (cu_new[b + 1] - cu_new[b]) + i and sees the cached
+ * tokens j <= p and, with window > 0, j > p - window.  Scores, weights, out and lse
+ * as in qurl_kv_attn_decode, a row of q in the place of a sequence's.  A row that sees no token (p < 0) gets out = 0 and
+ * lse = -inf.  Rows of q, out and lse outside cu_new[0] .. cu_new[B] - 1 (padding) are neither read nor written.
+ *   q            [M, ldq] bf16, finite, the q_heads * head_dim query columns first.
+ *   caches, block_table [B, ld_table], window, scale   as in qurl_kv_attn_decode.
+ *   cu_new       [B + 1] int32, not decreasing, within [0, M] (as qurl_kv_append gives it).
+ *   seq_lens     [B] int32, the new tokens included; negative counts as 0.
+ *   out          [M, ldo] bf16, not overlapping q.     lse [M, q_heads] fp32 or NULL.
+ *   workspace    qurl_kv_attn_chunk_workspace_size(...) bytes or more (the size goes by head_dim; one
+ *                workspace serves calls of any other layout it is large enough for), 16-byte aligned, ZERO-FILLED
+ *                before its first use: it holds counters that every call leaves zero.  Calls that
+ *                may run at the same time need separate workspaces; qurl_kv_attn_decode's is another.
+ * Lengths, rows and pages are read on the device: a token whose page is negative or past num_slots is left out,
+ * a length past max_blocks * block_size is cut to it, rows past M or in decreasing order count as none, and
+ * each latches QURL_ERR_INVALID_ARG in the device status word.
+ * Sums are fp32.  A weight softmax(s)_j * v_scale is within 2^-11 of its value, or 2^-27 of the row's largest, whatever the
+ * tokens' scales from 2^-100 to 2^100; for scores of 2^24 and more (in log2 units), which are not told apart from
+ * their neighbours, scales from 2^-14 to 2^15.  Results are identical run to run.
+ * B = 0 and M = 0 are valid.  Errors: INVALID_ARG (NULL, a size out of range, q_heads % kv_heads, ld_table <
+ * max_blocks, window < 0, scale not finite), UNSUPPORTED (head_dim; M * q_heads of 2^31 or more, max_blocks *
+ * block_size above 2^30, B above 16384), ALIGNMENT, WORKSPACE.  One kernel launch.  If its bounded waits run out, or a
+ * timeout of an earlier kernel was still latched when it ran (QURL_ERR_TIMEOUT), zero the workspace before its
+ * next use.
+ */
+size_t qurl_kv_attn_chunk_workspace_size(int q_heads, int kv_heads, int head_dim);
+qurl_status qurl_kv_attn_chunk(const void* q, int ldq, int M, int q_heads, int kv_heads, int head_dim,
+                               const void* k_cache, const float* k_scale, const void* v_cache, const float* v_scale,
+                               long long num_slots, const int32_t* block_table, int ld_table, int max_blocks,
+                               int block_size, const int32_t* cu_new, const int32_t* seq_lens, int B, int window,
+                               float scale, void* out, int ldo, float* lse, void* workspace, size_t ws_bytes,
+                               qurl_stream_t stream);
+
+/*
  * The residual update between two blocks of a layer with the norms on both
  * sides of it, then per-token quantization for the next projection ([UAQ] fold
  * into the norm, [LOSS]).  Per token m:

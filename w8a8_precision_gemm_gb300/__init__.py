@@ -103,6 +103,8 @@ def load() -> ctypes.CDLL:
             "qurl_kv_cache_dequant": [P, P, P, i, i, i, ctypes.c_longlong, P, P],
             "qurl_kv_attn_decode": [P, i, i, i, i, i, P, P, P, P, ctypes.c_longlong, P, i, i, i, P, i, f, P, i, P, P,
                                     z, P],
+            "qurl_kv_attn_chunk": [P, i, i, i, i, i, P, P, P, P, ctypes.c_longlong, P, i, i, i, P, P, i, i, f, P, i, P, P, z,
+                                   P],
             "qurl_rope": [P, i, i, i, i, i, P, P, i, i, f, i, P, i, P],
             "qurl_rope_kv_cache_quant": [P, i, i, i, i, i, P, P, i, i, f, P, i, P, ctypes.c_longlong, P, P, P, P, P],
             "qurl_kv_append": [P, P, i, P, i, i, i, P, i, P, P, i, P, P, P, P, P],
@@ -124,6 +126,8 @@ def load() -> ctypes.CDLL:
         L.qurl_nvfp4_workspace_size.restype = ctypes.c_size_t
         L.qurl_kv_attn_workspace_size.argtypes = [i, i, i, i, i, i]
         L.qurl_kv_attn_workspace_size.restype = ctypes.c_size_t
+        L.qurl_kv_attn_chunk_workspace_size.argtypes = [i, i, i]
+        L.qurl_kv_attn_chunk_workspace_size.restype = ctypes.c_size_t
         L.qurl_acr_workspace_size.argtypes = []
         L.qurl_acr_workspace_size.restype = ctypes.c_size_t
         L.qurl_status_string.argtypes = [ctypes.c_int]
@@ -389,6 +393,40 @@ def qurl_kv_attn_decode(q, q_heads, k_cache, k_scale, v_cache, v_scale, block_ta
                                    out.data_ptr(), _ld(out), lse_at, workspace.data_ptr(),
                                    workspace.numel() * workspace.element_size(), _stream(stream)),
         "qurl_kv_attn_decode")
+
+
+def qurl_kv_attn_chunk_workspace_size(q_heads, kv_heads, head_dim) -> int:
+    return int(load().qurl_kv_attn_chunk_workspace_size(q_heads, kv_heads, head_dim))
+
+
+def qurl_kv_attn_chunk(q, q_heads, k_cache, k_scale, v_cache, v_scale, block_table, block_size, cu_new, seq_lens, scale,
+                       out, workspace, window=0, lse=None, stream=None):
+    """Causal attention of several new tokens per sequence, rows of q [M, >= q_heads * head_dim], over the
+    paged FP8 cache (see include/qurl.h)."""
+    _here(q, k_cache, k_scale, v_cache, v_scale, block_table, cu_new, seq_lens, out, workspace, lse)
+    num_slots, kv_heads, head_dim = shape = k_cache.shape
+    M, columns = q.shape
+    B, max_blocks = block_table.shape
+    if (v_cache.shape != shape or k_cache.element_size() != 1 or v_cache.element_size() != 1
+            or not k_cache.is_contiguous() or not v_cache.is_contiguous()):
+        raise ValueError("caches are contiguous, 8-bit, [slots, kv_heads, head_dim]")
+    if q.dtype is not torch.bfloat16 or out.dtype is not torch.bfloat16 or out.shape[0] != M:
+        raise ValueError("q and out are bf16 [M, ...]")
+    if min(columns, out.shape[1]) < q_heads * head_dim:
+        raise ValueError("q and out have q_heads * head_dim columns at least")
+    if block_table.dtype is not torch.int32:
+        raise ValueError("block_table is int32 [B, blocks]")
+    _dense(workspace)
+    ks, vs = _vec(torch.float32, num_slots * kv_heads, (k_scale, "k_scale"), (v_scale, "v_scale"))
+    lens, = _vec(torch.int32, B, (seq_lens, "seq_lens"))
+    cu, = _vec(torch.int32, B + 1, (cu_new, "cu_new"))
+    lse_at, = _vec(torch.float32, M * q_heads, (lse, "lse"))
+    _ok(load().qurl_kv_attn_chunk(q.data_ptr(), _ld(q), M, q_heads, kv_heads, head_dim, k_cache.data_ptr(), ks,
+                                  v_cache.data_ptr(), vs, num_slots, block_table.data_ptr(),
+                                  _ld(block_table) if max_blocks else 0, max_blocks, block_size, cu, lens, B, window,
+                                  scale, out.data_ptr(), _ld(out), lse_at, workspace.data_ptr(),
+                                  workspace.numel() * workspace.element_size(), _stream(stream)),
+        "qurl_kv_attn_chunk")
 
 
 def _rotation(M, head_dim, positions, inv_freq):
@@ -697,6 +735,29 @@ def kv_attn_decode(q, q_heads, k_cache, k_scale, v_cache, v_scale, block_table, 
     lse = torch.empty((B, q_heads), dtype=torch.float32, device=q.device) if want_lse else None
     qurl_kv_attn_decode(q, q_heads, k_cache, k_scale, v_cache, v_scale, block_table, block_size, seq_lens,
                         hd ** -0.5 if scale is None else scale, out, ws, window, lse, stream)
+    return (out, lse) if want_lse else out
+
+
+def kv_attn_chunk_workspace(q_heads, kv_heads, head_dim, device="cuda") -> torch.Tensor:
+    """Scratch for kv_attn_chunk calls of this head layout, any batch, zero-filled once (its counters) and left
+    ready for reuse by every call, one of another layout included where it is large enough."""
+    n = qurl_kv_attn_chunk_workspace_size(q_heads, kv_heads, head_dim)
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+@_for_stream
+def kv_attn_chunk(q, q_heads, k_cache, k_scale, v_cache, v_scale, block_table, block_size, cu_new, seq_lens, scale=None,
+                  window=0, want_lse=False, ws=None, stream=None):
+    """Causal attention of several new tokens per sequence over the paged FP8 cache.  scale defaults to
+    head_dim ** -0.5.  Returns out [M, q_heads * head_dim] bf16, or (out, lse [M, q_heads]); rows behind the last
+    sequence's are not written."""
+    M, (_, kv_heads, hd) = q.shape[0], k_cache.shape
+    if ws is None:
+        ws = kv_attn_chunk_workspace(q_heads, kv_heads, hd, q.device)
+    out = torch.empty((M, q_heads * hd), dtype=torch.bfloat16, device=q.device)
+    lse = torch.empty((M, q_heads), dtype=torch.float32, device=q.device) if want_lse else None
+    qurl_kv_attn_chunk(q, q_heads, k_cache, k_scale, v_cache, v_scale, block_table, block_size, cu_new, seq_lens,
+                       hd ** -0.5 if scale is None else scale, out, ws, window, lse, stream)
     return (out, lse) if want_lse else out
 
 

@@ -986,6 +986,69 @@ qurl_status qurl_kv_attn_decode(const void* q, int ldq, int B, int q_heads, int 
   return QURL_OK;
 }
 
+size_t qurl_kv_attn_chunk_workspace_size(int q_heads, int kv_heads, int head_dim) {
+  if (q_heads <= 0 || kv_heads <= 0 || head_dim <= 0 || q_heads % kv_heads != 0 || head_dim > 256) return 0;
+  return qurl::attn_chunk_workspace_bytes(q_heads, kv_heads, head_dim, device_sms());
+}
+
+qurl_status qurl_kv_attn_chunk(const void* q, int ldq, int M, int q_heads, int kv_heads, int head_dim,
+                               const void* k_cache, const float* k_scale, const void* v_cache, const float* v_scale,
+                               long long num_slots, const int32_t* block_table, int ld_table, int max_blocks,
+                               int block_size, const int32_t* cu_new, const int32_t* seq_lens, int B, int window,
+                               float scale, void* out, int ldo, float* lse, void* workspace, size_t ws_bytes,
+                               qurl_stream_t stream) {
+  if (M < 0 || B < 0 || q_heads <= 0 || kv_heads <= 0 || head_dim <= 0 || num_slots < 0 || max_blocks < 0 ||
+      block_size <= 0 || ld_table < max_blocks || window < 0 || !std::isfinite(scale) || q_heads % kv_heads != 0)
+    return QURL_ERR_INVALID_ARG;
+  if (head_dim % 16 != 0 || head_dim > 256) return QURL_ERR_UNSUPPORTED;
+  const long long q_dim = static_cast<long long>(q_heads) * head_dim;
+  if (ldq < q_dim || ldo < q_dim) return QURL_ERR_INVALID_ARG;
+  if (static_cast<long long>(max_blocks) * block_size > (1LL << 30) ||
+      static_cast<long long>(M) * q_heads >= (1LL << 31) || B > qurl::kMaxRequests)
+    return QURL_ERR_UNSUPPORTED;
+  if (B == 0 || M == 0) return QURL_OK;
+  if (!q || !cu_new || !seq_lens || !out || !workspace || (max_blocks > 0 && !block_table) ||
+      (num_slots > 0 && (!k_cache || !k_scale || !v_cache || !v_scale)))
+    return QURL_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) || !aligned16(workspace) ||
+      (static_cast<long long>(ldq) * 2) % 16 != 0 || (static_cast<long long>(ldo) * 2) % 16 != 0 ||
+      !aligned4(k_scale) || !aligned4(v_scale) || !aligned4(block_table) || !aligned4(cu_new) || !aligned4(seq_lens) ||
+      !aligned4(lse))
+    return QURL_ERR_ALIGNMENT;
+  DevState* dev = nullptr;
+  QURL_TRY(device_state(&dev));
+  if (ws_bytes < qurl::attn_chunk_workspace_bytes(q_heads, kv_heads, head_dim, dev->num_sms))
+    return QURL_ERR_WORKSPACE;
+  qurl::AttnChunkArgs a{};
+  a.q = reinterpret_cast<const __nv_bfloat16*>(q);
+  a.ldq = ldq;
+  a.M = M;
+  a.B = B;
+  a.q_heads = q_heads;
+  a.kv_heads = kv_heads;
+  a.head_dim = head_dim;
+  a.k_cache = reinterpret_cast<const uint8_t*>(k_cache);
+  a.k_scale = k_scale;
+  a.v_cache = reinterpret_cast<const uint8_t*>(v_cache);
+  a.v_scale = v_scale;
+  a.num_slots = num_slots;
+  a.block_table = block_table;
+  a.ld_table = ld_table;
+  a.max_blocks = max_blocks;
+  a.block_size = block_size;
+  a.cu_new = cu_new;
+  a.seq_lens = seq_lens;
+  a.window = window;
+  a.scale = scale;
+  a.out = reinterpret_cast<__nv_bfloat16*>(out);
+  a.ldo = ldo;
+  a.lse = lse;
+  a.ws = workspace;
+  a.status = dev->status;
+  QURL_CUDA(qurl::launch_kv_attn_chunk(a, dev->num_sms, reinterpret_cast<cudaStream_t>(stream)));
+  return QURL_OK;
+}
+
 qurl_status qurl_kv_append(const int32_t* cached_lens, const int32_t* new_lens, int B, int32_t* block_table,
                            int ld_table, int max_blocks, int block_size, const int32_t* free_pages, int num_pages,
                            const int32_t* n_free, int32_t* n_free_out, int M, int64_t* slot_mapping,

@@ -73,6 +73,33 @@ struct AttnArgs {
 size_t attn_workspace_bytes(int q_heads, int kv_heads, int head_dim, int num_sms);
 cudaError_t launch_kv_attn_decode(const AttnArgs& a, int num_sms, cudaStream_t st);
 
+// attn_chunk.cu: causal attention of several new tokens per sequence over the same
+// cache (qurl_kv_attn_chunk), and the workspace it needs.
+struct AttnChunkArgs {
+  const __nv_bfloat16* q;
+  long long ldq;
+  int M, B, q_heads, kv_heads, head_dim;
+  const uint8_t* k_cache;
+  const float* k_scale;
+  const uint8_t* v_cache;
+  const float* v_scale;
+  long long num_slots;
+  const int* block_table;
+  long long ld_table;
+  int max_blocks, block_size;
+  const int* cu_new;    // [B + 1]
+  const int* seq_lens;  // [B], the new tokens included
+  int window;
+  float scale;
+  __nv_bfloat16* out;
+  long long ldo;
+  float* lse;  // null: not wanted
+  void* ws;
+  int* status;
+};
+size_t attn_chunk_workspace_bytes(int q_heads, int kv_heads, int head_dim, int num_sms);
+cudaError_t launch_kv_attn_chunk(const AttnChunkArgs& a, int num_sms, cudaStream_t st);
+
 // pages.cu: pages for a step's new tokens (qurl_kv_append), and pages given back
 // (qurl_kv_release).
 constexpr int kMaxRequests = 16384;  // the lengths' prefix sums lie in shared memory
