@@ -53,33 +53,45 @@ namespace {
 
 constexpr int kSoftmax = 256;     // threads 0..255: two groups of 128, a row a thread
 constexpr int kConverters = 128;  // threads 256..383
-constexpr int kThreads = kSoftmax + kConverters + 32;  // and the MMA warp
+constexpr int kThreads = 512;     // and two warps that issue the MMAs, one that hands out the segments, one without work
+// Registers a thread: 128 at launch (512 threads), moved between the warpgroups: the softmax threads' loop over 32
+// scores at a time needs room to overlap its loads, products and exponentials.
+constexpr int kRegsSoftmax = 176, kRegsConvert = 80, kRegsMma = 80;
+static_assert(2 * kRegsSoftmax + kRegsConvert + kRegsMma <= 4 * 128, "registers at launch");
 constexpr int kRing = 8;          // tiles whose scales are kept
+constexpr int kSegments = 4;      // segments handed out ahead
 // What a unit costs beside its tiles, in tiles of one row tile, and the least that a range gets.
 constexpr int kUnitCost = 2;
 constexpr int kMinRange = 8;
 constexpr float kWide = 0x1p24f;  // scores from here on are not told apart from their neighbours
+constexpr float kFar = 100.0f;    // a reference lies no further than this below the largest score
+constexpr float kHeavy = 0x1p15f; // weights above this move the reference, and so do exponentials whose sum is above
+constexpr float kMuch = 0x1p110f;
 
-// PANELS: 64-column panels of a head.
+// PANELS: 64-column panels of a head's values as fp16.
 template <int PANELS_>
 struct ChunkCfg {
   static constexpr int PANELS = PANELS_;
+  static constexpr int CODE_PANELS = (PANELS + 1) / 2; // 128-column panels of a head in 8 bits
   static constexpr int TILES = PANELS <= 2 ? 2 : 1;    // row tiles
   static constexpr int ROWS = 128 * TILES;
   static constexpr int BN = PANELS <= 2 ? 128 : 64;    // tokens per tile
-  static constexpr int STAGES = 2;
-  static constexpr int Q_BYTES = PANELS * 128 * 128;   // a row tile of queries
-  static constexpr int KV_BYTES = PANELS * BN * 128;   // a tile of keys, or of values
-  static constexpr int OFF_K = TILES * Q_BYTES;
-  static constexpr int OFF_V = OFF_K + STAGES * KV_BYTES;
-  static constexpr int SMEM = OFF_V + STAGES * KV_BYTES + 1024;
+  static constexpr int K_STAGES = 3, V_STAGES = 2, RAW_STAGES = 2;
+  static constexpr int Q_PIECE = CODE_PANELS * 128 * 128;  // a row tile of queries, one of the two pieces
+  static constexpr int K_BYTES = CODE_PANELS * BN * 128;   // a tile of keys
+  static constexpr int V_BYTES = PANELS * BN * 128;        // a tile of values as fp16
   static constexpr int LANES = PANELS == 1 ? 4 : PANELS == 2 ? 8 : 16;  // lanes per token row in the gather
   static constexpr int WARP_ROWS = BN / 4;             // token rows of a tile per converter warp
   static constexpr int LOADS = WARP_ROWS * LANES / 32; // 16-byte pieces per lane, keys and values each
+  static constexpr int RAW_BYTES = LOADS * kConverters * 16;  // a tile of value codes as they come
+  static constexpr int OFF_K = TILES * 2 * Q_PIECE;
+  static constexpr int OFF_V = OFF_K + K_STAGES * K_BYTES;
+  static constexpr int OFF_RAW = OFF_V + V_STAGES * V_BYTES;
+  static constexpr int SMEM = OFF_RAW + RAW_STAGES * RAW_BYTES + 1024;
   static constexpr int TM_S = BN;                      // columns between the two score buffers
   static constexpr int TM_O = 256;                     // first column of the outputs (64 PANELS per row tile)
   static_assert(2 * TM_S <= TM_O && TM_O + TILES * 64 * PANELS <= 512, "TMEM columns");
-  static_assert(SMEM <= 216 * 1024, "shared memory");
+  static_assert(SMEM <= 212 * 1024, "shared memory");
 };
 
 struct ChunkPlan {
@@ -98,28 +110,51 @@ __device__ __forceinline__ float lg2(float x) {
   asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));  // (subnormal scales too)
   return y;
 }
-__device__ __forceinline__ float warp_fmax(float v) {
-  float r;
-  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-  return r;
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+// One arrival on `bar` once this thread's earlier cp.async have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 // 2^n, n in [-126, 127], and floor(log2 x) of a normal x > 0 (-127 for zero and subnormals).
 __device__ __forceinline__ float pow2(int n) { return __uint_as_float(static_cast<uint32_t>(n + 127) << 23); }
 __device__ __forceinline__ int exponent(float x) { return static_cast<int>(__float_as_uint(x) >> 23) - 127; }
 
+// A wait that ends as soon as the phase does: without a hint of how long it may take the thread is suspended by the
+// barrier itself, with one it sleeps in between.
+__device__ __forceinline__ bool try_wait_now(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 // mbar_wait (ptx.cuh) that gives up for a timeout only: a page out of range latched by
 // this kernel leaves the other sequences' results alone.
-__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, int* status) {
-  if (mbar_try_wait(bar, parity)) return true;
+__device__ __forceinline__ bool wait_long(uint64_t* bar, uint32_t parity, int* status) {
   const uint64_t t0 = globaltimer_ns();
-  while (!mbar_try_wait(bar, parity)) {
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (try_wait_now(bar, parity)) return true;
     if (*reinterpret_cast<volatile int*>(status) == kDevTimeout) return false;
     if (globaltimer_ns() - t0 > kWaitLimitNs) {
       atomicExch(status, kDevTimeout);
       return false;
     }
   }
-  return true;
+}
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, int* status) {
+  if (try_wait_now(bar, parity)) return true;
+  return wait_long(bar, parity, status);
 }
 // The same for MMAs that this thread has issued itself, whatever the status says:
 // none may still be writing TMEM when it is released.
@@ -154,15 +189,6 @@ __device__ __forceinline__ uint64_t desc_transposed(uint32_t saddr, uint32_t pan
   d |= static_cast<uint64_t>(1u) << 46;
   d |= static_cast<uint64_t>(2u) << 61;
   return d;
-}
-
-// One arrival per thread of the softmax warps, and whether `v` holds in any of them.
-__device__ __forceinline__ bool any_of(bool v) {
-  int r = v ? 1 : 0;
-  asm volatile(
-      "{\n\t.reg .pred a, b;\n\tsetp.ne.s32 a, %0, 0;\n\tbarrier.cta.red.or.pred b, 1, 256, a;\n\tselp.s32 %0, 1, 0, b;\n\t}"
-      : "+r"(r)::"memory");
-  return r != 0;
 }
 
 // A sequence: its rows of q, the tokens it has and those of them that are new.
@@ -201,12 +227,29 @@ __device__ __forceinline__ Unit unit_of(const AttnChunkArgs& a, const Seq& s, in
   return w;
 }
 
+// One unit's tiles inside this CTA's range, as the roles take it from shared memory.
+struct Segment {
+  int n;       // tiles (0: no more segments)
+  int b;       // sequence
+  int head;    // KV head
+  int qrow;    // row of q of the sequence's first new token, and
+  int pos;     // its position
+  int row;     // the unit's first (token, head) pair of the sequence, and
+  int rows;    // how many
+  int first;   // first token of the first tile
+  int stop;    // tokens that the unit's last row sees
+  int part;    // the whole unit: -1; else the place of these partial sums,
+  int r0, r1;  // the first and last range with tiles of the unit
+};
+
 struct Shared {
-  uint64_t kfull[2], kempty[2], vfull[2], vempty[2];  // a stage of keys, of values
+  uint64_t kfull[3], kempty[3], vfull[2], vempty[2];  // a stage of keys, of values
   uint64_t scfull[kRing];                             // the scales of a tile
+  uint64_t sgfull[kSegments], sgempty[kSegments];     // a segment
   uint64_t qfull;                                     // a segment's queries, and its outputs may be overwritten
   uint64_t sfull[2], pfull[2], ofull[2];              // scores, weights (per score buffer), outputs (per row tile)
-  uint64_t drain;
+  uint64_t meet;                                      // the softmax threads
+  uint64_t drain[2];
   uint32_t tmem;
   int ranges;                 // ranges in use
   long long total;            // the cost of all units
@@ -214,9 +257,9 @@ struct Shared {
   // where this CTA's range begins
   int b, u, head;
   long long at;               // cost before that unit
+  Segment segment[kSegments];
   alignas(16) float ks[kRing][128];
   alignas(16) float vs[kRing][128];
-  float vmax[kRing][4], vmin[kRing][4];  // of the scales each converter warp has loaded (0, infinity: none)
   uint32_t valid[kRing][4];   // tokens whose page exists
   int last;
 };
@@ -244,8 +287,7 @@ __device__ __forceinline__ long long cost_of(const AttnChunkArgs& a, const Seq& 
   return sum;
 }
 
-// Walks the segments (one unit's tiles inside this CTA's range) in order; every role
-// walks the same ones.
+// Walks the segments of this CTA's range in order.
 template <class C>
 struct Walk {
   const AttnChunkArgs& a;
@@ -302,19 +344,36 @@ struct Walk {
   }
 };
 
-// 16 codes -> 32 bytes of fp16.
+// 16 codes -> 32 bytes of fp16.  (A code that is no number becomes 512: what lies behind a query's own position
+// meets weights of zero, and must stay out.)
+__device__ __forceinline__ void widen4(uint32_t c, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\t.reg .b32 x, y;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 x, l;\n\tcvt.rn.f16x2.e4m3x2 y, h;\n\t"
+      "min.f16x2 %0, x, %3;\n\tmin.f16x2 %1, y, %3;\n\t}"
+      : "=&r"(lo), "=&r"(hi)
+      : "r"(c), "r"(0x60006000u));
+}
 __device__ __forceinline__ void widen16(const uint4 c, uint4& lo, uint4& hi) {
-  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-  uint32_t o[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[i] & 0xFFFF), __NV_E4M3);
-    const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[i] >> 16), __NV_E4M3);
-    o[2 * i] = static_cast<uint32_t>(a.x) | static_cast<uint32_t>(a.y) << 16;
-    o[2 * i + 1] = static_cast<uint32_t>(b.x) | static_cast<uint32_t>(b.y) << 16;
-  }
-  lo = make_uint4(o[0], o[1], o[2], o[3]);
-  hi = make_uint4(o[4], o[5], o[6], o[7]);
+  widen4(c.x, lo.x, lo.y);
+  widen4(c.y, lo.z, lo.w);
+  widen4(c.z, hi.x, hi.y);
+  widen4(c.w, hi.z, hi.w);
+}
+
+__device__ __forceinline__ void st_shared(uint32_t at, const uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+__device__ __forceinline__ uint4 ld_shared(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ float4 ld_shared_f4(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at));
+  return v;
 }
 
 __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
@@ -332,99 +391,148 @@ struct Seen {
   }
 };
 
-// The largest of the scores s_j ks_j over the columns a row sees (not yet times the row's factor).
-template <int BN, bool MASK>
-__device__ __forceinline__ float tile_max(uint32_t s_addr, const float* ks, const Seen& seen, const uint32_t* valid) {
-  float m0 = -INFINITY, m1 = -INFINITY;
-#pragma unroll
-  for (int c = 0; c < BN / 32; ++c) {
-    uint32_t s[32];
-    tmem_ld32(s_addr + 32 * c, s);
-    const uint32_t bits = MASK ? seen.bits(c, valid[c]) : 0xFFFFFFFFu;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float4 k = *reinterpret_cast<const float4*>(ks + 32 * c + 4 * i);
-      const float2 y0 = __fmul2_rn(make_float2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), make_float2(k.x, k.y));
-      const float2 y1 = __fmul2_rn(make_float2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), make_float2(k.z, k.w));
-      if (MASK) {
-        if (bits >> (4 * i) & 1) m0 = fmaxf(m0, y0.x);
-        if (bits >> (4 * i + 1) & 1) m1 = fmaxf(m1, y0.y);
-        if (bits >> (4 * i + 2) & 1) m0 = fmaxf(m0, y1.x);
-        if (bits >> (4 * i + 3) & 1) m1 = fmaxf(m1, y1.y);
-      } else {
-        m0 = fmaxf(m0, fmaxf(y0.x, y1.x));
-        m1 = fmaxf(m1, fmaxf(y0.y, y1.y));
-      }
-    }
-  }
-  return fmaxf(m0, m1);
-}
-
-// The largest of x_j + log2 |vs_j| over the columns a row sees.
-template <int BN>
-__device__ __noinline__ float tile_max_weight(uint32_t s_addr, const float* ks, const float* vs, float f, Seen seen,
-                                              const uint32_t* valid) {
-  float m = -INFINITY;
-#pragma unroll 1
-  for (int c = 0; c < BN / 32; ++c) {
-    uint32_t s[32];
-    tmem_ld32(s_addr + 32 * c, s);
-    const uint32_t bits = seen.bits(c, valid[c]);
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const float y = __fmul_rn(__fmul_rn(__uint_as_float(s[i]), ks[32 * c + i]), f) + lg2(fabsf(vs[32 * c + i]));
-      if (bits >> i & 1) m = fmaxf(m, y);
-    }
-  }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float m;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
   return m;
 }
 
-// The weights of a tile, written over its scores as fp16 pairs; returns the sum of exp2(x_j - R).
-// WIDE: scores so large that a product rounded apart from the difference decides (kWide).
-template <int BN, bool MASK, bool WIDE>
-__device__ __forceinline__ float tile_weights(uint32_t s_addr, const float* ks, const float* vs, float f, float R,
-                                              const Seen& seen, const uint32_t* valid) {
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&w)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "r"(w[8]), "r"(w[9]),
+      "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15])
+      : "memory");
+}
+// 32 columns of this thread's TMEM lane, on their way until tmem_wait_ld; `landed` keeps what uses them behind it.
+__device__ __forceinline__ void tmem_ld32_start(uint32_t taddr, float* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]),
+          "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]),
+          "=f"(r[16]), "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]),
+          "=f"(r[24]), "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void landed(float* r) {
+  asm volatile(""
+               : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]),
+          "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15]),
+          "+f"(r[16]), "+f"(r[17]), "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]), "+f"(r[23]),
+          "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]), "+f"(r[30]), "+f"(r[31])::"memory");
+}
+__device__ __forceinline__ void tmem_row64(uint32_t taddr, float (&r)[64]) {
+  tmem_ld32_start(taddr, r);
+  tmem_ld32_start(taddr + 32, r + 32);
+  tmem_wait_ld();
+  landed(r);
+  landed(r + 32);
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+// The weights of 64 tokens from their scores s, as fp16 pairs: w = exp2(s ks f - R) vs.  Returns the largest |w|
+// and adds the exponentials to `sum`.  Of the columns a row does not see (MASK) every weight is 0.  MASK is
+// also the form for scores so large that a product rounded apart from the difference decides (kWide).
+template <bool MASK>
+__device__ __forceinline__ float weights64(const float (&s)[64], uint32_t ks, uint32_t vs, float f, float R,
+                                           uint32_t bits0, uint32_t bits1, float2& sum, uint32_t (&w)[32]) {
   float2 sum0 = make_float2(0.0f, 0.0f), sum1 = sum0;
   const float2 f2 = make_float2(f, f), r2 = make_float2(-R, -R);
+  float m0 = 0.0f, m1 = 0.0f;
 #pragma unroll
-  for (int c = 0; c < BN / 32; ++c) {
-    uint32_t s[32];
-    tmem_ld32(s_addr + 32 * c, s);
-    const uint32_t bits = MASK ? seen.bits(c, valid[c]) : 0xFFFFFFFFu;
-    uint32_t w[16];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float4 k = *reinterpret_cast<const float4*>(ks + 32 * c + 4 * i);
-      const float4 v = *reinterpret_cast<const float4*>(vs + 32 * c + 4 * i);
-      const float2 y0 = __fmul2_rn(make_float2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), make_float2(k.x, k.y));
-      const float2 y1 = __fmul2_rn(make_float2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), make_float2(k.z, k.w));
-      const float2 z0 = WIDE ? __fadd2_rn(__fmul2_rn(y0, f2), r2) : __ffma2_rn(y0, f2, r2);
-      const float2 z1 = WIDE ? __fadd2_rn(__fmul2_rn(y1, f2), r2) : __ffma2_rn(y1, f2, r2);
-      float2 p0 = make_float2(ex2(z0.x), ex2(z0.y)), p1 = make_float2(ex2(z1.x), ex2(z1.y));
-      float2 w0, w1;
-      if (MASK) {
-        const bool b0 = bits >> (4 * i) & 1, b1 = bits >> (4 * i + 1) & 1, b2 = bits >> (4 * i + 2) & 1, b3 = bits >> (4 * i + 3) & 1;
-        p0 = make_float2(b0 ? p0.x : 0.0f, b1 ? p0.y : 0.0f);
-        p1 = make_float2(b2 ? p1.x : 0.0f, b3 ? p1.y : 0.0f);
-        w0 = make_float2(b0 ? p0.x * v.x : 0.0f, b1 ? p0.y * v.y : 0.0f);
-        w1 = make_float2(b2 ? p1.x * v.z : 0.0f, b3 ? p1.y * v.w : 0.0f);
-      } else {
-        w0 = __fmul2_rn(p0, make_float2(v.x, v.y));
-        w1 = __fmul2_rn(p1, make_float2(v.z, v.w));
-      }
-      sum0 = __fadd2_rn(sum0, p0);
-      sum1 = __fadd2_rn(sum1, p1);
-      w[2 * i] = half2_bits(w0.x, w0.y);
-      w[2 * i + 1] = half2_bits(w1.x, w1.y);
+  for (int i = 0; i < 16; ++i) {
+    const float4 k = ld_shared_f4(ks + 16 * i), v = ld_shared_f4(vs + 16 * i);
+    const float2 y0 = __fmul2_rn(make_float2(s[4 * i], s[4 * i + 1]), make_float2(k.x, k.y));
+    const float2 y1 = __fmul2_rn(make_float2(s[4 * i + 2], s[4 * i + 3]), make_float2(k.z, k.w));
+    const float2 z0 = MASK ? __fadd2_rn(__fmul2_rn(y0, f2), r2) : __ffma2_rn(y0, f2, r2);
+    const float2 z1 = MASK ? __fadd2_rn(__fmul2_rn(y1, f2), r2) : __ffma2_rn(y1, f2, r2);
+    float2 p0 = make_float2(ex2(z0.x), ex2(z0.y)), p1 = make_float2(ex2(z1.x), ex2(z1.y));
+    float2 w0, w1;
+    if (MASK) {
+      const uint32_t b = (i < 8 ? bits0 : bits1) >> (4 * (i & 7));
+      p0 = make_float2(b & 1 ? p0.x : 0.0f, b & 2 ? p0.y : 0.0f);
+      p1 = make_float2(b & 4 ? p1.x : 0.0f, b & 8 ? p1.y : 0.0f);
+      w0 = make_float2(b & 1 ? p0.x * v.x : 0.0f, b & 2 ? p0.y * v.y : 0.0f);
+      w1 = make_float2(b & 4 ? p1.x * v.z : 0.0f, b & 8 ? p1.y * v.w : 0.0f);
+    } else {
+      w0 = __fmul2_rn(p0, make_float2(v.x, v.y));
+      w1 = __fmul2_rn(p1, make_float2(v.z, v.w));
     }
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(s_addr + 16 * c),
-        "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "r"(w[8]), "r"(w[9]),
-        "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15])
-        : "memory");
+    sum0 = __fadd2_rn(sum0, p0);
+    sum1 = __fadd2_rn(sum1, p1);
+    m0 = max3(m0, fabsf(w0.x), fabsf(w0.y));
+    m1 = max3(m1, fabsf(w1.x), fabsf(w1.y));
+    w[2 * i] = half2_bits(w0.x, w0.y);
+    w[2 * i + 1] = half2_bits(w1.x, w1.y);
   }
-  return (sum0.x + sum0.y) + (sum1.x + sum1.y);
+  sum = __fadd2_rn(sum, __fadd2_rn(sum0, sum1));
+  return fmaxf(m0, m1);
+}
+
+// The reference that puts the largest weight of these 64 tokens at 2^3 (see kWide and kFar for its limits), from
+// their scores; -infinity if none counts.
+__device__ __forceinline__ float reference64(const float (&s)[64], uint32_t ks, uint32_t vs, float f, uint32_t bits0,
+                                             uint32_t bits1) {
+  float most = -INFINITY, heavy = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float4 k = ld_shared_f4(ks + 16 * i), v = ld_shared_f4(vs + 16 * i);
+    const float kk[4] = {k.x, k.y, k.z, k.w}, vv[4] = {v.x, v.y, v.z, v.w};
+    const uint32_t b = (i < 8 ? bits0 : bits1) >> (4 * (i & 7));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float x = __fmul_rn(__fmul_rn(s[4 * i + e], kk[e]), f);
+      if (b >> e & 1) {
+        most = fmaxf(most, x);
+        heavy = fmaxf(heavy, x + lg2(fabsf(vv[e])));
+      }
+    }
+  }
+  return fabsf(most) < kWide ? fmaxf(heavy - 3.0f, most - kFar) : most;
+}
+
+// The natural logarithm of a row's sum of exponentials, from its reference and its sum by it (the reference may
+// lie far from the largest score).
+__device__ __forceinline__ float log_sum(float R, float l) {
+  if (!(l > 0.0f)) return -INFINITY;
+  const int e = exponent(l);
+  return ((R + static_cast<float>(e)) + log2f(l * pow2(-e))) * 0.693147180559945309f;
+}
+
+template <int REGS>
+__device__ __forceinline__ void more_regs() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+template <int REGS>
+__device__ __forceinline__ void fewer_regs() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+
+// Segment `seg`, by a warp whose lanes all call this; false behind the last one, or if a wait has run out (then
+// `ok` is false too).
+__device__ __forceinline__ bool next_segment(Shared& sh, int seg, Segment& g, bool& ok, int* status) {
+  ok = wait_phase(&sh.sgfull[seg % kSegments], (seg / kSegments) & 1, status);
+  ok = __all_sync(0xFFFFFFFFu, ok);
+  if (!ok) return false;
+  g = sh.segment[seg % kSegments];
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&sh.sgempty[seg % kSegments]);
+  return g.n > 0;
 }
 
 template <int PANELS>
@@ -438,22 +546,40 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.kfull[i], kConverters);
-      mbar_init(&sh.kempty[i], 1);
       mbar_init(&sh.vfull[i], kConverters);
-      mbar_init(&sh.vempty[i], 1);
+      mbar_init(&sh.vempty[i], 2);
+      mbar_init(&sh.drain[i], 1);
       mbar_init(&sh.sfull[i], 1);
       mbar_init(&sh.pfull[i], 128);
       mbar_init(&sh.ofull[i], 1);
     }
-    for (int i = 0; i < kRing; ++i) mbar_init(&sh.scfull[i], kConverters);
+    for (int i = 0; i < C::K_STAGES; ++i) {
+      mbar_init(&sh.kfull[i], kConverters);
+      mbar_init(&sh.kempty[i], 2);
+    }
+    for (int i = 0; i < kRing; ++i) mbar_init(&sh.scfull[i], 2 * kConverters);
+    for (int i = 0; i < kSegments; ++i) {
+      mbar_init(&sh.sgfull[i], 1);
+      mbar_init(&sh.sgempty[i], 14);  // the warps of the softmax, the converters and the MMAs
+    }
     mbar_init(&sh.qfull, kSoftmax);
-    mbar_init(&sh.drain, 1);
+    mbar_init(&sh.meet, kSoftmax);
     fence_barrier_init();
   }
   if (warp == 12) {
     tmem_alloc(&sh.tmem, 512);
     tmem_relinquish();
+  }
+  // head_dim an odd multiple of 16: the MMA's last 32 columns of a score reach past the head, into bytes that no
+  // copy writes; they are zero in keys (never NaN; the queries' are written as zeros)
+  if (hd & 16) {
+    const int col = hd & 127, panel = hd >> 7;
+    for (int i = tid; i < C::K_STAGES * C::BN; i += kThreads) {
+      const int st = i / C::BN, row = i % C::BN;
+      *reinterpret_cast<uint4*>(smem + C::OFF_K + st * C::K_BYTES + panel * C::BN * 128 + row * 128 + (col ^ ((row & 7) << 4))) =
+          make_uint4(0, 0, 0, 0);
+    }
+    fence_proxy_async_smem();
   }
   tc_fence_before();
   __syncthreads();
@@ -543,148 +669,230 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
   bool ok = true;
   if (warp >= 8 && warp < 12) {
     // ------------------------------------------------------------ converters: lane = token row for the lookups
+    // Short loops over shared memory rather than unrolled ones over registers: straight-line code of several KB runs
+    // at the rate at which instructions are fetched.
+    fewer_regs<kRegsConvert>();
     const int w = warp - 8, chunks = hd >> 4;  // 16-byte pieces of a head
     const int sub = lane / C::LANES, piece = lane % C::LANES;
-    const bool swap = (piece & 4) != 0;        // (lanes of a row write both halves of their pieces in turn: no bank twice)
     const bool loads = piece < chunks;
-    auto put = [&](uint8_t* base, const uint4 (&raw)[C::LOADS]) {
-#pragma unroll
-      for (int i = 0; i < C::LOADS; ++i) {
-        const int row = w * C::WARP_ROWS + i * (32 / C::LANES) + sub;
-        uint4 lo, hi;
-        widen16(raw[i], lo, hi);
-        uint8_t* at = base + (piece >> 2) * (C::BN * 128) + row * 128;
-        const int c0 = ((2 * piece) & 7) ^ (row & 7), c1 = ((2 * piece + 1) & 7) ^ (row & 7);
-        if (loads) {
-          *reinterpret_cast<uint4*>(at + (swap ? c1 : c0) * 16) = swap ? hi : lo;
-          *reinterpret_cast<uint4*>(at + (swap ? c0 : c1) * 16) = swap ? lo : hi;
-        }
-      }
+    const uint32_t s_k = smem_addr(smem + C::OFF_K), s_v = smem_addr(smem + C::OFF_V);
+    const uint32_t raw = smem_addr(smem + C::OFF_RAW) + (tid - kSoftmax) * 16;  // this thread's pieces
+    Segment k;
+    int seg = 0, t = 0, page = -1, in_page = 0, head = 0;
+    bool more = next_segment(sh, 0, k, ok, a.status);
+    auto look_up = [&]() {  // the page of this lane's token in tile t of the segment
+      const int j = k.first + t * C::BN + w * C::WARP_ROWS + lane, blk = j / a.block_size;
+      in_page = lane < C::WARP_ROWS && j < k.stop ? j - blk * a.block_size : -1;
+      if (in_page >= 0) page = __ldg(a.block_table + static_cast<long long>(k.b) * a.ld_table + blk);
+      head = k.head;
     };
-    int g = 0;
-    for (Walk<C> k(a, sh); ok && k.next();) {
-      const int* table = a.block_table + static_cast<long long>(k.b) * a.ld_table;
-      const int stop = k.s.len - k.s.fresh + (k.w.row + k.w.rows - 1) / group + 1;  // tokens the unit's last row sees
-      for (int t = k.t0; t < k.t1; ++t, ++g) {
-        const int st = g & 1, ring = g % kRing;
-        const int row = w * C::WARP_ROWS + lane;
-        const int j = (k.w.tile0 + t) * C::BN + row;
+    if (more) look_up();
+    bool have = false;
+    for (int g = 0; ok && (have || more); ++g) {
+      // gathers tile g (its page has been looked up) and looks up the next one's
+      const bool gathers = more;
+      if (gathers) {
+        const int st = g % C::K_STAGES, ring = g % kRing;
         long long at = -1;
-        if (lane < C::WARP_ROWS && j < stop) {
-          const int blk = j / a.block_size;
-          const int page = __ldg(table + blk);
-          const long long slot = static_cast<long long>(page) * a.block_size + (j - blk * a.block_size);
+        if (in_page >= 0) {
+          const long long slot = static_cast<long long>(page) * a.block_size + in_page;
           if (page < 0 || slot >= a.num_slots) latch_bad_index(a.status);
-          else at = slot * a.kv_heads + k.head;
+          else at = slot * a.kv_heads + head;
         }
-        uint4 kr[C::LOADS], vr[C::LOADS];
-#pragma unroll
+        if (g >= C::K_STAGES) ok = wait_phase(&sh.kempty[st], (g / C::K_STAGES + 1) & 1, a.status);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        const uint32_t valid = __ballot_sync(0xFFFFFFFFu, at >= 0);
+        if (lane < C::WARP_ROWS) {
+          const uint32_t n = at >= 0 ? 4 : 0;
+          const long long i = at >= 0 ? at : 0;
+          cp_async4(smem_addr(&sh.ks[ring][w * C::WARP_ROWS + lane]), a.k_scale + i, n);
+          cp_async4(smem_addr(&sh.vs[ring][w * C::WARP_ROWS + lane]), a.v_scale + i, n);
+        }
+        const long long byte = at >= 0 ? at * hd : -1;
+        const uint32_t k_st = s_k + st * C::K_BYTES + (piece >> 3) * (C::BN * 128), raw_st = raw + (g & 1) * C::RAW_BYTES;
+#pragma unroll 2
         for (int i = 0; i < C::LOADS; ++i) {
-          const long long r = __shfl_sync(0xFFFFFFFFu, at, i * (32 / C::LANES) + sub);
-          kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
-          if (r >= 0 && loads) {
-            kr[i] = __ldg(reinterpret_cast<const uint4*>(a.k_cache + r * hd) + piece);
-            vr[i] = __ldg(reinterpret_cast<const uint4*>(a.v_cache + r * hd) + piece);
+          const int r = i * (32 / C::LANES) + sub, row = w * C::WARP_ROWS + r;
+          const long long off = __shfl_sync(0xFFFFFFFFu, byte, r);
+          if (loads) {
+            const uint32_t n = off >= 0 ? 16 : 0;
+            const long long from = off >= 0 ? off + piece * 16 : 0;
+            cp_async16(k_st + row * 128 + (((piece & 7) ^ (row & 7)) << 4), a.k_cache + from, n);
+            cp_async16(raw_st + i * (kConverters * 16), a.v_cache + from, n);
           }
         }
-        const float ks = at >= 0 ? __ldg(a.k_scale + at) : 0.0f, vs = at >= 0 ? __ldg(a.v_scale + at) : 0.0f;
-        // (a scale that is no number: a range that no tile's scales keep to)
-        const float va = fabsf(vs), vfin = va < INFINITY ? va : 0.0f;
-        const float top = warp_fmax(at >= 0 ? va < INFINITY ? va : FLT_MAX : 0.0f);
-        const float low = -warp_fmax(at >= 0 ? -vfin : -INFINITY);
-        const uint32_t there = __ballot_sync(0xFFFFFFFFu, at >= 0);
-        if (g >= 2) ok = wait_phase(&sh.kempty[st], ((g >> 1) & 1) ^ 1, a.status);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
-        if (lane < C::WARP_ROWS) {
-          sh.ks[ring][row] = ks;
-          sh.vs[ring][row] = vs;
-        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        cp_async_arrive(&sh.kfull[st]);
+        cp_async_arrive(&sh.scfull[ring]);
         if (lane == 0) {
-          sh.vmax[ring][w] = top;
-          sh.vmin[ring][w] = low;
-          if (C::WARP_ROWS == 32) sh.valid[ring][w] = there;
-          else reinterpret_cast<uint16_t*>(&sh.valid[ring][0])[w] = static_cast<uint16_t>(there);
+          if (C::WARP_ROWS == 32) sh.valid[ring][w] = valid;
+          else reinterpret_cast<uint16_t*>(&sh.valid[ring][0])[w] = static_cast<uint16_t>(valid);
         }
-        put(smem + C::OFF_K + st * C::KV_BYTES, kr);
-        fence_proxy_async_smem();
         mbar_arrive(&sh.scfull[ring]);
-        mbar_arrive(&sh.kfull[st]);
-        if (g >= 2) ok = wait_phase(&sh.vempty[st], ((g >> 1) & 1) ^ 1, a.status);
+        if (++t == k.n) {
+          more = next_segment(sh, ++seg, k, ok, a.status);
+          if (!ok) break;
+          t = 0;
+        }
+        if (more) look_up();
+      }
+      if (have) {  // tile g - 1: the thread's own pieces as fp16 (lanes of a row write the halves of theirs in turn: no bank twice)
+        if (gathers) asm volatile("cp.async.wait_group 1;" ::: "memory");
+        else asm volatile("cp.async.wait_group 0;" ::: "memory");
+        const int h = g - 1;
+        if (h >= 2) ok = wait_phase(&sh.vempty[h & 1], ((h >> 1) & 1) ^ 1, a.status);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
-        put(smem + C::OFF_V + st * C::KV_BYTES, vr);
-        fence_proxy_async_smem();
-        mbar_arrive(&sh.vfull[st]);
+        const uint32_t base = s_v + (h & 1) * C::V_BYTES + (piece >> 2) * (C::BN * 128);
+        const bool swap = (piece & 4) != 0;
+#pragma unroll 2
+        for (int i = 0; i < C::LOADS; ++i) {
+          const int row = w * C::WARP_ROWS + i * (32 / C::LANES) + sub;
+          if (loads) {
+            uint4 lo, hi;
+            widen16(ld_shared(raw + (h & 1) * C::RAW_BYTES + i * (kConverters * 16)), lo, hi);
+            const uint32_t c0 = ((2 * piece) & 7) ^ (row & 7);
+            st_shared(base + row * 128 + ((swap ? c0 ^ 1 : c0) << 4), swap ? hi : lo);
+            st_shared(base + row * 128 + ((swap ? c0 : c0 ^ 1) << 4), swap ? lo : hi);
+          }
+        }
+        mbar_arrive(&sh.vfull[h & 1]);
       }
+      have = gathers;
     }
-  } else if (warp == 12) {
-    // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t id_s = umma_idesc_f32acc(0, 0, 128, C::BN);
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp >= 12) {
+    // ------------------------------------------------------------ MMA issuers, one for each row tile
+    fewer_regs<kRegsMma>();
+    if (warp < 14 && lane == 0) {
+      const int mma = warp - 12;  // the row tile whose MMAs this thread issues
+      constexpr uint32_t id_hi = umma_idesc_f32acc(0, 0, 128, C::BN), id_lo = umma_idesc_f32acc(1, 0, 128, C::BN);  // e4m3, e5m2
       const uint32_t id_o = umma_idesc_f32acc(0, 0, 128, hd) | (1u << 16);  // B (values) transposed
-      const uint32_t s_q = smem_addr(smem), s_k = s_q + C::OFF_K, s_v = s_q + C::OFF_V;
-      const int ksteps = hd >> 4;
+      const uint64_t q0 = umma_desc_sw128(smem_addr(smem)), k0 = umma_desc_sw128(smem_addr(smem) + C::OFF_K),
+                     v0 = desc_transposed(smem_addr(smem) + C::OFF_V, C::BN * 128);
+      const int ksteps = (hd + 31) >> 5;
       int g = 0, seg = 0;
-      uint32_t weights[2] = {0, 0};  // tiles of weights taken from each score buffer
+      uint32_t before = 0;  // bit b: parity of the tiles that went through score buffer b before this segment
+      // Unrolled, each MMA a few instructions from constants: a loop that forms its descriptors takes 175 cycles an
+      // MMA, which itself takes 64.
       auto scores = [&](int tile, int buf, int st) {
-        for (int kk = 0; kk < ksteps; ++kk)
-          umma_f16(tmem + buf * C::TM_S, umma_desc_sw128(s_q + tile * C::Q_BYTES + (kk >> 2) * (128 * 128) + (kk & 3) * 32),
-                   umma_desc_sw128(s_k + st * C::KV_BYTES + (kk >> 2) * (C::BN * 128) + (kk & 3) * 32), id_s, kk != 0);
+        const uint64_t qd = q0 + tile * (2 * C::Q_PIECE / 16), kd = k0 + st * (C::K_BYTES / 16);
+        const uint32_t at = tmem + buf * C::TM_S;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          const uint64_t hd_q = qd + half * (C::Q_PIECE / 16);
+          const uint32_t id = half != 0 ? id_lo : id_hi;
+#pragma unroll
+          for (int kk = 0; kk < 2 * PANELS; ++kk)
+            if (kk < ksteps)
+              umma_f8f6f4(at, hd_q + ((kk >> 2) * (128 * 128) + (kk & 3) * 32) / 16,
+                          kd + ((kk >> 2) * (C::BN * 128) + (kk & 3) * 32) / 16, id, half | kk);
+        }
         umma_commit(&sh.sfull[buf]);
       };
-      auto outputs = [&](int tile, int buf, int st, bool first) {
-        if (!wait_phase(&sh.pfull[buf], weights[buf] & 1, a.status)) return false;
-        ++weights[buf];
+      auto outputs = [&](int tile, int buf, int st, int use, bool first) {
+        if (!wait_phase(&sh.pfull[buf], ((before >> buf) + use) & 1, a.status)) return false;
         tc_fence_after();
+        uint64_t vd = v0 + st * (C::V_BYTES / 16);
+        uint32_t p_at = tmem + buf * C::TM_S;
+        const uint32_t o_at = tmem + C::TM_O + tile * 64 * PANELS;
+#pragma unroll 1
+        for (int x = first ? 0 : 1; p_at < tmem + buf * C::TM_S + C::BN / 2; x = 1) {
 #pragma unroll
-        for (int kk = 0; kk < C::BN / 16; ++kk)
-          umma_f16_tmem_a(tmem + C::TM_O + tile * 64 * PANELS, tmem + buf * C::TM_S + kk * 8,
-                          desc_transposed(s_v + st * C::KV_BYTES + kk * 16 * 128, C::BN * 128), id_o, !first || kk != 0);
+          for (int kk = 0; kk < 4; ++kk) umma_f16_tmem_a(o_at, p_at + kk * 8, vd + kk * (16 * 128 / 16), id_o, x | kk);
+          p_at += 32;
+          vd += 4 * (16 * 128 / 16);
+        }
         umma_commit(&sh.ofull[tile]);
         return true;
       };
       auto keys = [&](int i) {
-        if (!wait_phase(&sh.kfull[i & 1], (i >> 1) & 1, a.status)) return false;
+        // (the converters' copies and stores are fenced here, where nothing is on its way: a fence waits for loads)
+        if (!wait_phase(&sh.kfull[i % C::K_STAGES], (i / C::K_STAGES) & 1, a.status)) return false;
+        fence_proxy_async_smem();
         tc_fence_after();
         return true;
       };
-      auto values = [&](int i) { return wait_phase(&sh.vfull[i & 1], (i >> 1) & 1, a.status); };
-      for (Walk<C> k(a, sh); ok && k.next(); ++seg) {
+      auto values = [&](int i) {
+        if (!wait_phase(&sh.vfull[i & 1], (i >> 1) & 1, a.status)) return false;
+        fence_proxy_async_smem();
+        return true;
+      };
+      for (; ok; ++seg) {
+        ok = wait_phase(&sh.sgfull[seg % kSegments], (seg / kSegments) & 1, a.status);
+        if (!ok) break;
+        const int n = sh.segment[seg % kSegments].n;
+        const bool two = sh.segment[seg % kSegments].rows > 128;
+        mbar_arrive(&sh.sgempty[seg % kSegments]);
+        if (n == 0) break;
         ok = wait_phase(&sh.qfull, seg & 1, a.status);
         if (!ok) break;
         tc_fence_after();
-        const int n = k.t1 - k.t0;
-        const bool two = k.w.rows > 128;
-        for (int i = 0; i <= n && ok; ++i) {
-          if (i < n && !keys(g + i)) ok = false;
-          if (ok && i > 0 && !values(g + i - 1)) ok = false;
-          if (!ok) break;
-          if (two) {  // scores of tile i take the place of the weights of tile i - 1
-#pragma unroll
-            for (int q = 0; q < C::TILES; ++q) {
-              if (ok && i > 0) ok = outputs(q, q, (g + i - 1) & 1, i == 1);
-              if (ok && i < n) scores(q, q, (g + i) & 1);
+        if (two) {  // the outputs of tile i - 1, then the scores of tile i, which take the weights' place
+          for (int i = 0; i <= n && ok; ++i) {
+            if (i < n) ok = keys(g + i);
+            if (ok && i > 0) {
+              ok = values(g + i - 1) && outputs(mma, mma, (g + i - 1) & 1, i - 1, i == 1);
+              if (ok) umma_commit(&sh.vempty[(g + i - 1) & 1]);
             }
-            if (ok && i < n) umma_commit(&sh.kempty[(g + i) & 1]);
-          } else {
-            if (i < n) {
-              scores(0, i & 1, (g + i) & 1);
-              umma_commit(&sh.kempty[(g + i) & 1]);
+            if (ok && i < n) {
+              scores(mma, mma, (g + i) % C::K_STAGES);
+              umma_commit(&sh.kempty[(g + i) % C::K_STAGES]);
             }
-            if (i > 0) ok = outputs(0, (i - 1) & 1, (g + i - 1) & 1, i == 1);
           }
-          if (!ok) break;
-          if (i > 0) umma_commit(&sh.vempty[(g + i - 1) & 1]);
+        } else if (mma == 0) {  // one row tile: the scores of tile i, in the other buffer, then the outputs of tile i - 1
+          for (int i = 0; i <= n && ok; ++i) {
+            if (i < n) {
+              ok = keys(g + i);
+              if (!ok) break;
+              scores(0, i & 1, (g + i) % C::K_STAGES);
+              umma_commit(&sh.kempty[(g + i) % C::K_STAGES]);
+              umma_commit(&sh.kempty[(g + i) % C::K_STAGES]);  // (for the other thread)
+            }
+            if (i > 0) {
+              ok = values(g + i - 1) && outputs(0, (i - 1) & 1, (g + i - 1) & 1, (i - 1) >> 1, i == 1);
+              if (!ok) break;
+              umma_commit(&sh.vempty[(g + i - 1) & 1]);
+              umma_commit(&sh.vempty[(g + i - 1) & 1]);
+            }
+          }
         }
         g += n;
+        before ^= two ? 3u * (n & 1) : ((n + 1) >> 1 & 1) | (n >> 1 & 1) << 1;
       }
-      umma_commit(&sh.drain);
-      wait_drain(&sh.drain, 0, a.status);
+      umma_commit(&sh.drain[mma]);
+      wait_drain(&sh.drain[mma], 0, a.status);
+    } else if (warp == 14) {
+      // ---------------------------------------------------------- the segments, for all the others
+      Walk<C> k(a, sh);
+      bool more = true;
+      for (int seg = 0; ok && more; ++seg) {
+        more = k.next();
+        const int slot = seg % kSegments;
+        if (seg >= kSegments) ok = wait_phase(&sh.sgempty[slot], (seg / kSegments + 1) & 1, a.status);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (ok && lane == 0) {
+          Segment g = {};
+          if (more) {
+            const bool whole = k.t0 == 0 && k.t1 == k.w.tiles;
+            g = {k.t1 - k.t0, k.b, k.head, k.s.row0, k.s.len - k.s.fresh, k.w.row, k.w.rows, (k.w.tile0 + k.t0) * C::BN,
+                 k.s.len - k.s.fresh + (k.w.row + k.w.rows - 1) / group + 1,
+                 whole ? -1 : 2 * static_cast<int>(blockIdx.x) + (k.t0 == 0 ? 1 : 0), 0, 0};
+            if (!whole) {
+              g.r0 = k.range_of(0);
+              g.r1 = k.range_of(k.w.tiles - 1);
+            }
+          }
+          sh.segment[slot] = g;
+          mbar_arrive(&sh.sgfull[slot]);
+        }
+      }
     }
     __syncwarp();
-  } else if (warp < 8) {
+  } else {
     // ------------------------------------------------------------ softmax: a row a thread
+    more_regs<kRegsSoftmax>();
     const int tile = warp >> 2, r = tid & 127;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     // tokens before the first position see nothing
@@ -698,121 +906,167 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
           for (int c = tid; c < a.q_heads; c += kSoftmax) a.lse[row * a.q_heads + c] = -INFINITY;
       }
     }
-    int g = 0, seg = 0;
-    uint32_t before[2] = {0, 0}, done = 0;  // tiles that went through each score buffer before this segment, outputs of this row tile
-    for (Walk<C> k(a, sh); k.next(); ++seg) {
-      const int n = k.t1 - k.t0;
-      const bool two = k.w.rows > 128, active = tile == 0 || two;
-      const int pair = k.w.row + tile * 128 + r;  // this thread's (token, head)
-      const bool mine = tile * 128 + r < k.w.rows;
+    int g = 0, meets = 0;
+    uint32_t before = 0, done = 0;  // bit b: parity of the tiles that went through score buffer b before this segment; outputs of this row tile
+    // the softmax threads wait for one another
+    auto meet = [&]() {
+      mbar_arrive(&sh.meet);
+      ok = wait_phase(&sh.meet, meets++ & 1, a.status);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      return ok;
+    };
+    Segment k;
+    for (int seg = 0; ok && next_segment(sh, seg, k, ok, a.status); ++seg) {
+      const int n = k.n;
+      const bool two = k.rows > 128, active = tile == 0 || two;
+      const bool mine = tile * 128 + r < k.rows;
+      const int pair = k.row + tile * 128 + r;  // this thread's (token, head)
       const int token = pair / group, qh = k.head * group + (pair - token * group);
-      const int pos = k.s.len - k.s.fresh + token;
+      const int pos = k.pos + token;
+      const uint32_t o_addr = lane_base + C::TM_O + tile * 64 * PANELS;
       float f = 0.0f;
-      if (ok && active) {
-        // this row's queries as fp16
-        const uint4* src = reinterpret_cast<const uint4*>(a.q + static_cast<long long>(k.s.row0 + token) * a.ldq +
+      if (active) {
+        // this row's queries in two pieces: e4m3, and the rest as e5m2
+        const uint4* src = reinterpret_cast<const uint4*>(a.q + static_cast<long long>(k.qrow + token) * a.ldq +
                                                           static_cast<long long>(qh) * hd);
-        float top = 0.0f;
-        const int vecs = hd >> 3;
-        if (mine)
-          for (int i = 0; i < vecs; ++i) {
-            const uint4 u = __ldg(src + i);
-            const uint32_t uw[4] = {u.x, u.y, u.z, u.w};
+        const int vecs = mine ? hd >> 3 : 0;
+        auto vec = [&](int i) { return i < vecs ? __ldg(src + i) : make_uint4(0, 0, 0, 0); };
+        __nv_bfloat162 m = __floats2bfloat162_rn(0.0f, 0.0f);
+        {
+          uint4 u[8 * PANELS];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              top = fmaxf(top, fmaxf(fabsf(__uint_as_float(uw[e] << 16)), fabsf(__uint_as_float(uw[e] & 0xFFFF0000u))));
+          for (int i = 0; i < 8 * PANELS; ++i) u[i] = vec(i);
+#pragma unroll
+          for (int i = 0; i < 8 * PANELS; ++i) {
+            const uint32_t uw[4] = {u[i].x & 0x7FFF7FFFu, u[i].y & 0x7FFF7FFFu, u[i].z & 0x7FFF7FFFu, u[i].w & 0x7FFF7FFFu};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162*>(&uw[e]));
           }
-        // (a row below 2^-106: fewer bits, nothing to score)
-        const int up = min(14 - exponent(top), 120);
+        }
+        const float top = fmaxf(__low2float(m), __high2float(m));
+        // (a row below 2^-113: fewer bits, nothing to score)
+        const int up = min(7 - exponent(top), 120);
         const float f1 = a.scale < 0.0f ? -pow2(up / 2) : pow2(up / 2), f2 = pow2(up - up / 2);
-        uint8_t* dst = smem + tile * C::Q_BYTES + r * 128;
-        for (int i = 0; i < vecs; ++i) {
-          const uint4 u = mine ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-          const uint32_t uw[4] = {u.x, u.y, u.z, u.w};
-          uint32_t o[4];
+        const uint32_t dst = smem_addr(smem) + 2 * tile * C::Q_PIECE + r * 128;
+        uint4 u0 = vec(0), u1 = vec(1);
+#pragma unroll 1
+        for (int i = 0; i < (hd + 31) >> 5 << 1; ++i) {  // 16 values; zeros past the head
+          const uint32_t uw[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+          u0 = vec(2 * i + 2);
+          u1 = vec(2 * i + 3);
+          uint32_t hi[4], lo[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            o[e] = half2_bits(__uint_as_float(uw[e] << 16) * f1 * f2, __uint_as_float(uw[e] & 0xFFFF0000u) * f1 * f2);
-          *reinterpret_cast<uint4*>(dst + (i >> 3) * (128 * 128) + (((i & 7) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+          for (int e = 0; e < 8; ++e) {
+            const float x0 = __uint_as_float(uw[e] << 16) * f1 * f2, x1 = __uint_as_float(uw[e] & 0xFFFF0000u) * f1 * f2;
+            const uint32_t c = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
+            const float2 v = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c), __NV_E4M3)));
+            const uint32_t d = __nv_cvt_float2_to_fp8x2(make_float2(x0 - v.x, x1 - v.y), __NV_SATFINITE, __NV_E5M2);
+            hi[e >> 1] = (e & 1) != 0 ? hi[e >> 1] | c << 16 : c;
+            lo[e >> 1] = (e & 1) != 0 ? lo[e >> 1] | d << 16 : d;
+          }
+          const uint32_t o = dst + (i >> 3) * (128 * 128) + (((i & 7) ^ (r & 7)) << 4);
+          st_shared(o, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+          st_shared(o + C::Q_PIECE, make_uint4(lo[0], lo[1], lo[2], lo[3]));
         }
         // raw score x the key's scale x this = score in log2 units
         f = fabsf(a.scale) * 1.44269504088896340736f / fabsf(f1) / f2;
         fence_proxy_async_smem();
       }
-      if (ok) {
-        tc_fence_before();
-        mbar_arrive(&sh.qfull);
-      }
-      float R = -INFINITY, l = 0.0f, most = -INFINITY, heavy = -INFINITY;  // largest x, bound on log2 of the largest p vs
+      tc_fence_before();
+      mbar_arrive(&sh.qfull);
+      float R = -INFINITY, l = 0.0f;
+      bool wide = false;
       if (active) {
-        for (int i = 0; i < n && ok; ++i) {
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
           const int buf = two ? tile : i & 1, ring = (g + i) % kRing;
           ok = wait_phase(&sh.scfull[ring], ((g + i) / kRing) & 1, a.status) &&
-               wait_phase(&sh.sfull[buf], (before[buf] + (two ? i : i >> 1)) & 1, a.status);
+               wait_phase(&sh.sfull[buf], ((before >> buf) + (two ? i : i >> 1)) & 1, a.status);
           ok = __all_sync(0xFFFFFFFFu, ok);
           if (!ok) break;
           tc_fence_after();
           const uint32_t s_addr = lane_base + buf * C::TM_S;
-          const float *ks = sh.ks[ring], *vs = sh.vs[ring];
-          const uint32_t* valid = sh.valid[ring];
           // columns of this tile that the row sees (a row past the unit's: all, of a query of zeros)
-          const int j0 = (k.w.tile0 + k.t0 + i) * C::BN;
+          const int j0 = k.first + i * C::BN;
           Seen seen = {0, C::BN};
           if (mine) seen = {a.window > 0 ? pos - a.window + 1 - j0 : 0, pos + 1 - j0};
-          uint32_t all = valid[0] & (C::BN > 32 ? valid[1] : ~0u);
-          if (C::BN == 128) all &= valid[2] & valid[3];
-          const bool mask = __any_sync(0xFFFFFFFFu, (mine && (seen.lo > 0 || seen.hi < C::BN)) || all != 0xFFFFFFFFu);
-          const float vtop = fmaxf(fmaxf(sh.vmax[ring][0], sh.vmax[ring][1]), fmaxf(sh.vmax[ring][2], sh.vmax[ring][3]));
-          const float vlow = fminf(fminf(sh.vmin[ring][0], sh.vmin[ring][1]), fminf(sh.vmin[ring][2], sh.vmin[ring][3]));
-          float tm = mask ? tile_max<C::BN, true>(s_addr, ks, seen, valid) : tile_max<C::BN, false>(s_addr, ks, seen, valid);
-          if (tm > -INFINITY) tm = __fmul_rn(tm, f);
-          most = fmaxf(most, tm);
-          const bool apart = !(vtop <= vlow * 64.0f);
-          if (apart) heavy = fmaxf(heavy, tile_max_weight<C::BN>(s_addr, ks, vs, f, seen, valid));
-          else heavy = fmaxf(heavy, tm + lg2(vtop));
-          const bool wide = __any_sync(0xFFFFFFFFu, fabsf(most) >= kWide && most > -INFINITY);
-          // the reference, where it has to move
-          const bool move = most > -INFINITY && (!(R > -INFINITY) || !(heavy - R < 15.0f) || !(most - R < 112.0f));
-          float back = 1.0f;
-          if (move) {
-            const float to = fabsf(most) < kWide ? fmaxf(heavy - 11.5f, most - 100.0f) : most;
-            back = to > R ? ex2(R - to) : 1.0f;
-            R = fmaxf(R, to);
-            l *= back;
+          bool waited = i == 0;  // for the outputs of the tile before
+          bool mask = seen.lo > 0 || seen.hi < C::BN;
+          uint32_t every = 0xFFFFFFFFu;
+#pragma unroll
+          for (int c = 0; c < C::BN / 32; ++c) every &= sh.valid[ring][c];
+          mask = __any_sync(0xFFFFFFFFu, mask || every != 0xFFFFFFFFu);
+#pragma unroll 1
+          for (int c = 0; c < C::BN / 64; ++c) {
+            const uint32_t ks = smem_addr(sh.ks[ring]) + 256 * c, vs = smem_addr(sh.vs[ring]) + 256 * c;
+            uint32_t bits0 = 0xFFFFFFFFu, bits1 = 0xFFFFFFFFu;
+            if (mask) {
+              bits0 = seen.bits(2 * c, sh.valid[ring][2 * c]);
+              bits1 = seen.bits(2 * c + 1, sh.valid[ring][2 * c + 1]);
+            }
+            uint32_t w[32];
+            float2 sum;
+#pragma unroll 1
+            for (int tries = 0;; ++tries) {
+              float s[64];
+              tmem_row64(s_addr + 64 * c, s);
+              sum = make_float2(0.0f, 0.0f);
+              const float top = mask || wide ? weights64<true>(s, ks, vs, f, R, bits0, bits1, sum, w)
+                                             : weights64<false>(s, ks, vs, f, R, bits0, bits1, sum, w);
+              // (the sum too: of tokens without a value, and of all where there is no reference yet)
+              const bool over = !(top <= kHeavy) || !(sum.x + sum.y <= kMuch);
+              if (__builtin_expect(tries > 0 || !__any_sync(0xFFFFFFFFu, over), 1)) break;
+              // a reference has to move: what was summed by it before is scaled, and these weights are taken again
+              tmem_row64(s_addr + 64 * c, s);  // (again: they are not kept through the weights)
+              const float to = reference64(s, ks, vs, f, bits0, bits1);
+              float back = 1.0f;
+              if (over && to > R) {
+                back = ex2(R - to);
+                R = to;
+              }
+              wide = __any_sync(0xFFFFFFFFu, wide || (fabsf(R) >= kWide && R > -INFINITY));
+              l *= back;
+              if (!waited) {
+                ok = wait_phase(&sh.ofull[tile], (done - 1) & 1, a.status);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                waited = true;
+                tc_fence_after();
+              }
+              const int outs = i > 0 ? hd : 0;
+              tmem_wait_st();
+#pragma unroll 1
+              for (int x = 0; x < outs; x += 16) {
+                uint32_t o[16];
+                tmem_ld16(o_addr + x, o);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * back);
+                tmem_st16(o_addr + x, o);
+              }
+#pragma unroll 1
+              for (int x = 0; x < 32 * c; x += 16) {
+                uint32_t o[16];
+                tmem_ld16(s_addr + x, o);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                  const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&o[e]));
+                  o[e] = half2_bits(v.x * back, v.y * back);
+                }
+                tmem_st16(s_addr + x, o);
+              }
+            }
+            if (!ok) break;
+            l += sum.x + sum.y;
+            tmem_st32(s_addr + 32 * c, w);
           }
-          // the tile's weights are only handed over once the outputs of the one before are there: a wait by parity
-          // must not be two phases behind
-          if (i > 0) {
+          if (!ok) break;
+          // the weights are only handed over once the outputs of the tile before are there: a wait by parity must not
+          // be two phases behind
+          if (!waited) {
             ok = wait_phase(&sh.ofull[tile], (done - 1) & 1, a.status);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
           }
-          if (i > 0 && __any_sync(0xFFFFFFFFu, back != 1.0f)) {
-            tc_fence_after();
-            const uint32_t o_addr = lane_base + C::TM_O + tile * 64 * PANELS;
-            for (int c = 0; c < hd; c += 16) {
-              float o[16];
-              asm volatile(
-                  "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-                  "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
-                  "tcgen05.wait::ld.sync.aligned;"
-                  : "=f"(o[0]), "=f"(o[1]), "=f"(o[2]), "=f"(o[3]), "=f"(o[4]), "=f"(o[5]), "=f"(o[6]), "=f"(o[7]), "=f"(o[8]),
-                    "=f"(o[9]), "=f"(o[10]), "=f"(o[11]), "=f"(o[12]), "=f"(o[13]), "=f"(o[14]), "=f"(o[15])
-                  : "r"(o_addr + c)
-                  : "memory");
-#pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] *= back;
-              asm volatile(
-                  "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-                  "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(o_addr + c),
-                  "f"(o[0]), "f"(o[1]), "f"(o[2]), "f"(o[3]), "f"(o[4]), "f"(o[5]), "f"(o[6]), "f"(o[7]), "f"(o[8]), "f"(o[9]),
-                  "f"(o[10]), "f"(o[11]), "f"(o[12]), "f"(o[13]), "f"(o[14]), "f"(o[15])
-                  : "memory");
-            }
-          }
-          if (wide) l += tile_weights<C::BN, true, true>(s_addr, ks, vs, f, R, seen, valid);
-          else if (mask) l += tile_weights<C::BN, true, false>(s_addr, ks, vs, f, R, seen, valid);
-          else l += tile_weights<C::BN, false, false>(s_addr, ks, vs, f, R, seen, valid);
           tmem_wait_st();
           tc_fence_before();
           mbar_arrive(&sh.pfull[buf]);
@@ -820,118 +1074,82 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
         }
         if (ok) ok = wait_phase(&sh.ofull[tile], (done - 1) & 1, a.status);
         ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;  // nothing is stored, counted or joined
         tc_fence_after();
       }
       // (the group without rows waits for the other: the score buffers' and the scales' phases that it did not watch
       // have passed when it watches them again)
-      if (!two) named_barrier(1, kSoftmax);
+      if (!two && !meet()) break;
       g += n;
-      before[0] += two ? n : (n + 1) >> 1;
-      before[1] += two ? n : n >> 1;
-      const bool whole = n == k.w.tiles;
-      const long long orow = k.s.row0 + token;
-      if (whole) {
-        if (ok && active) {
-          const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-          __nv_bfloat16* out = a.out + orow * a.ldo + static_cast<long long>(qh) * hd;
-          for (int c = 0; c < hd; c += 16) {
-            float o[16];
-            asm volatile(
-                "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-                "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
-                "tcgen05.wait::ld.sync.aligned;"
-                : "=f"(o[0]), "=f"(o[1]), "=f"(o[2]), "=f"(o[3]), "=f"(o[4]), "=f"(o[5]), "=f"(o[6]), "=f"(o[7]), "=f"(o[8]),
-                  "=f"(o[9]), "=f"(o[10]), "=f"(o[11]), "=f"(o[12]), "=f"(o[13]), "=f"(o[14]), "=f"(o[15])
-                : "r"(lane_base + C::TM_O + tile * 64 * PANELS + c)
-                : "memory");
+      before ^= two ? 3u * (n & 1) : ((n + 1) >> 1 & 1) | (n >> 1 & 1) << 1;
+      const bool whole = k.part < 0;
+      if (active) {
+        // the whole unit: the outputs; a part of it: (reference, sum, unnormalised outputs) into the workspace
+        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+        const long long orow = k.qrow + token;
+        __nv_bfloat16* out = a.out + orow * a.ldo + static_cast<long long>(qh) * hd;
+        float* dst = p.partial + static_cast<long long>(whole ? 0 : k.part) * C::ROWS * hd + (tile * 128 + r) * 4;
+#pragma unroll 1
+        for (int c = 0; c < hd; c += 16) {
+          uint32_t u[16];
+          tmem_ld16(o_addr + c, u);
+          if (mine && whole) {
             uint32_t w[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const __nv_bfloat162 h = __floats2bfloat162_rn(o[2 * e] * inv, o[2 * e + 1] * inv);
+              const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(u[2 * e]) * inv, __uint_as_float(u[2 * e + 1]) * inv);
               w[e] = *reinterpret_cast<const uint32_t*>(&h);
             }
-            if (mine) {
-              reinterpret_cast<uint4*>(out + c)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-              reinterpret_cast<uint4*>(out + c)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-            }
-          }
-          if (a.lse && mine) {
-            const int e = exponent(l);  // (the reference may lie far from the largest score)
-            a.lse[orow * a.q_heads + qh] = l > 0.0f ? ((R + static_cast<float>(e)) + log2f(l * pow2(-e))) * 0.693147180559945309f : -INFINITY;
-          }
-        }
-        tc_fence_before();
-        continue;
-      }
-      // part of a unit: (reference, sum, outputs) into the workspace
-      const int part = 2 * static_cast<int>(blockIdx.x) + (k.t0 == 0 ? 1 : 0);
-      if (ok && active) {
-        float* dst = p.partial + static_cast<long long>(part) * C::ROWS * hd + (tile * 128 + r) * 4;
-        for (int c = 0; c < hd; c += 16) {
-          float o[16];
-          asm volatile(
-              "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-              "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
-              "tcgen05.wait::ld.sync.aligned;"
-              : "=f"(o[0]), "=f"(o[1]), "=f"(o[2]), "=f"(o[3]), "=f"(o[4]), "=f"(o[5]), "=f"(o[6]), "=f"(o[7]), "=f"(o[8]),
-                "=f"(o[9]), "=f"(o[10]), "=f"(o[11]), "=f"(o[12]), "=f"(o[13]), "=f"(o[14]), "=f"(o[15])
-              : "r"(lane_base + C::TM_O + tile * 64 * PANELS + c)
-              : "memory");
-          if (mine)
+            reinterpret_cast<uint4*>(out + c)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            reinterpret_cast<uint4*>(out + c)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+          } else if (mine) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              __stcg(reinterpret_cast<float4*>(dst + static_cast<long long>(c / 4 + e) * C::ROWS * 4),
-                     make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
+              __stcg(reinterpret_cast<uint4*>(dst + static_cast<long long>(c / 4 + e) * C::ROWS * 4),
+                     make_uint4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]));
+          }
+          __syncwarp();
         }
-        if (mine) __stcg(reinterpret_cast<float2*>(p.partial_ml + (static_cast<long long>(part) * C::ROWS + tile * 128 + r) * 2), make_float2(R, l));
+        if (mine && whole && a.lse) a.lse[orow * a.q_heads + qh] = log_sum(R, l);
+        if (mine && !whole)
+          __stcg(reinterpret_cast<float2*>(p.partial_ml + (static_cast<long long>(k.part) * C::ROWS + tile * 128 + r) * 2), make_float2(R, l));
       }
       tc_fence_before();
+      if (whole) continue;
       __threadfence();
-      if (any_of(!ok)) {  // nothing is counted or joined
-        ok = false;
-        continue;
-      }
-      const int r0 = k.range_of(0), r1 = k.range_of(k.w.tiles - 1);
+      if (!meet()) break;
       if (tid == 0) {
-        sh.last = atomicAdd(p.counter + r0, 1u) == static_cast<unsigned>(r1 - r0);
-        if (sh.last) p.counter[r0] = 0;  // ready for the next call
+        sh.last = atomicAdd(p.counter + k.r0, 1u) == static_cast<unsigned>(k.r1 - k.r0);
+        if (sh.last) p.counter[k.r0] = 0;  // ready for the next call
         __threadfence();
       }
-      named_barrier(1, kSoftmax);
-      const bool join = sh.last != 0;
-      if (join) {
-        // the parts in order of their ranges; a thread takes 4 columns of a row
-        const int rows = k.w.rows;
-        for (int it = tid; it < rows * (hd >> 2); it += kSoftmax) {
-          const int c4 = it / rows, rr = it - c4 * rows;
-          float m = -INFINITY, sum = 0.0f;
-          float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (!meet()) break;
+      if (sh.last == 0) continue;
+      // the parts in order of their ranges; a thread takes 4 columns of a row
+      for (int it = tid; it < k.rows * (hd >> 2); it += kSoftmax) {
+        const int c4 = it / k.rows, rr = it - c4 * k.rows;
+        float m = -INFINITY, sum = 0.0f;
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-          for (int x = r0; x <= r1; ++x) {
-            const long long q = 2LL * x + (x == r0 ? 1 : 0);
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.partial_ml + (q * C::ROWS + rr) * 2));
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(p.partial + q * C::ROWS * hd + (static_cast<long long>(c4) * C::ROWS + rr) * 4));
-            const float to = fmaxf(m, ml.x);
-            const float f0 = m > -INFINITY ? ex2(m - to) : 0.0f, f1 = ml.x > -INFINITY ? ex2(ml.x - to) : 0.0f;
-            m = to;
-            sum = sum * f0 + ml.y * f1;
-            o.x = o.x * f0 + v.x * f1;
-            o.y = o.y * f0 + v.y * f1;
-            o.z = o.z * f0 + v.z * f1;
-            o.w = o.w * f0 + v.w * f1;
-          }
-          const int pr = k.w.row + rr, tok = pr / group, h = k.head * group + (pr - tok * group);
-          const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-          const __nv_bfloat162 h0 = __floats2bfloat162_rn(o.x * inv, o.y * inv), h1 = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-          *reinterpret_cast<uint2*>(a.out + static_cast<long long>(k.s.row0 + tok) * a.ldo + static_cast<long long>(h) * hd + 4 * c4) =
-              make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
-          if (a.lse && c4 == 0) {
-            const int e = exponent(sum);
-            a.lse[static_cast<long long>(k.s.row0 + tok) * a.q_heads + h] =
-                sum > 0.0f ? ((m + static_cast<float>(e)) + log2f(sum * pow2(-e))) * 0.693147180559945309f : -INFINITY;
-          }
+        for (int x = k.r0; x <= k.r1; ++x) {
+          const long long q = 2LL * x + (x == k.r0 ? 1 : 0);
+          const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.partial_ml + (q * C::ROWS + rr) * 2));
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(p.partial + q * C::ROWS * hd + (static_cast<long long>(c4) * C::ROWS + rr) * 4));
+          const float to = fmaxf(m, ml.x);
+          const float f0 = m > -INFINITY ? ex2(m - to) : 0.0f, f1 = ml.x > -INFINITY ? ex2(ml.x - to) : 0.0f;
+          m = to;
+          sum = sum * f0 + ml.y * f1;
+          o.x = o.x * f0 + v.x * f1;
+          o.y = o.y * f0 + v.y * f1;
+          o.z = o.z * f0 + v.z * f1;
+          o.w = o.w * f0 + v.w * f1;
         }
-        named_barrier(1, kSoftmax);  // (sh.last is read before it is written again)
+        const int pr = k.row + rr, tok = pr / group, h = k.head * group + (pr - tok * group);
+        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+        const __nv_bfloat162 h0 = __floats2bfloat162_rn(o.x * inv, o.y * inv), h1 = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+        *reinterpret_cast<uint2*>(a.out + static_cast<long long>(k.qrow + tok) * a.ldo + static_cast<long long>(h) * hd + 4 * c4) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
+        if (a.lse && c4 == 0) a.lse[static_cast<long long>(k.qrow + tok) * a.q_heads + h] = log_sum(m, sum);
       }
     }
   }
