@@ -248,6 +248,7 @@ struct Shared {
   uint64_t sgfull[kSegments], sgempty[kSegments];     // a segment
   uint64_t qfull;                                     // a segment's queries, and its outputs may be overwritten
   uint64_t sfull[2], pfull[2], ofull[2];              // scores, weights (per score buffer), outputs (per row tile)
+  uint64_t turn[2];                                   // a row tile's MMAs of a step are issued
   uint64_t meet;                                      // the softmax threads
   uint64_t drain[2];
   uint32_t tmem;
@@ -549,6 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
       mbar_init(&sh.vfull[i], kConverters);
       mbar_init(&sh.vempty[i], 2);
       mbar_init(&sh.drain[i], 1);
+      mbar_init(&sh.turn[i], 1);
       mbar_init(&sh.sfull[i], 1);
       mbar_init(&sh.pfull[i], 128);
       mbar_init(&sh.ofull[i], 1);
@@ -680,8 +682,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
     Segment k;
     int seg = 0, t = 0, page = -1, in_page = 0, head = 0;
     bool more = next_segment(sh, 0, k, ok, a.status);
-    auto look_up = [&]() {  // the page of this lane's token in tile t of the segment
-      const int j = k.first + t * C::BN + w * C::WARP_ROWS + lane, blk = j / a.block_size;
+    auto look_up = [&]() {  // the page of this lane's token in tile t of the segment, from its end
+      const int j = k.first + (k.n - 1 - t) * C::BN + w * C::WARP_ROWS + lane, blk = j / a.block_size;
       in_page = lane < C::WARP_ROWS && j < k.stop ? j - blk * a.block_size : -1;
       if (in_page >= 0) page = __ldg(a.block_table + static_cast<long long>(k.b) * a.ld_table + blk);
       head = k.head;
@@ -772,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
       const uint64_t q0 = umma_desc_sw128(smem_addr(smem)), k0 = umma_desc_sw128(smem_addr(smem) + C::OFF_K),
                      v0 = desc_transposed(smem_addr(smem) + C::OFF_V, C::BN * 128);
       const int ksteps = (hd + 31) >> 5;
-      int g = 0, seg = 0;
+      int g = 0, seg = 0, steps = 0;
       uint32_t before = 0;  // bit b: parity of the tiles that went through score buffer b before this segment
       // Unrolled, each MMA a few instructions from constants: a loop that forms its descriptors takes 175 cycles an
       // MMA, which itself takes 64.
@@ -832,14 +834,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
         if (two) {  // the outputs of tile i - 1, then the scores of tile i, which take the weights' place
           for (int i = 0; i <= n && ok; ++i) {
             if (i < n) ok = keys(g + i);
+            // the tiles take turns: MMAs of both in one another's midst would end together, both softmax groups would
+            // then run side by side and the tensor core wait for both
+            auto turn = [&]() { return mma == 0 ? steps == 0 || wait_phase(&sh.turn[1], (steps - 1) & 1, a.status) : wait_phase(&sh.turn[0], steps & 1, a.status); };
+            if (ok && i == 0) ok = turn();
             if (ok && i > 0) {
-              ok = values(g + i - 1) && outputs(mma, mma, (g + i - 1) & 1, i - 1, i == 1);
+              ok = values(g + i - 1) && turn() && outputs(mma, mma, (g + i - 1) & 1, i - 1, i == 1);
               if (ok) umma_commit(&sh.vempty[(g + i - 1) & 1]);
             }
             if (ok && i < n) {
               scores(mma, mma, (g + i) % C::K_STAGES);
               umma_commit(&sh.kempty[(g + i) % C::K_STAGES]);
             }
+            mbar_arrive(&sh.turn[mma]);
+            ++steps;
           }
         } else if (mma == 0) {  // one row tile: the scores of tile i, in the other buffer, then the outputs of tile i - 1
           for (int i = 0; i <= n && ok; ++i) {
@@ -975,7 +983,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
       tc_fence_before();
       mbar_arrive(&sh.qfull);
       float R = -INFINITY, l = 0.0f;
-      bool wide = false;
+      bool wide = false, fresh = true;  // (fresh: no reference yet)
       if (active) {
 #pragma unroll 1
         for (int i = 0; i < n; ++i) {
@@ -987,7 +995,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
           tc_fence_after();
           const uint32_t s_addr = lane_base + buf * C::TM_S;
           // columns of this tile that the row sees (a row past the unit's: all, of a query of zeros)
-          const int j0 = k.first + i * C::BN;
+          const int j0 = k.first + (n - 1 - i) * C::BN;
           Seen seen = {0, C::BN};
           if (mine) seen = {a.window > 0 ? pos - a.window + 1 - j0 : 0, pos + 1 - j0};
           bool waited = i == 0;  // for the outputs of the tile before
@@ -1009,14 +1017,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
 #pragma unroll 1
             for (int tries = 0;; ++tries) {
               float s[64];
-              tmem_row64(s_addr + 64 * c, s);
-              sum = make_float2(0.0f, 0.0f);
-              const float top = mask || wide ? weights64<true>(s, ks, vs, f, R, bits0, bits1, sum, w)
-                                             : weights64<false>(s, ks, vs, f, R, bits0, bits1, sum, w);
-              // (the sum too: of tokens without a value, and of all where there is no reference yet)
-              const bool over = !(top <= kHeavy) || !(sum.x + sum.y <= kMuch);
-              if (__builtin_expect(tries > 0 || !__any_sync(0xFFFFFFFFu, over), 1)) break;
+              bool over = true;
+              if (!fresh) {
+                tmem_row64(s_addr + 64 * c, s);
+                sum = make_float2(0.0f, 0.0f);
+                const float top = mask || wide ? weights64<true>(s, ks, vs, f, R, bits0, bits1, sum, w)
+                                               : weights64<false>(s, ks, vs, f, R, bits0, bits1, sum, w);
+                // (the sum too: of tokens without a value, and of all where there is no reference yet)
+                over = !(top <= kHeavy) || !(sum.x + sum.y <= kMuch);
+                if (__builtin_expect(tries > 0 || !__any_sync(0xFFFFFFFFu, over), 1)) break;
+              }
               // a reference has to move: what was summed by it before is scaled, and these weights are taken again
+              fresh = false;
               tmem_row64(s_addr + 64 * c, s);  // (again: they are not kept through the weights)
               const float to = reference64(s, ks, vs, f, bits0, bits1);
               float back = 1.0f;
@@ -1125,31 +1137,54 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
       }
       if (!meet()) break;
       if (sh.last == 0) continue;
-      // the parts in order of their ranges; a thread takes 4 columns of a row
-      for (int it = tid; it < k.rows * (hd >> 2); it += kSoftmax) {
-        const int c4 = it / k.rows, rr = it - c4 * k.rows;
-        float m = -INFINITY, sum = 0.0f;
-        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-        for (int x = k.r0; x <= k.r1; ++x) {
-          const long long q = 2LL * x + (x == k.r0 ? 1 : 0);
-          const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.partial_ml + (q * C::ROWS + rr) * 2));
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(p.partial + q * C::ROWS * hd + (static_cast<long long>(c4) * C::ROWS + rr) * 4));
-          const float to = fmaxf(m, ml.x);
-          const float f0 = m > -INFINITY ? ex2(m - to) : 0.0f, f1 = ml.x > -INFINITY ? ex2(ml.x - to) : 0.0f;
-          m = to;
-          sum = sum * f0 + ml.y * f1;
-          o.x = o.x * f0 + v.x * f1;
-          o.y = o.y * f0 + v.y * f1;
-          o.z = o.z * f0 + v.z * f1;
-          o.w = o.w * f0 + v.w * f1;
+      // the parts in order of their ranges; a thread takes 4 columns of a row, of 4 rows at a time
+      const int all = k.rows * (hd >> 2);
+#pragma unroll 1
+      for (int it0 = tid; it0 < all; it0 += 4 * kSoftmax) {
+        float m[4], sum[4];
+        float4 o[4];
+        int c4[4], rr[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const int it = min(it0 + y * kSoftmax, all - 1);
+          c4[y] = it / k.rows;
+          rr[y] = it - c4[y] * k.rows;
+          m[y] = -INFINITY;
+          sum[y] = 0.0f;
+          o[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         }
-        const int pr = k.row + rr, tok = pr / group, h = k.head * group + (pr - tok * group);
-        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-        const __nv_bfloat162 h0 = __floats2bfloat162_rn(o.x * inv, o.y * inv), h1 = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-        *reinterpret_cast<uint2*>(a.out + static_cast<long long>(k.qrow + tok) * a.ldo + static_cast<long long>(h) * hd + 4 * c4) =
-            make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
-        if (a.lse && c4 == 0) a.lse[static_cast<long long>(k.qrow + tok) * a.q_heads + h] = log_sum(m, sum);
+#pragma unroll 1
+        for (int x = k.r0; x <= k.r1; ++x) {
+          const long long q = (2LL * x + (x == k.r0 ? 1 : 0)) * C::ROWS;
+          float2 ml[4];
+          float4 v[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            ml[y] = __ldcg(reinterpret_cast<const float2*>(p.partial_ml + (q + rr[y]) * 2));
+            v[y] = __ldcg(reinterpret_cast<const float4*>(p.partial + q * hd + (static_cast<long long>(c4[y]) * C::ROWS + rr[y]) * 4));
+          }
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const float to = fmaxf(m[y], ml[y].x);
+            const float f0 = m[y] > -INFINITY ? ex2(m[y] - to) : 0.0f, f1 = ml[y].x > -INFINITY ? ex2(ml[y].x - to) : 0.0f;
+            m[y] = to;
+            sum[y] = sum[y] * f0 + ml[y].y * f1;
+            o[y].x = o[y].x * f0 + v[y].x * f1;
+            o[y].y = o[y].y * f0 + v[y].y * f1;
+            o[y].z = o[y].z * f0 + v[y].z * f1;
+            o[y].w = o[y].w * f0 + v[y].w * f1;
+          }
+        }
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          if (it0 + y * kSoftmax >= all) break;
+          const int pr = k.row + rr[y], tok = pr / group, h = k.head * group + (pr - tok * group);
+          const float inv = sum[y] > 0.0f ? 1.0f / sum[y] : 0.0f;
+          const __nv_bfloat162 h0 = __floats2bfloat162_rn(o[y].x * inv, o[y].y * inv), h1 = __floats2bfloat162_rn(o[y].z * inv, o[y].w * inv);
+          *reinterpret_cast<uint2*>(a.out + static_cast<long long>(k.qrow + tok) * a.ldo + static_cast<long long>(h) * hd + 4 * c4[y]) =
+              make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
+          if (a.lse && c4[y] == 0) a.lse[static_cast<long long>(k.qrow + tok) * a.q_heads + h] = log_sum(m[y], sum[y]);
+        }
       }
     }
   }
