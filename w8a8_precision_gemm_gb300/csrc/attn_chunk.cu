@@ -168,13 +168,30 @@ __device__ __forceinline__ void wait_drain(uint64_t* bar, uint32_t parity, int* 
   }
 }
 
-__device__ __forceinline__ void umma_f16_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                                uint32_t accumulate) {
+// MMAs issued by the lane of a warp that `lead` marks, from values that are the same in all of it: what forms them then stays in
+// uniform registers.  (In a branch that one lane takes they are moved there for each MMA, 125 cycles of an MMA's 64.)
+__device__ __forceinline__ void umma_scores(uint32_t d_tmem, uint32_t alo, uint32_t blo, uint32_t hi, uint32_t idesc,
+                                            uint32_t accumulate, uint32_t lead) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "setp.ne.b32 q, %6, 0;\n\t"
+      "mov.b64 a, {%1, %3};\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(alo), "r"(blo), "r"(hi), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+// A (128 x 16 fp16) in TMEM.
+__device__ __forceinline__ void umma_outputs(uint32_t d_tmem, uint32_t a_tmem, uint32_t blo, uint32_t hi, uint32_t idesc,
+                                             uint32_t accumulate, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "setp.ne.b32 q, %6, 0;\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(blo), "r"(hi), "r"(idesc), "r"(accumulate), "r"(lead)
       : "memory");
 }
 
@@ -767,8 +784,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
   } else if (warp >= 12) {
     // ------------------------------------------------------------ MMA issuers, one for each row tile
     fewer_regs<kRegsMma>();
-    if (warp < 14 && lane == 0) {
-      const int mma = warp - 12;  // the row tile whose MMAs this thread issues
+    if (warp < 14) {
+      // the whole warp goes through the steps, its first lane issues
+      const int mma = __shfl_sync(0xFFFFFFFFu, warp, 0) - 12;  // the row tile whose MMAs this warp issues
+      const uint32_t lead = lane == 0 ? 1 : 0, tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait_phase(bar, parity, a.status)) != 0; };
+      auto commit = [&](uint64_t* bar) {
+        if (lead) umma_commit(bar);
+      };
       constexpr uint32_t id_hi = umma_idesc_f32acc(0, 0, 128, C::BN), id_lo = umma_idesc_f32acc(1, 0, 128, C::BN);  // e4m3, e5m2
       const uint32_t id_o = umma_idesc_f32acc(0, 0, 128, hd) | (1u << 16);  // B (values) transposed
       const uint64_t q0 = umma_desc_sw128(smem_addr(smem)), k0 = umma_desc_sw128(smem_addr(smem) + C::OFF_K),
@@ -776,59 +799,48 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
       const int ksteps = (hd + 31) >> 5;
       int g = 0, seg = 0, steps = 0;
       uint32_t before = 0;  // bit b: parity of the tiles that went through score buffer b before this segment
-      // Unrolled, each MMA a few instructions from constants: a loop that forms its descriptors takes 175 cycles an
-      // MMA, which itself takes 64.
       auto scores = [&](int tile, int buf, int st) {
-        const uint64_t qd = q0 + tile * (2 * C::Q_PIECE / 16), kd = k0 + st * (C::K_BYTES / 16);
-        const uint32_t at = tmem + buf * C::TM_S;
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          const uint64_t hd_q = qd + half * (C::Q_PIECE / 16);
-          const uint32_t id = half != 0 ? id_lo : id_hi;
+        const uint32_t qd = static_cast<uint32_t>(q0) + tile * (2 * C::Q_PIECE / 16), kd = static_cast<uint32_t>(k0) + st * (C::K_BYTES / 16);
+        const uint32_t at = tm + buf * C::TM_S;
+#pragma unroll(PANELS <= 2 ? 2 : 1)
+        for (int half = 0; half < 2; ++half)
 #pragma unroll
           for (int kk = 0; kk < 2 * PANELS; ++kk)
-            if (kk < ksteps)
-              umma_f8f6f4(at, hd_q + ((kk >> 2) * (128 * 128) + (kk & 3) * 32) / 16,
-                          kd + ((kk >> 2) * (C::BN * 128) + (kk & 3) * 32) / 16, id, half | kk);
-        }
-        umma_commit(&sh.sfull[buf]);
+            umma_scores(at, qd + (half * C::Q_PIECE + (kk >> 2) * (128 * 128) + (kk & 3) * 32) / 16,
+                        kd + ((kk >> 2) * (C::BN * 128) + (kk & 3) * 32) / 16, static_cast<uint32_t>(q0 >> 32), half != 0 ? id_lo : id_hi, half | kk, kk < ksteps ? lead : 0);
+        commit(&sh.sfull[buf]);
       };
       auto outputs = [&](int tile, int buf, int st, int use, bool first) {
-        if (!wait_phase(&sh.pfull[buf], ((before >> buf) + use) & 1, a.status)) return false;
+        if (!wait(&sh.pfull[buf], ((before >> buf) + use) & 1)) return false;
         tc_fence_after();
-        uint64_t vd = v0 + st * (C::V_BYTES / 16);
-        uint32_t p_at = tmem + buf * C::TM_S;
-        const uint32_t o_at = tmem + C::TM_O + tile * 64 * PANELS;
-#pragma unroll 1
-        for (int x = first ? 0 : 1; p_at < tmem + buf * C::TM_S + C::BN / 2; x = 1) {
+        const uint32_t vd = static_cast<uint32_t>(v0) + st * (C::V_BYTES / 16);
+        const uint32_t p_at = tm + buf * C::TM_S, o_at = tm + C::TM_O + tile * 64 * PANELS;
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) umma_f16_tmem_a(o_at, p_at + kk * 8, vd + kk * (16 * 128 / 16), id_o, x | kk);
-          p_at += 32;
-          vd += 4 * (16 * 128 / 16);
-        }
-        umma_commit(&sh.ofull[tile]);
+        for (int kk = 0; kk < C::BN / 16; ++kk) umma_outputs(o_at, p_at + kk * 8, vd + kk * (16 * 128 / 16), static_cast<uint32_t>(v0 >> 32), id_o, kk > 0 || !first ? 1 : 0, lead);
+        commit(&sh.ofull[tile]);
         return true;
       };
       auto keys = [&](int i) {
         // (the converters' copies and stores are fenced here, where nothing is on its way: a fence waits for loads)
-        if (!wait_phase(&sh.kfull[i % C::K_STAGES], (i / C::K_STAGES) & 1, a.status)) return false;
+        if (!wait(&sh.kfull[i % C::K_STAGES], (i / C::K_STAGES) & 1)) return false;
         fence_proxy_async_smem();
         tc_fence_after();
         return true;
       };
       auto values = [&](int i) {
-        if (!wait_phase(&sh.vfull[i & 1], (i >> 1) & 1, a.status)) return false;
+        if (!wait(&sh.vfull[i & 1], (i >> 1) & 1)) return false;
         fence_proxy_async_smem();
         return true;
       };
       for (; ok; ++seg) {
-        ok = wait_phase(&sh.sgfull[seg % kSegments], (seg / kSegments) & 1, a.status);
+        ok = wait(&sh.sgfull[seg % kSegments], (seg / kSegments) & 1);
         if (!ok) break;
-        const int n = sh.segment[seg % kSegments].n;
-        const bool two = sh.segment[seg % kSegments].rows > 128;
-        mbar_arrive(&sh.sgempty[seg % kSegments]);
+        const int n = __shfl_sync(0xFFFFFFFFu, sh.segment[seg % kSegments].n, 0);
+        const bool two = __shfl_sync(0xFFFFFFFFu, sh.segment[seg % kSegments].rows, 0) > 128;
+        __syncwarp();
+        if (lead) mbar_arrive(&sh.sgempty[seg % kSegments]);
         if (n == 0) break;
-        ok = wait_phase(&sh.qfull, seg & 1, a.status);
+        ok = wait(&sh.qfull, seg & 1);
         if (!ok) break;
         tc_fence_after();
         if (two) {  // the outputs of tile i - 1, then the scores of tile i, which take the weights' place
@@ -836,17 +848,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
             if (i < n) ok = keys(g + i);
             // the tiles take turns: MMAs of both in one another's midst would end together, both softmax groups would
             // then run side by side and the tensor core wait for both
-            auto turn = [&]() { return mma == 0 ? steps == 0 || wait_phase(&sh.turn[1], (steps - 1) & 1, a.status) : wait_phase(&sh.turn[0], steps & 1, a.status); };
+            auto turn = [&]() { return mma == 0 ? steps == 0 || wait(&sh.turn[1], (steps - 1) & 1) : wait(&sh.turn[0], steps & 1); };
             if (ok && i == 0) ok = turn();
             if (ok && i > 0) {
               ok = values(g + i - 1) && turn() && outputs(mma, mma, (g + i - 1) & 1, i - 1, i == 1);
-              if (ok) umma_commit(&sh.vempty[(g + i - 1) & 1]);
+              if (ok) commit(&sh.vempty[(g + i - 1) & 1]);
             }
             if (ok && i < n) {
               scores(mma, mma, (g + i) % C::K_STAGES);
-              umma_commit(&sh.kempty[(g + i) % C::K_STAGES]);
+              commit(&sh.kempty[(g + i) % C::K_STAGES]);
             }
-            mbar_arrive(&sh.turn[mma]);
+            if (lead) mbar_arrive(&sh.turn[mma]);
             ++steps;
           }
         } else if (mma == 0) {  // one row tile: the scores of tile i, in the other buffer, then the outputs of tile i - 1
@@ -855,21 +867,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
               ok = keys(g + i);
               if (!ok) break;
               scores(0, i & 1, (g + i) % C::K_STAGES);
-              umma_commit(&sh.kempty[(g + i) % C::K_STAGES]);
-              umma_commit(&sh.kempty[(g + i) % C::K_STAGES]);  // (for the other thread)
+              commit(&sh.kempty[(g + i) % C::K_STAGES]);
+              commit(&sh.kempty[(g + i) % C::K_STAGES]);  // (for the other thread)
             }
             if (i > 0) {
               ok = values(g + i - 1) && outputs(0, (i - 1) & 1, (g + i - 1) & 1, (i - 1) >> 1, i == 1);
               if (!ok) break;
-              umma_commit(&sh.vempty[(g + i - 1) & 1]);
-              umma_commit(&sh.vempty[(g + i - 1) & 1]);
+              commit(&sh.vempty[(g + i - 1) & 1]);
+              commit(&sh.vempty[(g + i - 1) & 1]);
             }
           }
         }
         g += n;
         before ^= two ? 3u * (n & 1) : ((n + 1) >> 1 & 1) | (n >> 1 & 1) << 1;
       }
-      umma_commit(&sh.drain[mma]);
+      commit(&sh.drain[mma]);
       wait_drain(&sh.drain[mma], 0, a.status);
     } else if (warp == 14) {
       // ---------------------------------------------------------- the segments, for all the others
