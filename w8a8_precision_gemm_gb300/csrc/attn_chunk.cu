@@ -42,7 +42,7 @@
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
-#include <cfloat>
+#include <climits>
 #include <cstdint>
 
 #include "ptx.cuh"
@@ -56,13 +56,15 @@ constexpr int kConverters = 128;  // threads 256..383
 constexpr int kThreads = 512;     // and two warps that issue the MMAs, one that hands out the segments, one without work
 // Registers a thread: 128 at launch (512 threads), moved between the warpgroups: the softmax threads' loop over 32
 // scores at a time needs room to overlap its loads, products and exponentials.
-constexpr int kRegsSoftmax = 176, kRegsConvert = 80, kRegsMma = 80;
+constexpr int kRegsSoftmax = 168, kRegsConvert = 88, kRegsMma = 88;
 static_assert(2 * kRegsSoftmax + kRegsConvert + kRegsMma <= 4 * 128, "registers at launch");
 constexpr int kRing = 8;          // tiles whose scales are kept
 constexpr int kSegments = 4;      // segments handed out ahead
-// What a unit costs beside its tiles, in tiles of one row tile, and the least that a range gets.
-constexpr int kUnitCost = 2;
-constexpr int kMinRange = 8;
+// Costs: a tile of one row tile 2, of two 3 (4100 and 5000 cycles: the tensor core has more to do, the loads are the same), a
+// unit beside its tiles 15 (measured from 6 to 30: eight prompts of 1000 tokens 291 us at 6, 266 at 15), and the least
+// that a range gets (at 16 one prompt of 500 tokens takes 60 us, at 12 35).
+constexpr int kUnitCost = 15;
+constexpr int kMinRange = 12;
 constexpr float kWide = 0x1p24f;  // scores from here on are not told apart from their neighbours
 constexpr float kFar = 100.0f;    // a reference lies no further than this below the largest score
 constexpr float kHeavy = 0x1p15f; // weights above this move the reference, and so do exponentials whose sum is above
@@ -80,6 +82,7 @@ struct ChunkCfg {
   static constexpr int Q_PIECE = CODE_PANELS * 128 * 128;  // a row tile of queries, one of the two pieces
   static constexpr int K_BYTES = CODE_PANELS * BN * 128;   // a tile of keys
   static constexpr int V_BYTES = PANELS * BN * 128;        // a tile of values as fp16
+  static constexpr int Q_LANES = PANELS == 1 ? 8 : PANELS == 2 ? 16 : 32;  // lanes that copy a row of queries, 16 bytes each
   static constexpr int LANES = PANELS == 1 ? 4 : PANELS == 2 ? 8 : 16;  // lanes per token row in the gather
   static constexpr int WARP_ROWS = BN / 4;             // token rows of a tile per converter warp
   static constexpr int LOADS = WARP_ROWS * LANES / 32; // 16-byte pieces per lane, keys and values each
@@ -223,7 +226,7 @@ __device__ __forceinline__ Seq seq_of(const AttnChunkArgs& a, int b, bool* bad =
 // A unit's rows [row, row + rows) of (token, head) pairs, and the tiles of tokens they see.
 struct Unit {
   int row, rows, tile0, tiles;
-  int weight;  // row tiles
+  int weight;  // the cost of a tile
   __device__ int cost() const { return tiles == 0 ? 0 : kUnitCost + tiles * weight; }
 };
 
@@ -240,7 +243,7 @@ __device__ __forceinline__ Unit unit_of(const AttnChunkArgs& a, const Seq& s, in
   const int lo = a.window > 0 ? max(0, first - a.window + 1) : 0;
   w.tile0 = lo / C::BN;
   w.tiles = last < 0 ? 0 : last / C::BN + 1 - w.tile0;
-  w.weight = w.rows > 128 ? 2 : 1;
+  w.weight = w.rows > 128 ? 3 : 2;
   return w;
 }
 
@@ -399,15 +402,12 @@ __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// A tile's scores seen by one row: columns [lo, hi) of the tile, and only those that are valid.
-struct Seen {
-  int lo, hi;
-  __device__ uint32_t bits(int chunk, uint32_t valid) const {
-    const int l = min(max(lo - 32 * chunk, 0), 32), h = min(max(hi - 32 * chunk, 0), 32);
-    const uint32_t below_h = h == 32 ? 0xFFFFFFFFu : (1u << h) - 1, below_l = l == 32 ? 0xFFFFFFFFu : (1u << l) - 1;
-    return below_h & ~below_l & valid;
-  }
-};
+// Of 32 tokens from column `at` of a tile on, those a row sees (columns [lo, hi)) that are valid (`valid`: a bit for each).
+__device__ __forceinline__ uint32_t seen32(int lo, int hi, int at, uint32_t valid) {
+  const int l = min(max(lo - at, 0), 32), h = min(max(hi - at, 0), 32);
+  const uint32_t below_l = l == 32 ? 0xFFFFFFFFu : (1u << l) - 1, below_h = h == 32 ? 0xFFFFFFFFu : (1u << h) - 1;
+  return below_h & ~below_l & valid;
+}
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float m;
@@ -444,6 +444,11 @@ __device__ __forceinline__ void landed(float* r) {
           "+f"(r[16]), "+f"(r[17]), "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]), "+f"(r[23]),
           "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]), "+f"(r[30]), "+f"(r[31])::"memory");
 }
+__device__ __forceinline__ void tmem_row32(uint32_t taddr, float (&r)[32]) {
+  tmem_ld32_start(taddr, r);
+  tmem_wait_ld();
+  landed(r);
+}
 __device__ __forceinline__ void tmem_row64(uint32_t taddr, float (&r)[64]) {
   tmem_ld32_start(taddr, r);
   tmem_ld32_start(taddr + 32, r + 32);
@@ -464,33 +469,19 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
 }
 
 // The weights of 64 tokens from their scores s, as fp16 pairs: w = exp2(s ks f - R) vs.  Returns the largest |w|
-// and adds the exponentials to `sum`.  Of the columns a row does not see (MASK) every weight is 0.  MASK is
-// also the form for scores so large that a product rounded apart from the difference decides (kWide).
-template <bool MASK>
-__device__ __forceinline__ float weights64(const float (&s)[64], uint32_t ks, uint32_t vs, float f, float R,
-                                           uint32_t bits0, uint32_t bits1, float2& sum, uint32_t (&w)[32]) {
+// and adds the exponentials to `sum`.
+__device__ __forceinline__ float weights64(const float (&s)[64], uint32_t ks, uint32_t vs, float f, float R, float2& sum,
+                                           uint32_t (&w)[32]) {
   float2 sum0 = make_float2(0.0f, 0.0f), sum1 = sum0;
   const float2 f2 = make_float2(f, f), r2 = make_float2(-R, -R);
   float m0 = 0.0f, m1 = 0.0f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     const float4 k = ld_shared_f4(ks + 16 * i), v = ld_shared_f4(vs + 16 * i);
-    const float2 y0 = __fmul2_rn(make_float2(s[4 * i], s[4 * i + 1]), make_float2(k.x, k.y));
-    const float2 y1 = __fmul2_rn(make_float2(s[4 * i + 2], s[4 * i + 3]), make_float2(k.z, k.w));
-    const float2 z0 = MASK ? __fadd2_rn(__fmul2_rn(y0, f2), r2) : __ffma2_rn(y0, f2, r2);
-    const float2 z1 = MASK ? __fadd2_rn(__fmul2_rn(y1, f2), r2) : __ffma2_rn(y1, f2, r2);
-    float2 p0 = make_float2(ex2(z0.x), ex2(z0.y)), p1 = make_float2(ex2(z1.x), ex2(z1.y));
-    float2 w0, w1;
-    if (MASK) {
-      const uint32_t b = (i < 8 ? bits0 : bits1) >> (4 * (i & 7));
-      p0 = make_float2(b & 1 ? p0.x : 0.0f, b & 2 ? p0.y : 0.0f);
-      p1 = make_float2(b & 4 ? p1.x : 0.0f, b & 8 ? p1.y : 0.0f);
-      w0 = make_float2(b & 1 ? p0.x * v.x : 0.0f, b & 2 ? p0.y * v.y : 0.0f);
-      w1 = make_float2(b & 4 ? p1.x * v.z : 0.0f, b & 8 ? p1.y * v.w : 0.0f);
-    } else {
-      w0 = __fmul2_rn(p0, make_float2(v.x, v.y));
-      w1 = __fmul2_rn(p1, make_float2(v.z, v.w));
-    }
+    const float2 z0 = __ffma2_rn(__fmul2_rn(make_float2(s[4 * i], s[4 * i + 1]), make_float2(k.x, k.y)), f2, r2);
+    const float2 z1 = __ffma2_rn(__fmul2_rn(make_float2(s[4 * i + 2], s[4 * i + 3]), make_float2(k.z, k.w)), f2, r2);
+    const float2 p0 = make_float2(ex2(z0.x), ex2(z0.y)), p1 = make_float2(ex2(z1.x), ex2(z1.y));
+    const float2 w0 = __fmul2_rn(p0, make_float2(v.x, v.y)), w1 = __fmul2_rn(p1, make_float2(v.z, v.w));
     sum0 = __fadd2_rn(sum0, p0);
     sum1 = __fadd2_rn(sum1, p1);
     m0 = max3(m0, fabsf(w0.x), fabsf(w0.y));
@@ -498,30 +489,70 @@ __device__ __forceinline__ float weights64(const float (&s)[64], uint32_t ks, ui
     w[2 * i] = half2_bits(w0.x, w0.y);
     w[2 * i + 1] = half2_bits(w1.x, w1.y);
   }
-  sum = __fadd2_rn(sum, __fadd2_rn(sum0, sum1));
+  sum = __fadd2_rn(sum0, sum1);
   return fmaxf(m0, m1);
 }
 
-// The reference that puts the largest weight of these 64 tokens at 2^3 (see kWide and kFar for its limits), from
-// their scores; -infinity if none counts.
-__device__ __forceinline__ float reference64(const float (&s)[64], uint32_t ks, uint32_t vs, float f, uint32_t bits0,
-                                             uint32_t bits1) {
-  float most = -INFINITY, heavy = -INFINITY;
+// The same, stored, for tokens of which some do not count (those a row does not see, below `lo` or from `hi` on in the tile,
+// or not in `valid`), or whose scores are so large that a product rounded apart from the difference decides (kWide).
+// Returns the sum of the exponentials.  A loop over short code, as reference64: what runs once or twice in a unit is fetched
+// each time, at several cycles an instruction.  at: the first token in the tile; the weights lie where no score is
+// still to be read.
+__device__ __forceinline__ float weights64_slow(uint32_t taddr, uint32_t to, uint32_t ks, uint32_t vs, float f, float R, int at, int lo,
+                                                int hi, const uint32_t* valid) {
+  float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    float s[32];
+    uint32_t w[16];
+    tmem_row32(taddr + 32 * h, s);
+    const uint32_t bits = seen32(lo, hi, at + 32 * h, valid[h]);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float4 k = ld_shared_f4(ks + 16 * i), v = ld_shared_f4(vs + 16 * i);
-    const float kk[4] = {k.x, k.y, k.z, k.w}, vv[4] = {v.x, v.y, v.z, v.w};
-    const uint32_t b = (i < 8 ? bits0 : bits1) >> (4 * (i & 7));
+    for (int i = 0; i < 8; ++i) {
+      const float4 k = ld_shared_f4(ks + 128 * h + 16 * i), v = ld_shared_f4(vs + 128 * h + 16 * i);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float x = __fmul_rn(__fmul_rn(s[4 * i + e], kk[e]), f);
-      if (b >> e & 1) {
-        most = fmaxf(most, x);
-        heavy = fmaxf(heavy, x + lg2(fabsf(vv[e])));
+      for (int e = 0; e < 4; e += 2) {
+        const float2 y = __fmul2_rn(make_float2(s[4 * i + e], s[4 * i + e + 1]), e == 0 ? make_float2(k.x, k.y) : make_float2(k.z, k.w));
+        const float2 z = __fadd2_rn(__fmul2_rn(y, make_float2(f, f)), make_float2(-R, -R));
+        const bool b0 = bits >> (4 * i + e) & 1, b1 = bits >> (4 * i + e + 1) & 1;
+        const float2 p = make_float2(b0 ? ex2(z.x) : 0.0f, b1 ? ex2(z.y) : 0.0f);
+        sum = __fadd2_rn(sum, p);
+        // (a scale of a token that does not count is nothing to multiply by)
+        w[2 * i + e / 2] = half2_bits(p.x * (b0 ? (e == 0 ? v.x : v.z) : 0.0f), p.y * (b1 ? (e == 0 ? v.y : v.w) : 0.0f));
+      }
+    }
+    tmem_st16(to + 16 * h, w);
+  }
+  return sum.x + sum.y;
+}
+
+// The reference that puts the largest weight of the same tokens at 2^3 (see kWide and kFar for its limits), from their
+// scores; -infinity if none counts.
+__device__ __forceinline__ float reference64(uint32_t taddr, uint32_t ks, uint32_t vs, float f, int at, int lo, int hi,
+                                             const uint32_t* valid) {
+  float most[4], heavy[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) most[e] = heavy[e] = -INFINITY;
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    float s[32];
+    tmem_row32(taddr + 32 * h, s);
+    const uint32_t bits = seen32(lo, hi, at + 32 * h, valid[h]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float4 k = ld_shared_f4(ks + 128 * h + 16 * i), v = ld_shared_f4(vs + 128 * h + 16 * i);
+      const float kk[4] = {k.x, k.y, k.z, k.w}, vv[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float x = bits >> (4 * i + e) & 1 ? __fmul_rn(__fmul_rn(s[4 * i + e], kk[e]), f) : -INFINITY;
+        most[e] = fmaxf(most[e], x);
+        heavy[e] = fmaxf(heavy[e], x > -INFINITY ? x + lg2(fabsf(vv[e])) : x);
       }
     }
   }
-  return fabsf(most) < kWide ? fmaxf(heavy - 3.0f, most - kFar) : most;
+  most[0] = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
+  heavy[0] = fmaxf(fmaxf(heavy[0], heavy[1]), fmaxf(heavy[2], heavy[3]));
+  return fabsf(most[0]) < kWide ? fmaxf(heavy[0] - 3.0f, most[0] - kFar) : most[0];
 }
 
 // The natural logarithm of a row's sum of exponentials, from its reference and its sum by it (the reference may
@@ -935,8 +966,71 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
       ok = __all_sync(0xFFFFFFFFu, ok);
       return ok;
     };
+    // Queries: copied as they are while the last tile of the segment before is under way, then turned in place into two
+    // pieces, e4m3 and the rest as e5m2 (16 values as bf16 lie where their 16 bytes of each piece come to lie).
+    const int q_steps = (hd + 31) >> 5 << 1;
+    const uint32_t q_tile = smem_addr(smem) + 2 * tile * C::Q_PIECE;
+    auto spot = [&](int row, int step) { return q_tile + (step >> 3) * (128 * 128) + row * 128 + (((step & 7) ^ (row & 7)) << 4); };
+    auto copy_queries = [&](const Segment& s) {  // the warp's rows; zeros past the head and past the unit
+      if (tile * 128 >= s.rows && tile != 0) return;
+      const int vec = lane % C::Q_LANES;
+#pragma unroll 2
+      for (int x = 0; x < C::Q_LANES; ++x) {
+        const int row = (warp & 3) * 32 + x * (32 / C::Q_LANES) + lane / C::Q_LANES, at = tile * 128 + row, pair = s.row + at;
+        const int token = pair / group, qh = s.head * group + (pair - token * group);
+        const bool there = at < s.rows && vec * 8 < hd;
+        const __nv_bfloat16* src = a.q;
+        if (there) src += static_cast<long long>(s.qrow + token) * a.ldq + static_cast<long long>(qh) * hd + vec * 8;
+        if (vec < 2 * q_steps) cp_async16(spot(row, vec >> 1) + (vec & 1) * C::Q_PIECE, src, there ? 16 : 0);
+      }
+    };
+    auto turn_queries = [&]() {  // this thread's row; returns what makes log2 units of a raw score times the key's scale
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncwarp();
+      __nv_bfloat162 m = __floats2bfloat162_rn(0.0f, 0.0f);
+#pragma unroll 2
+      for (int i = 0; i < q_steps; ++i) {
+        const uint4 u0 = ld_shared(spot(r, i)), u1 = ld_shared(spot(r, i) + C::Q_PIECE);
+        const uint32_t uw[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t x = uw[e] & 0x7FFF7FFFu;
+          m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162*>(&x));
+        }
+      }
+      const float top = fmaxf(__low2float(m), __high2float(m));
+      // (a row below 2^-113: fewer bits, nothing to score)
+      const int up = min(7 - exponent(top), 120);
+      const float f1 = a.scale < 0.0f ? -pow2(up / 2) : pow2(up / 2), f2 = pow2(up - up / 2);
+#pragma unroll 1
+      for (int i = 0; i < q_steps; ++i) {
+        const uint4 u0 = ld_shared(spot(r, i)), u1 = ld_shared(spot(r, i) + C::Q_PIECE);
+        const uint32_t uw[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float x0 = __uint_as_float(uw[e] << 16) * f1 * f2, x1 = __uint_as_float(uw[e] & 0xFFFF0000u) * f1 * f2;
+          const uint32_t c = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
+          const float2 v = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c), __NV_E4M3)));
+          const uint32_t d = __nv_cvt_float2_to_fp8x2(make_float2(x0 - v.x, x1 - v.y), __NV_SATFINITE, __NV_E5M2);
+          hi[e >> 1] = (e & 1) != 0 ? hi[e >> 1] | c << 16 : c;
+          lo[e >> 1] = (e & 1) != 0 ? lo[e >> 1] | d << 16 : d;
+        }
+        st_shared(spot(r, i), make_uint4(hi[0], hi[1], hi[2], hi[3]));
+        st_shared(spot(r, i) + C::Q_PIECE, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+      }
+      fence_proxy_async_smem();
+      return fabsf(a.scale) * 1.44269504088896340736f / fabsf(f1) / f2;
+    };
     Segment k;
-    for (int seg = 0; ok && next_segment(sh, seg, k, ok, a.status); ++seg) {
+    float f = 0.0f;
+    bool more = next_segment(sh, 0, k, ok, a.status);
+    if (more) {
+      copy_queries(k);
+      if (tile == 0 || k.rows > 128) f = turn_queries();
+      mbar_arrive(&sh.qfull);
+    }
+    for (int seg = 0; ok && more; ++seg) {
       const int n = k.n;
       const bool two = k.rows > 128, active = tile == 0 || two;
       const bool mine = tile * 128 + r < k.rows;
@@ -944,56 +1038,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
       const int token = pair / group, qh = k.head * group + (pair - token * group);
       const int pos = k.pos + token;
       const uint32_t o_addr = lane_base + C::TM_O + tile * 64 * PANELS;
-      float f = 0.0f;
-      if (active) {
-        // this row's queries in two pieces: e4m3, and the rest as e5m2
-        const uint4* src = reinterpret_cast<const uint4*>(a.q + static_cast<long long>(k.qrow + token) * a.ldq +
-                                                          static_cast<long long>(qh) * hd);
-        const int vecs = mine ? hd >> 3 : 0;
-        auto vec = [&](int i) { return i < vecs ? __ldg(src + i) : make_uint4(0, 0, 0, 0); };
-        __nv_bfloat162 m = __floats2bfloat162_rn(0.0f, 0.0f);
-        {
-          uint4 u[8 * PANELS];
-#pragma unroll
-          for (int i = 0; i < 8 * PANELS; ++i) u[i] = vec(i);
-#pragma unroll
-          for (int i = 0; i < 8 * PANELS; ++i) {
-            const uint32_t uw[4] = {u[i].x & 0x7FFF7FFFu, u[i].y & 0x7FFF7FFFu, u[i].z & 0x7FFF7FFFu, u[i].w & 0x7FFF7FFFu};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162*>(&uw[e]));
-          }
-        }
-        const float top = fmaxf(__low2float(m), __high2float(m));
-        // (a row below 2^-113: fewer bits, nothing to score)
-        const int up = min(7 - exponent(top), 120);
-        const float f1 = a.scale < 0.0f ? -pow2(up / 2) : pow2(up / 2), f2 = pow2(up - up / 2);
-        const uint32_t dst = smem_addr(smem) + 2 * tile * C::Q_PIECE + r * 128;
-        uint4 u0 = vec(0), u1 = vec(1);
-#pragma unroll 1
-        for (int i = 0; i < (hd + 31) >> 5 << 1; ++i) {  // 16 values; zeros past the head
-          const uint32_t uw[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
-          u0 = vec(2 * i + 2);
-          u1 = vec(2 * i + 3);
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float x0 = __uint_as_float(uw[e] << 16) * f1 * f2, x1 = __uint_as_float(uw[e] & 0xFFFF0000u) * f1 * f2;
-            const uint32_t c = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
-            const float2 v = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c), __NV_E4M3)));
-            const uint32_t d = __nv_cvt_float2_to_fp8x2(make_float2(x0 - v.x, x1 - v.y), __NV_SATFINITE, __NV_E5M2);
-            hi[e >> 1] = (e & 1) != 0 ? hi[e >> 1] | c << 16 : c;
-            lo[e >> 1] = (e & 1) != 0 ? lo[e >> 1] | d << 16 : d;
-          }
-          const uint32_t o = dst + (i >> 3) * (128 * 128) + (((i & 7) ^ (r & 7)) << 4);
-          st_shared(o, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-          st_shared(o + C::Q_PIECE, make_uint4(lo[0], lo[1], lo[2], lo[3]));
-        }
-        // raw score x the key's scale x this = score in log2 units
-        f = fabsf(a.scale) * 1.44269504088896340736f / fabsf(f1) / f2;
-        fence_proxy_async_smem();
-      }
-      tc_fence_before();
-      mbar_arrive(&sh.qfull);
       float R = -INFINITY, l = 0.0f;
       bool wide = false, fresh = true;  // (fresh: no reference yet)
       if (active) {
@@ -1005,50 +1049,50 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
           ok = __all_sync(0xFFFFFFFFu, ok);
           if (!ok) break;
           tc_fence_after();
+          if (i == n - 1) {  // the queries have been read: the next segment's
+            ok = wait_phase(&sh.sgfull[(seg + 1) % kSegments], ((seg + 1) / kSegments) & 1, a.status);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            if (sh.segment[(seg + 1) % kSegments].n > 0) copy_queries(sh.segment[(seg + 1) % kSegments]);
+          }
           const uint32_t s_addr = lane_base + buf * C::TM_S;
           // columns of this tile that the row sees (a row past the unit's: all, of a query of zeros)
           const int j0 = k.first + (n - 1 - i) * C::BN;
-          Seen seen = {0, C::BN};
-          if (mine) seen = {a.window > 0 ? pos - a.window + 1 - j0 : 0, pos + 1 - j0};
+          const int hi = mine ? pos + 1 - j0 : C::BN, reach = mine && a.window > 0 ? a.window : INT_MAX;
           bool waited = i == 0;  // for the outputs of the tile before
-          bool mask = seen.lo > 0 || seen.hi < C::BN;
           uint32_t every = 0xFFFFFFFFu;
 #pragma unroll
           for (int c = 0; c < C::BN / 32; ++c) every &= sh.valid[ring][c];
-          mask = __any_sync(0xFFFFFFFFu, mask || every != 0xFFFFFFFFu);
+          const bool mask = __any_sync(0xFFFFFFFFu, hi > reach || hi < C::BN || every != 0xFFFFFFFFu);
 #pragma unroll 1
           for (int c = 0; c < C::BN / 64; ++c) {
             const uint32_t ks = smem_addr(sh.ks[ring]) + 256 * c, vs = smem_addr(sh.vs[ring]) + 256 * c;
-            uint32_t bits0 = 0xFFFFFFFFu, bits1 = 0xFFFFFFFFu;
-            if (mask) {
-              bits0 = seen.bits(2 * c, sh.valid[ring][2 * c]);
-              bits1 = seen.bits(2 * c + 1, sh.valid[ring][2 * c + 1]);
-            }
-            uint32_t w[32];
-            float2 sum;
-#pragma unroll 1
-            for (int tries = 0;; ++tries) {
+            if (!mask && !wide && !fresh) {
               float s[64];
-              bool over = true;
-              if (!fresh) {
-                tmem_row64(s_addr + 64 * c, s);
-                sum = make_float2(0.0f, 0.0f);
-                const float top = mask || wide ? weights64<true>(s, ks, vs, f, R, bits0, bits1, sum, w)
-                                               : weights64<false>(s, ks, vs, f, R, bits0, bits1, sum, w);
-                // (the sum too: of tokens without a value, and of all where there is no reference yet)
-                over = !(top <= kHeavy) || !(sum.x + sum.y <= kMuch);
-                if (__builtin_expect(tries > 0 || !__any_sync(0xFFFFFFFFu, over), 1)) break;
+              uint32_t w[32];
+              float2 sum;
+              tmem_row64(s_addr + 64 * c, s);
+              const float top = weights64(s, ks, vs, f, R, sum, w);
+              // (the sum too: of tokens without a value, and of all where there is no reference yet)
+              const bool over = !(top <= kHeavy) || !(sum.x + sum.y <= kMuch);
+              if (__builtin_expect(!__any_sync(0xFFFFFFFFu, over), 1)) {
+                l += sum.x + sum.y;
+                tmem_st32(s_addr + 32 * c, w);
+                continue;
               }
-              // a reference has to move: what was summed by it before is scaled, and these weights are taken again
-              fresh = false;
-              tmem_row64(s_addr + 64 * c, s);  // (again: they are not kept through the weights)
-              const float to = reference64(s, ks, vs, f, bits0, bits1);
-              float back = 1.0f;
-              if (over && to > R) {
-                back = ex2(R - to);
-                R = to;
-              }
-              wide = __any_sync(0xFFFFFFFFu, wide || (fabsf(R) >= kWide && R > -INFINITY));
+            }
+            const int lo = max(hi, 0) - reach;
+            const float to = reference64(s_addr + 64 * c, ks, vs, f, 64 * c, lo, hi, &sh.valid[ring][2 * c]);
+            float back = 1.0f;
+            // (not for less than 2^8: the weights may be as much above where a reference puts them)
+            const bool moves = to > R + 8.0f || (fabsf(to) >= kWide && to > R);
+            if (moves) {
+              back = ex2(R - to);
+              R = to;
+            }
+            wide = __any_sync(0xFFFFFFFFu, wide || (fabsf(R) >= kWide && R > -INFINITY));
+            if (!fresh && __any_sync(0xFFFFFFFFu, moves)) {
+              // what was summed by the old reference is scaled
               l *= back;
               if (!waited) {
                 ok = wait_phase(&sh.ofull[tile], (done - 1) & 1, a.status);
@@ -1079,9 +1123,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
                 tmem_st16(s_addr + x, o);
               }
             }
-            if (!ok) break;
-            l += sum.x + sum.y;
-            tmem_st32(s_addr + 32 * c, w);
+            fresh = false;
+            l += weights64_slow(s_addr + 64 * c, s_addr + 32 * c, ks, vs, f, R, 64 * c, lo, hi, &sh.valid[ring][2 * c]);
           }
           if (!ok) break;
           // the weights are only handed over once the outputs of the tile before are there: a wait by parity must not
@@ -1106,13 +1149,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
       if (!two && !meet()) break;
       g += n;
       before ^= two ? 3u * (n & 1) : ((n + 1) >> 1 & 1) | (n >> 1 & 1) << 1;
-      const bool whole = k.part < 0;
+      // the next segment's scores are computed while this one's outputs are stored
+      const Segment was = k;
+      more = next_segment(sh, seg + 1, k, ok, a.status);
+      if (!ok) break;
+      if (more) {
+        if (!active) copy_queries(k);  // (the other threads have)
+        if (tile == 0 || k.rows > 128) f = turn_queries();
+        tc_fence_before();
+        mbar_arrive(&sh.qfull);
+      }
+      const bool whole = was.part < 0;
       if (active) {
         // the whole unit: the outputs; a part of it: (reference, sum, unnormalised outputs) into the workspace
         const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-        const long long orow = k.qrow + token;
+        const long long orow = was.qrow + token;
         __nv_bfloat16* out = a.out + orow * a.ldo + static_cast<long long>(qh) * hd;
-        float* dst = p.partial + static_cast<long long>(whole ? 0 : k.part) * C::ROWS * hd + (tile * 128 + r) * 4;
+        float* dst = p.partial + static_cast<long long>(whole ? 0 : was.part) * C::ROWS * hd + (tile * 128 + r) * 4;
 #pragma unroll 1
         for (int c = 0; c < hd; c += 16) {
           uint32_t u[16];
@@ -1136,21 +1189,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
         }
         if (mine && whole && a.lse) a.lse[orow * a.q_heads + qh] = log_sum(R, l);
         if (mine && !whole)
-          __stcg(reinterpret_cast<float2*>(p.partial_ml + (static_cast<long long>(k.part) * C::ROWS + tile * 128 + r) * 2), make_float2(R, l));
+          __stcg(reinterpret_cast<float2*>(p.partial_ml + (static_cast<long long>(was.part) * C::ROWS + tile * 128 + r) * 2), make_float2(R, l));
       }
       tc_fence_before();
       if (whole) continue;
       __threadfence();
       if (!meet()) break;
       if (tid == 0) {
-        sh.last = atomicAdd(p.counter + k.r0, 1u) == static_cast<unsigned>(k.r1 - k.r0);
-        if (sh.last) p.counter[k.r0] = 0;  // ready for the next call
+        sh.last = atomicAdd(p.counter + was.r0, 1u) == static_cast<unsigned>(was.r1 - was.r0);
+        if (sh.last) p.counter[was.r0] = 0;  // ready for the next call
         __threadfence();
       }
       if (!meet()) break;
       if (sh.last == 0) continue;
       // the parts in order of their ranges; a thread takes 4 columns of a row, of 4 rows at a time
-      const int all = k.rows * (hd >> 2);
+      const int all = was.rows * (hd >> 2);
 #pragma unroll 1
       for (int it0 = tid; it0 < all; it0 += 4 * kSoftmax) {
         float m[4], sum[4];
@@ -1159,15 +1212,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
           const int it = min(it0 + y * kSoftmax, all - 1);
-          c4[y] = it / k.rows;
-          rr[y] = it - c4[y] * k.rows;
+          c4[y] = it / was.rows;
+          rr[y] = it - c4[y] * was.rows;
           m[y] = -INFINITY;
           sum[y] = 0.0f;
           o[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         }
-#pragma unroll 1
-        for (int x = k.r0; x <= k.r1; ++x) {
-          const long long q = (2LL * x + (x == k.r0 ? 1 : 0)) * C::ROWS;
+#pragma unroll 2
+        for (int x = was.r0; x <= was.r1; ++x) {
+          const long long q = (2LL * x + (x == was.r0 ? 1 : 0)) * C::ROWS;
           float2 ml[4];
           float4 v[4];
 #pragma unroll
@@ -1190,12 +1243,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
           if (it0 + y * kSoftmax >= all) break;
-          const int pr = k.row + rr[y], tok = pr / group, h = k.head * group + (pr - tok * group);
+          const int pr = was.row + rr[y], tok = pr / group, h = was.head * group + (pr - tok * group);
           const float inv = sum[y] > 0.0f ? 1.0f / sum[y] : 0.0f;
           const __nv_bfloat162 h0 = __floats2bfloat162_rn(o[y].x * inv, o[y].y * inv), h1 = __floats2bfloat162_rn(o[y].z * inv, o[y].w * inv);
-          *reinterpret_cast<uint2*>(a.out + static_cast<long long>(k.qrow + tok) * a.ldo + static_cast<long long>(h) * hd + 4 * c4[y]) =
+          *reinterpret_cast<uint2*>(a.out + static_cast<long long>(was.qrow + tok) * a.ldo + static_cast<long long>(h) * hd + 4 * c4[y]) =
               make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
-          if (a.lse && c4[y] == 0) a.lse[static_cast<long long>(k.qrow + tok) * a.q_heads + h] = log_sum(m[y], sum[y]);
+          if (a.lse && c4[y] == 0) a.lse[static_cast<long long>(was.qrow + tok) * a.q_heads + h] = log_sum(m[y], sum[y]);
         }
       }
     }
