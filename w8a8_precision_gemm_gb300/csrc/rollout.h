@@ -149,7 +149,7 @@ struct RopeArgs {
   const int* positions;
   const double* inv_freq;
   float factor;
-  int group;  // lanes per head, set by the launch
+  int group, parts;  // lanes per head, warps that share a token's heads: set by the launch
   // with the cache
   int kv_heads;
   const long long* slots;
