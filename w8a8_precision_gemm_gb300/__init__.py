@@ -439,17 +439,16 @@ def _rotation(M, head_dim, positions, inv_freq):
     return rot, at, freq
 
 
-def _apart(x, out):
-    """out is x itself, or shares no memory with it as far as the views' own elements tell."""
-    if out.data_ptr() == x.data_ptr():
+def _apart(M, x, ldx, columns, out, ldo, out_columns):
+    """Of matrices of M rows: out is x itself, or shares no memory with it as far as the columns in use tell."""
+    a, b = x.data_ptr(), out.data_ptr()
+    if a == b or M == 0:
         return
-    end = lambda t: t.data_ptr() + t.element_size() * (1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride())))  # noqa: E731
-    if x.numel() and out.numel() and x.data_ptr() < end(out) and out.data_ptr() < end(x) \
-            and x.untyped_storage().data_ptr() == out.untyped_storage().data_ptr():
+    size, out_size = x.element_size(), out.element_size()
+    if a < b + out_size * ((M - 1) * ldo + out_columns) and b < a + size * ((M - 1) * ldx + columns):
         # (columns of one matrix, side by side)
-        ld, size = x.stride(0), x.element_size()
-        gap = (out.data_ptr() - x.data_ptr()) // size % ld if ld else 0
-        if x.dtype is not out.dtype or out.stride(0) != ld or gap < x.shape[1] or gap + out.shape[1] > ld:
+        gap = (b - a) // size % ldx if ldx else 0
+        if x.dtype is not out.dtype or ldo != ldx or gap < columns or gap + out_columns > ldx:
             raise ValueError("out overlaps the input")
 
 
@@ -462,7 +461,7 @@ def qurl_rope(X, heads, head_dim, positions, inv_freq, out, layout=ROPE_HALF, fa
     ldx, ldo = _ld(X), _ld(out)
     if min(X.shape[1], out.shape[1]) < heads * head_dim:
         raise ValueError("X and out have heads * head_dim columns at least")
-    _apart(X[:, :heads * head_dim], out[:, :heads * head_dim])
+    _apart(M, X, ldx, heads * head_dim, out, ldo, heads * head_dim)
     rot, at, freq = _rotation(M, head_dim, positions, inv_freq)
     _ok(load().qurl_rope(X.data_ptr(), FP32 if X.dtype is torch.float32 else BF16, M, ldx, heads, head_dim, at, freq,
                          rot, layout, factor, 1 if inverse else 0, out.data_ptr(), ldo, _stream(stream)), "qurl_rope")
@@ -483,7 +482,7 @@ def qurl_rope_kv_cache_quant(qkv, q_heads, positions, inv_freq, q_out, slot_mapp
     if columns < (q_heads + 2 * kv_heads) * head_dim or q_out.shape[1] < q_heads * head_dim:
         raise ValueError("qkv has the columns of q_heads + 2 kv_heads heads, q_out those of q_heads")
     ldq, ldo = _ld(qkv), _ld(q_out)
-    _apart(qkv[:, :(q_heads + 2 * kv_heads) * head_dim], q_out[:, :q_heads * head_dim])
+    _apart(M, qkv, ldq, (q_heads + 2 * kv_heads) * head_dim, q_out, ldo, q_heads * head_dim)
     rot, at, freq = _rotation(M, head_dim, positions, inv_freq)
     ks, vs = _vec(torch.float32, num_slots * kv_heads, (k_scale, "k_scale"), (v_scale, "v_scale"))
     slots, = _vec(torch.int64, M, (slot_mapping, "slot_mapping"))
