@@ -549,8 +549,9 @@ qurl_status qurl_kv_attn_decode(const void* q, int ldq, int B, int q_heads, int 
  * Lengths, rows and pages are read on the device: a token whose page is negative or past num_slots is left out,
  * a length past max_blocks * block_size is cut to it, rows past M or in decreasing order count as none, and
  * each latches QURL_ERR_INVALID_ARG in the device status word.
- * Sums are fp32.  A weight softmax(s)_j * v_scale is within 2^-11 of its value, or 2^-27 of the row's largest, whatever the
- * tokens' scales from 2^-100 to 2^100; for scores of 2^24 and more (in log2 units), which are not told apart from
+ * Sums are fp32.  A value of q enters exactly, or (below 2^-13 of its row's largest) within 2^-21 of that.  A weight
+ * softmax(s)_j * v_scale is within 2^-10.9 of its value, or 2^-27 of the row's largest, whatever the tokens' scales
+ * from 2^-100 to 2^100; for scores of 2^24 and more (in log2 units), which are not told apart from
  * their neighbours, scales from 2^-14 to 2^15.  Results are identical run to run.
  * B = 0 and M = 0 are valid.  Errors: INVALID_ARG (NULL, a size out of range, q_heads % kv_heads, ld_table <
  * max_blocks, window < 0, scale not finite), UNSUPPORTED (head_dim; M * q_heads of 2^31 or more, max_blocks *

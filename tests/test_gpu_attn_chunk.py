@@ -1,10 +1,12 @@
 """Causal attention of several new tokens per sequence over the paged FP8 cache
 (qurl_kv_attn_chunk) against the formula in 64 bits on the cache's own codes and scales.
 
-Tolerances, from the arithmetic.  Scores: a query value is exact as fp16 or off by 2^-40 of
-its row's largest, products with a code are exact and summed in fp32, so s is within
-e = (head_dim + 8) 2^-24 sum_d |q_d k_d| scale of its value, which is the relative error of
-exp(s) above and below the fraction.  A weight is rounded to fp16, half a step: 2^-11 of
+Tolerances, from the arithmetic.  A query row is scaled so that its largest value is in [2^7, 2^8) and enters as e4m3
+(4 significant bits, steps of 2^-9 below 2^-6) and the rest as e5m2 (3 bits, steps of 2^-16 below 2^-14).  A bf16 value has
+8 bits: from 2^-6 on the rest is at most 8 units of its last place, whole ones of 2^-13 at least, and exact; below, the rest is at
+most 2^-10 and off by at most half a step there, 2^-14: 2^-21 of the row's largest.  Products with a code are
+exact and summed in fp32, so s is within e = ((head_dim + 8) 2^-24 sum_d |q_d k_d| + 2^-21 max |q| sum_d |k_d|) scale of
+its value, which is the relative error of exp(s) above and below the fraction.  A weight is rounded to fp16, half a step: 2^-11 of
 the value (with the fp32 roundings around it 2^-10.9), or 2^-27 of the row's largest weight
 (of exp(s) times the value's scale) where that is more; a tensor-core sum in fp32 adds 2^-20
 of the magnitudes.  So before its rounding to bf16 (half a step: 2^-8 of the value) an output is
@@ -90,7 +92,8 @@ def reference(a, keep=None):
             out[rows] = o
             lse[rows] = torch.logsumexp(s, -1).permute(2, 0, 1).reshape(len(rows), hq)
             e = torch.einsum("mhgd,lhd->hgml", x.abs(), k.abs()) * abs(a["scale"])
-            e = (hd + 8) * 2.0 ** -24 * e.masked_fill(hide, 0.0).amax(-1).permute(2, 0, 1).reshape(len(rows), hq)
+            small = torch.einsum("mhg,lh->hgml", x.abs().amax(-1), k.abs().sum(-1)) * abs(a["scale"])
+            e = ((hd + 8) * 2.0 ** -24 * e + 2.0 ** -21 * small).masked_fill(hide, 0.0).amax(-1).permute(2, 0, 1).reshape(len(rows), hq)
             serr[rows] = e
             top = (p * vs).amax(-1).permute(2, 0, 1).reshape(len(rows), hq)
             low = 2.0 ** -27 * 448 * len(j) * top
