@@ -1,193 +1,243 @@
-"""The operators between the qkv linear and the output projection as a rollout runs them: pages taken for the new tokens
-(qurl_kv_append), rotation and quantization into them (qurl_rope_kv_cache_quant), attention over them
-(qurl_kv_attn_chunk, qurl_kv_attn_decode for single tokens), pages given back (qurl_kv_release).
+"""The operators of a rollout and training step together, as an engine runs them:
+a decoder layer's decode step (RMSNorm -> qkv linear -> FP8 cache -> attention ->
+output projection -> residual update and norms -> MLP -> residual update and norm
+-> vocabulary projection -> sampler) for several tokens, then the trainer's side
+(token log-probabilities under two policies -> ACR objective -> logits' gradient).
 
-Bounds.  Queries: the rotation in fp32 is off by less than 2^-20 of the pair's size, then half a step of bf16.
-Cached keys: the same, then half a step of e4m3 (2^-4 of the value; 2^-10 of the head's step where that is more), the step
-itself rounded to fp32.  Values: the latter alone.  Attention: the bounds beside its own tests, on the cache's codes.
-Whole numbers and repeated runs: equal."""
+Each stage is checked on the stage before it as the GPU computed it, so the
+tolerances are those of a single stage (see the tests of each): the attention's
+output within 2^-8 of the value and 2^-10 of the weighted magnitudes, log-
+probabilities within 1e-5."""
 import pytest
 import torch
 
 import w8a8_precision_gemm_gb300 as q
-from test_gpu_attn_chunk import check, reference
-from test_gpu_pages import append, i4, release
 
 pytestmark = pytest.mark.gpu
 
-HQ, HK, HD, BLOCK = 10, 2, 128, 16
+HID, HEADS, KV, HD, INTER, VOCAB, BLOCK = 256, 4, 2, 64, 512, 1000, 16
+B, STEPS = 5, 40
 
 
-@pytest.fixture(autouse=True)
-def _status():
-    yield
-    q.qurl_check_device_status()
-
-
-class Engine:
-    """State of a batch of B requests: pages of a shared pool, what is cached."""
-
-    def __init__(self, B=6, most=400, pages=90, seed=0):
-        self.per = -(-most // BLOCK)
-        slots = pages * BLOCK
+class Layer:
+    def __init__(self, qt, seed=0):
+        self.qt = qt
         g = torch.Generator(device="cuda")
         g.manual_seed(seed)
-        byte = lambda: torch.randint(0, 120, (slots, HK, HD), device="cuda", generator=g, dtype=torch.uint8)  # noqa: E731
-        self.caches = [byte(), torch.full((slots, HK), 0.01, device="cuda"), byte(), torch.full((slots, HK), 0.01, device="cuda")]
-        self.free, self.n = q.kv_pages(pages)
-        self.table = torch.zeros((B, self.per), dtype=torch.int32, device="cuda")
-        self.cached = torch.zeros(B, dtype=torch.int32, device="cuda")
-        self.freq, self.factor = q.rope_frequencies(HD, scaling="yarn", factor=4.0, original_len=1024)
-        self.ws = q.kv_attn_chunk_workspace(HQ, HK, HD)
-        self.state = [self.free, self.n, self.table, self.cached, *self.caches]
+        w = lambda n, k: torch.randn((n, k), device="cuda", generator=g) * k ** -0.5  # noqa: E731
+        gain = lambda: 1 + 0.1 * torch.randn(HID, device="cuda", generator=g)  # noqa: E731
+        qkv_n = (HEADS + 2 * KV) * HD
+        self.qkv, self.sqkv, self.g1, _ = q.prepare_weights(w(qkv_n, HID), qt, gamma=gain())
+        self.o, self.so, _, _ = q.prepare_weights(w(HID, HEADS * HD), qt)
+        self.gu, self.sgu, self.g2, _ = q.prepare_weights(w(2 * INTER, HID), qt, gamma=gain())
+        self.down, self.sdown, _, _ = q.prepare_weights(w(HID, INTER), qt)
+        self.lm, self.slm, self.g3, _ = q.prepare_weights(w(VOCAB, HID) * 6, qt, gamma=gain())
+        self.post1, self.post2 = gain(), gain()
+        self.emb = torch.randn((VOCAB, HID), device="cuda", generator=g).to(torch.bfloat16)
+        per = -(-STEPS // BLOCK)
+        pages = B * per + 2
+        self.table = torch.randperm(pages, device="cuda", generator=g)[:B * per].view(B, per).to(torch.int32)
+        self.cache = q.kv_cache(pages * BLOCK, KV, HD)
+        self.attn_ws = q.kv_attn_workspace(B, HEADS, KV, HD, per, BLOCK)
+        self.ws = max((q.workspace(B, n, k, qt) for n, k in ((qkv_n, HID), (HID, HEADS * HD), (2 * INTER, HID), (HID, INTER),
+                                                               (VOCAB, HID))), key=lambda t: 0 if t is None else t.numel())
+        e = lambda n, t=torch.bfloat16: torch.empty((B, n), dtype=t, device="cuda")  # noqa: E731
+        c = q.code_dtype(qt)
+        self.y_qkv, self.attn, self.y_o, self.y_gu, self.y_down, self.logits = (
+            e(n) for n in (qkv_n, HEADS * HD, HID, 2 * INTER, HID, VOCAB))
+        self.h1, self.h2, self.x1, self.x2 = e(HID), e(HID), e(HID, c), e(HID, c)
+        self.xs, self.xo, self.xd = e(HID, c), e(HEADS * HD, c), e(INTER, c)
+        self.s = [torch.empty(B, device="cuda") for _ in range(5)]
+        self.lse = torch.empty((B, HEADS), device="cuda")
+        self.h = e(HID)
+        self.lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+        self.slots = torch.zeros(B, dtype=torch.int64, device="cuda")
+        self.token = torch.zeros(B, dtype=torch.int64, device="cuda")
+        self.logp = torch.empty(B, device="cuda")
+        self.u = torch.empty(B, device="cuda")
+        self.top_p = torch.full((B,), 0.95, device="cuda")
 
-    def step(self, new, qkv, keep=None, stream=None):
-        """One step; keep: tokens that each request keeps at its end (all of them otherwise)."""
-        slots, pos, cu, lens = q.kv_append(self.cached, new, self.table, BLOCK, self.free, self.n, qkv.shape[0], stream=stream)
-        x = q.rope_kv_cache_quant(qkv, HQ, pos, self.freq, slots, *self.caches, factor=self.factor, stream=stream)
-        out, lse = q.kv_attn_chunk(x, HQ, *self.caches, self.table, BLOCK, cu, lens, want_lse=True, ws=self.ws, stream=stream)
-        left = lens if keep is None else torch.minimum(lens, keep)
-        q.kv_release(lens, self.table, BLOCK, self.free, self.n, keep_lens=left, stream=stream)
-        self.cached.copy_(left)
-        return slots, pos, cu, lens, x, out, lse
+    def step(self):
+        """One new token per sequence; lens, slots and u are set before."""
+        torch.index_select(self.emb, 0, self.token, out=self.h)
+        q.qurl_rmsnorm_quant_linear(self.h, self.g1, 1e-6, self.qkv, self.sqkv, self.qt, self.y_qkv, self.xs, self.s[0], self.ws)
+        q.qurl_kv_cache_quant(self.y_qkv, HEADS * HD, KV, HD, self.slots, *self.cache)
+        q.qurl_kv_attn_decode(self.y_qkv, HEADS, *self.cache, self.table, BLOCK, self.lens, HD ** -0.5, self.attn,
+                              self.attn_ws, lse=self.lse)
+        q.qurl_quant_act_linear(self.attn, 1.5, self.o, self.so, self.qt, self.y_o, self.xo, self.s[1], self.ws)
+        q.qurl_residual_rmsnorm_quant(self.h, self.y_o, self.g2, self.qt, self.h1, self.x1, self.s[2], self.post1)
+        q.qurl_w8a8_linear(self.x1, self.s[2], self.gu, self.sgu, self.qt, self.y_gu, self.ws)
+        q.qurl_silu_mul_quant_linear(self.y_gu, 1.5, self.down, self.sdown, self.qt, self.y_down, self.xd, self.s[3], self.ws)
+        q.qurl_residual_rmsnorm_quant(self.h1, self.y_down, self.g3, self.qt, self.h2, self.x2, self.s[4], self.post2)
+        q.qurl_w8a8_linear(self.x2, self.s[4], self.lm, self.slm, self.qt, self.logits, self.ws)
+        q.qurl_sample(self.logits, self.u, self.token, top_p=self.top_p, logp=self.logp)
+
+    def place(self, t):
+        """Lengths and slots of the token at position t; sequence 3 is finished (padding) from 20 on."""
+        t = torch.full((B,), t, device="cuda")
+        done = torch.arange(B, device="cuda").eq(3) & (t >= 20)
+        page = self.table.long().gather(1, (t // BLOCK)[:, None])[:, 0]
+        self.slots.copy_(torch.where(done, -1, page * BLOCK + t % BLOCK))
+        self.lens.copy_(torch.where(done, 20, t + 1).int())
 
 
-def rows(M, seed):
+def check_attention(L, keys, values):
+    """The step's attention against all the step's keys and values so far (bf16, as projected)."""
+    k8, ks, v8, vs = L.cache
+    x = L.y_qkv[:, :HEADS * HD].double().view(B, KV, -1, HD)
+    for b in range(B):
+        n = int(L.lens[b])
+        j = torch.arange(n, device="cuda")
+        slot = L.table[b].long()[j // BLOCK] * BLOCK + j % BLOCK
+        k = k8.view(torch.uint8)[slot].view(torch.float8_e4m3fn).double() * ks[slot].double()[..., None]
+        v = v8.view(torch.uint8)[slot].view(torch.float8_e4m3fn).double() * vs[slot].double()[..., None]
+        # the cache holds what was projected, to half a step of e4m3 (2^-4 of the value, 2^-10 of the scale)
+        for got, want, sc in ((k, keys, ks[slot]), (v, values, vs[slot])):
+            want = torch.stack([s[b] for s in want[:n]]).double()
+            assert bool((got - want).abs().le(want.abs() * 2.0 ** -4 * 1.001 + sc.double()[..., None] * 2.0 ** -10).all())
+        s = torch.einsum("hgd,lhd->hgl", x[b], k) * HD ** -0.5
+        p = torch.softmax(s, -1)
+        want = torch.einsum("hgl,lhd->hgd", p, v).reshape(-1)
+        mag = torch.einsum("hgl,lhd->hgd", p, v.abs()).reshape(-1)
+        assert bool((L.attn[b].double() - want).abs().le(want.abs() * 2.0 ** -8 + mag * 2.0 ** -10).all())
+        assert bool((L.lse[b].double() - torch.logsumexp(s, -1).reshape(-1)).abs().le(1e-4).all())
+
+
+@pytest.mark.parametrize("qt", [q.INT8, q.FP8_E4M3])
+def test_decode_steps_then_training(qt):
+    L = Layer(qt)
     g = torch.Generator(device="cuda")
-    g.manual_seed(seed)
-    return torch.randn((M, (HQ + 2 * HK) * HD), device="cuda", generator=g).to(torch.bfloat16)
+    g.manual_seed(5)
+    keys, values, tokens, logps, logits = [], [], [], [], []
+    graph = None
+    for t in range(STEPS):
+        L.place(t)
+        L.u.copy_(torch.rand(B, device="cuda", generator=g))
+        if t == 3:  # from here on the captured step is replayed
+            graph = torch.cuda.CUDAGraph()
+            held = L.token.clone()
+            with torch.cuda.graph(graph):
+                L.step()
+            L.token.copy_(held)
+        L.step() if graph is None else graph.replay()
+        kv = L.y_qkv[:, HEADS * HD:].clone().view(B, 2, KV, HD)
+        keys.append(kv[:, 0])
+        values.append(kv[:, 1])
+        check_attention(L, keys, values)
+        z = L.logits.double()
+        ref = torch.log_softmax(z, -1).gather(1, L.token[:, None])[:, 0]
+        assert bool((L.logp.double() - ref).abs().le(1e-5).all())
+        # the token lies in the smallest set of 0.95
+        order = torch.sort(z, dim=-1, descending=True, stable=True)
+        before = torch.softmax(order.values, -1).cumsum(-1) - torch.softmax(order.values, -1)
+        rank = order.indices.eq(L.token[:, None]).int().argmax(-1)
+        assert bool((before.gather(1, rank[:, None])[:, 0] < 0.95 + 1e-9).all())
+        tokens.append(L.token.clone())
+        logps.append(L.logp.clone())
+        logits.append(L.logits.clone())
+    q.qurl_check_device_status()
+
+    # ---- the trainer: the same responses under a proximal and a trained policy (the rollout's logits, moved a little)
+    x = torch.cat(logits)
+    T = x.shape[0]
+    target = torch.cat(tokens)
+    mask = torch.ones(T, dtype=torch.uint8, device="cuda")
+    mask[3 + 20 * B::B] = 0  # the finished sequence's padding
+    target = torch.where(mask.bool(), target, -1)
+    prox = (x.float() + 0.02 * torch.randn(x.shape, device="cuda", generator=g)).to(torch.bfloat16)
+    new = (prox.float() + 0.05 * torch.randn(x.shape, device="cuda", generator=g)).to(torch.bfloat16)
+    adv = torch.randn(T, device="cuda", generator=g)
+    logp_prox, _ = q.token_logprob(prox, target)
+    logp, lse = q.token_logprob(new, target)
+    behav = torch.cat(logps)
+    stats, dterm, term = q.acr_objective(logp, logp_prox, behav, adv, mask, want_term=True)
+    d = q.token_logprob_grad(new, target, lse, dterm, scale=-1.0, denom=stats[1:2])
+    q.qurl_check_device_status()
+    assert float(stats[1]) == int(mask.sum())
+
+    leaf = new.double().requires_grad_(True)
+    lp = torch.log_softmax(leaf, -1).gather(1, target.clamp(min=0)[:, None])[:, 0]
+    w = torch.exp(logp_prox.double() - behav.double()).clamp(max=2.0)
+    R = torch.exp(lp - logp_prox.double())
+    c = torch.minimum(R.clamp(min=0.8), 1.2 / w)
+    loss = -(torch.minimum(R * adv, c * adv) * w * mask).sum() / mask.sum()
+    loss.backward()
+    assert abs(float(stats[0]) + float(loss.detach())) < 1e-5
+    near = ((R - 0.8).abs() < 1e-4) | ((R - 1.2 / w).abs() < 1e-4)  # a clip decided by the last bits
+    ok = ~near.detach()
+    # dterm's relative 2e-6, the exponentials' 2^-17 of p |w|, and half a step of bf16
+    weight = (dterm.double().abs() / float(stats[1]))[:, None]
+    err = (d.double() - leaf.grad).abs()
+    assert bool(err[ok].le(leaf.grad.abs()[ok] * 2.0 ** -8 * 1.01 + (weight * 2.0 ** -15)[ok]).all())
+    assert not bool(d[mask == 0].any())
 
 
-def turned(x, pos, freq, factor):
-    """Rows of heads in 64 bits, halves as pairs."""
-    t = pos.double()[:, None, None] * freq
-    a, b = x.double().chunk(2, -1)
-    return torch.cat([a * t.cos() - b * t.sin(), a * t.sin() + b * t.cos()], -1) * factor
+def test_calls_given_a_stream_do_not_touch_the_current_one():
+    """Every operator with stream=: the current stream is busy and its freed memory full of ones, the results on
+    the given stream are those of the current stream alone."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(9)
+    r = lambda *s: torch.randn(s, device="cuda", generator=g)  # noqa: E731
+    n, hid, V, slots = 3, 256, 5000, 4096
+    kc, ks, vc, vs = q.kv_cache(slots, 2, 64)
+    q.qurl_kv_cache_quant(r(slots, 8 * 64).to(torch.bfloat16), 4 * 64, 2, 64, torch.arange(slots, device="cuda"), kc, ks, vc, vs)
+    table = torch.arange(slots // 16, device="cuda", dtype=torch.int32)[None].repeat(n, 1).contiguous()
+    lens = torch.tensor([4000, 17, 2500], dtype=torch.int32, device="cuda")
+    query, h, y = r(n, 4 * 64).to(torch.bfloat16), r(n, hid).to(torch.bfloat16), r(n, hid).to(torch.bfloat16)
+    gain, logits, u, dl = 1 + 0.1 * r(hid), r(n, V), torch.rand(n, device="cuda", generator=g), r(n)
+    target, top_p = torch.tensor([5, -1, 4999], device="cuda"), torch.full_like(u, .9)
 
+    def calls(stream):
+        logp, lse = q.token_logprob(logits, target, stream=stream)
+        return [*q.kv_attn_decode(query, 4, kc, ks, vc, vs, table, 16, lens, want_lse=True, stream=stream),
+                *q.residual_rmsnorm_quant(h, y, gain, q.INT8, stream=stream),
+                *q.sample(logits, u, top_p=top_p, want_kept=True, stream=stream), logp, lse,
+                q.token_logprob_grad(logits, target, lse, dl, stream=stream)]
 
-STEPS = [  # (new tokens, tokens kept at the end, rows behind the last)
-    ([70, 1, 0, 33, 128, 300], None, 0),                       # prompts, one request idle
-    ([1, 1, 17, 5, 4, 1], [71, 0, 17, 35, 132, 301], 3),       # single tokens, drafts of which some are dropped, one finished
-    ([1, 200, 0, 1, 1, 90], [72, 200, 0, 36, 0, 0], 13),       # a prompt in the place of the finished one, three more end
-    ([1, 1, 1, 1, 1, 1], None, 0),                             # single tokens
-]
-
-
-def test_steps_of_a_batch():
-    e, host = Engine(), None
-    for i, (new, keep, pad) in enumerate(STEPS):
-        M, before = sum(new) + pad, [t.clone() for t in e.state]
-        cached, table = before[3].tolist(), before[2].tolist()
-        qkv = rows(M, i)
-        slots, pos, cu, lens, x, out, lse = e.step(i4(new), qkv, None if keep is None else i4(keep))
-        # pages, against the rules on the host
-        want = append(cached, new, table, BLOCK, before[0].tolist(), int(before[1]), M)
-        left = keep or want[3]
-        free, n = release(want[3], left, want[4], BLOCK, before[0].tolist(), want[5])
-        assert slots.tolist() == want[0] and pos.tolist() == want[1] and cu.tolist() == want[2] and lens.tolist() == want[3]
-        assert int(e.n) == n and e.free.tolist()[:n] == free[:n] and e.cached.tolist() == left
-        # queries, keys and values
-        there = slots >= 0
-        h = qkv.view(M, -1, HD)
-        want_q = turned(h[:, :HQ], pos, e.freq, e.factor)
-        size = (h[:, :HQ].double().abs() + h[:, :HQ].double().abs().roll(HD // 2, -1)) * e.factor
-        d = (x.view(M, HQ, HD).double() - want_q).abs()
-        assert bool(d.le(want_q.abs() * 2.0 ** -8 + size * 2.0 ** -19).all())
-        keys, values = turned(h[:, HQ:HQ + HK], pos, e.freq, e.factor)[there], h[:, HQ + HK:].double()[there]
-        for exact, codes, steps in ((keys, e.caches[0], e.caches[1]), (values, e.caches[2], e.caches[3])):
-            step = steps[slots[there]].double()
-            got = codes[slots[there]].view(torch.float8_e4m3fn).double() * step[..., None]
-            err = exact.abs() * (2.0 ** -4 + 2.0 ** -18) + step[..., None] * (2.0 ** -10 + 448 * 2.0 ** -18)
-            assert bool((got - exact).abs().le(err).all())
-        other = torch.ones(len(e.caches[1]), dtype=torch.bool, device="cuda")
-        other[slots[there]] = False
-        for now, then in zip(e.caches, before[4:]):
-            assert torch.equal(now[other], then[other])
-        # attention
-        a = dict(q=x, q_heads=HQ, k=e.caches[0].view(torch.float8_e4m3fn), ks=e.caches[1], v=e.caches[2].view(torch.float8_e4m3fn),
-                 vs=e.caches[3], table=torch.tensor(want[4], dtype=torch.int32, device="cuda"), block=BLOCK, cu=cu, lens=lens,
-                 scale=HD ** -0.5, window=0)
-        check(a, (out, lse))
-    # the last step's tokens are single: the attention of one token, to both kernels' bounds
-    one, l1 = q.kv_attn_decode(x, HQ, *e.caches, e.table, BLOCK, lens, want_lse=True)
-    _, _, to, tl = reference(a)
-    assert bool((one.double() - out.double()).abs().le(2 * to).all()) and bool((l1 - lse).abs().le(2 * tl).all())
-
-
-def test_a_captured_step_and_one_on_another_stream():
-    """The same steps eager, replayed and on a stream of their own: the same bits, state included."""
-    B = 6
-    plan = [([40, 3, 0, 17, 25, 1], [400] * 6), ([1, 1, 30, 4, 1, 1], [41, 0, 30, 19, 400, 400]), ([1, 38, 1, 1, 1, 1], [400] * 6)]
-    M = 128  # (rows behind the last sequence's in every step)
-    eager, graph, side = Engine(), Engine(), Engine()
-    new, keep, qkv = i4([0] * B), i4([0] * B), rows(M, 9)
-    graph.step(new, qkv, keep)  # (workspaces and the library, before the capture)
+    want = calls(None)
+    torch.cuda.synchronize()
     s = torch.cuda.Stream()
-    s.wait_stream(torch.cuda.current_stream())
-    with torch.cuda.stream(s):
-        g = torch.cuda.CUDAGraph()
-        with torch.cuda.graph(g, stream=s):
-            res = graph.step(new, qkv, keep)
-    torch.cuda.current_stream().wait_stream(s)
-    for i, (n, k) in enumerate(plan):
-        x = rows(M, 20 + i)
-        want = eager.step(i4(n), x, i4(k))
-        t = torch.cuda.Stream()
-        t.wait_stream(torch.cuda.current_stream())
-        n_t, k_t = i4(n), i4(k)
+    for _ in range(3):
+        dirt = [torch.full((1 << k,), 255, dtype=torch.uint8, device="cuda") for k in range(6, 24)]
         torch.cuda.synchronize()
-        with torch.cuda.stream(t):
-            got = side.step(n_t, x, k_t)
-        new.copy_(i4(n)), keep.copy_(i4(k)), qkv.copy_(x)
-        g.replay()
-        torch.cuda.synchronize()
-        rows_used = int(want[2][-1])
-        for a, b, c in zip(want, got, res):
-            part = slice(0, rows_used) if a.shape[0] == M else slice(None)
-            assert torch.equal(a[part], b[part]) and torch.equal(a[part], c[part])
-        for a, b, c in zip(eager.state, side.state, graph.state):
-            assert torch.equal(a, b) and torch.equal(a, c)
-
-
-def test_two_batches_at_once():
-    """Two engines on two streams, each with its workspace, in flight together: as one behind the other."""
-    plan = [([250, 1, 100, 33, 7, 300], None), ([1, 1, 1, 1, 1, 1], None), ([4, 4, 4, 4, 4, 4], None)]
-    xs = [[rows(sum(n), 50 + 10 * b + i) for i, (n, _) in enumerate(plan)] for b in range(2)]
-    news = [i4(n) for n, _ in plan]
-    alone = [Engine(pages=100, seed=b) for b in range(2)]
-    want = [[alone[b].step(news[i], xs[b][i])[5] for i in range(len(plan))] for b in range(2)]
-    both = [Engine(pages=100, seed=b) for b in range(2)]
-    streams = [torch.cuda.Stream() for _ in range(2)]
+        del dirt
+        torch.cuda._sleep(1 << 27)
+        got = calls(s)
+        s.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
     torch.cuda.synchronize()
-    got = [[], []]
-    for i in range(len(plan)):
-        for b in range(2):
-            with torch.cuda.stream(streams[b]):
-                got[b].append(both[b].step(news[i], xs[b][i])[5])
-    torch.cuda.synchronize()
-    for b in range(2):
-        for x, y in zip(want[b], got[b]):
-            assert torch.equal(x, y)
-        for x, y in zip(alone[b].state, both[b].state):
-            assert torch.equal(x, y)
 
 
-def test_stream_argument():
-    """What a call with stream= allocates and launches belongs to that stream: the caller's stream is not waited for, and
-    its results are there once the stream is through."""
-    e, s = Engine(), torch.cuda.Stream()
-    x, new = rows(60, 3), i4([10, 20, 0, 30, 0, 0])
-    want = Engine().step(new, x)
-    torch.cuda.synchronize()
-    slots, pos, cu, lens = q.kv_append(e.cached, new, e.table, BLOCK, e.free, e.n, 60, stream=s)
-    y = q.rope_kv_cache_quant(x, HQ, pos, e.freq, slots, *e.caches, factor=e.factor, stream=s)
-    out, lse = q.kv_attn_chunk(y, HQ, *e.caches, e.table, BLOCK, cu, lens, want_lse=True, stream=s)  # (its own workspace)
-    back = q.rope(y, HQ, pos, e.freq, factor=1 / e.factor, inverse=True, stream=s)
-    s.synchronize()
-    for a, b in zip((slots, pos, cu, lens, y, out, lse), want):
-        assert torch.equal(a, b)
-    # (there and back: half a step of both turned values, together 2^-8 of the pair's length, and half a step of the result)
-    d = (back.double() - x[:, :HQ * HD].double()).abs()
-    h = x[:, :HQ * HD].double().view(60, HQ, HD).abs()
-    size = (h + h.roll(HD // 2, -1)).view(60, -1)
-    assert bool(d.le(size * 2.0 ** -7 * (1 + 2.0 ** -6)).all())
+@pytest.mark.parametrize("mode", [0, 1, 2])
+@pytest.mark.parametrize("qt", [q.INT8, q.FP8_E4M3])
+def test_a_latched_parameter_leaves_later_calls_alone(qt, mode):
+    """A page, a target or a parameter out of range is reported at the next look at the status; the calls between,
+    each with other rows, compute what they compute without it, the linears that hand over inside their kernel
+    among them."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    for M, N, K in ((16, 4096, 4096), (64, 4608, 3584), (64, 512, 18944)):
+        W = torch.randn((N, K), device="cuda", generator=g) * 0.02
+        Wq, sw, _, _ = q.prepare_weights(W, qt, keep_scaled=False)
+        X = torch.randn((8, M, K), device="cuda", generator=g).to(torch.bfloat16)
+        ws = q.workspace(M, N, K, qt)
+        xq, sx = torch.empty((M, K), dtype=q.code_dtype(qt), device="cuda"), torch.empty(M, device="cuda")
+        logits = torch.randn((4, 1024), device="cuda", generator=g)
+        u = torch.tensor([.5, 1.5, .5, .5], device="cuda")
+        out = torch.full((2, 8, M, N), 7.0, dtype=torch.bfloat16, device="cuda")
+        before = q.qurl_set_fused_decode(mode)
+        try:
+            for k in (0, 1):
+                if k:
+                    q.sample(logits, u)  # u = 1.5 is out of range
+                for x, y in zip(X, out[k]):
+                    q.qurl_quant_act_linear(x, 1.5, Wq, sw, qt, y, xq, sx, ws)
+                if k:
+                    with pytest.raises(q.QurlError) as e:
+                        q.qurl_check_device_status()
+                    assert e.value.status == 1  # QURL_ERR_INVALID_ARG
+                q.qurl_check_device_status()
+        finally:
+            q.qurl_set_fused_decode(before)
+        assert torch.equal(out[0], out[1]) and not bool(ws[-256:].any())
