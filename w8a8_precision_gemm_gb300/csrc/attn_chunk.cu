@@ -45,7 +45,7 @@
 // Measured (GB300, 40 query and 8 KV heads of 128): 2048 tokens behind 30720, 1356 us, 980 TFLOP/s (dense, as the formula
 // counts), 52% of a cuBLAS bf16 GEMM: a tile of 256 rows takes 5000 cycles, of which the MMAs, two fp8 passes and one in fp16,
 // are 2050 if nothing held them up; their operands, the codes on their way through shared memory and the scales that
-// every row reads are together as many bytes as it can deliver.  Eight prompts of 1000 tokens: 266 us.  64 sequences
+// every row reads are together as many bytes as it can deliver.  Eight prompts of 1000 tokens: 235 us.  64 sequences
 // of 4 tokens behind 8192 or fewer: 254 us, 2.3 TB/s: a tile of tokens is 4100 cycles of one row tile's chain from scores to
 // weights to outputs.
 #include <cuda_bf16.h>
@@ -72,10 +72,10 @@ static_assert(2 * kRegsSoftmax + kRegsConvert + kRegsMma <= 4 * 128, "registers 
 constexpr int kRing = 8;          // tiles whose scales are kept
 constexpr int kSegments = 4;      // segments handed out ahead
 // Costs: a tile of one row tile 2, of two 3 (4100 and 5000 cycles: the tensor core has more to do, the loads are the same), a
-// unit beside its tiles 15 (measured from 6 to 30: eight prompts of 1000 tokens 291 us at 6, 266 at 15), and the least
-// that a range gets (at 16 one prompt of 500 tokens takes 60 us, at 12 35).
-constexpr int kUnitCost = 15;
-constexpr int kMinRange = 12;
+// unit beside its tiles 12 (eight prompts of 1000 tokens 235 us, at 15 and 20 240 and 243; one of 1000 tokens 62, 70 and 68),
+// and the least that a range gets 8 (with more, up to 48, calls of few units take longer: 4 tokens behind 4096 26 us, 58 at 48).
+constexpr int kUnitCost = 12;
+constexpr int kMinRange = 8;
 constexpr float kWide = 0x1p24f;  // scores from here on are not told apart from their neighbours
 constexpr float kFar = 100.0f;    // a reference lies no further than this below the largest score
 constexpr float kHeavy = 0x1p15f; // weights above this move the reference, and so do exponentials whose sum is above
@@ -346,6 +346,7 @@ struct Walk {
       at -= w.cost();
     }
   }
+  __device__ long long tiles_of(long long cost) const { return w.weight == 2 ? (cost + 1) / 2 : (cost + 2) / 3; }
   __device__ bool next() {
     const long long start = end < 0 ? 0 : range_start(sh, blockIdx.x);
     while (true) {
@@ -364,8 +365,8 @@ struct Walk {
         } while (w.tiles == 0);
       }
       const long long base = at + kUnitCost;  // tile t costs [base + t weight, + weight)
-      t0 = start > base ? static_cast<int>(min((start - base + w.weight - 1) / w.weight, static_cast<long long>(w.tiles))) : 0;
-      t1 = end > base ? static_cast<int>(min((end - base + w.weight - 1) / w.weight, static_cast<long long>(w.tiles))) : 0;
+      t0 = start > base ? static_cast<int>(min(tiles_of(start - base), static_cast<long long>(w.tiles))) : 0;
+      t1 = end > base ? static_cast<int>(min(tiles_of(end - base), static_cast<long long>(w.tiles))) : 0;
       if (t1 > t0) return true;
     }
   }
@@ -985,14 +986,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
     auto copy_queries = [&](const Segment& s) {  // the warp's rows; zeros past the head and past the unit
       if (tile * 128 >= s.rows && tile != 0) return;
       const int vec = lane % C::Q_LANES;
-#pragma unroll 2
+      constexpr int kStep = 32 / C::Q_LANES;  // rows that the warp copies at a time
+      int row = (warp & 3) * 32 + lane / C::Q_LANES;
+      int token = (s.row + tile * 128 + row) / group, qh = s.row + tile * 128 + row - token * group;  // (head of the group)
+#pragma unroll 4
       for (int x = 0; x < C::Q_LANES; ++x) {
-        const int row = (warp & 3) * 32 + x * (32 / C::Q_LANES) + lane / C::Q_LANES, at = tile * 128 + row, pair = s.row + at;
-        const int token = pair / group, qh = s.head * group + (pair - token * group);
-        const bool there = at < s.rows && vec * 8 < hd;
+        const bool there = tile * 128 + row < s.rows && vec * 8 < hd;
         const __nv_bfloat16* src = a.q;
-        if (there) src += static_cast<long long>(s.qrow + token) * a.ldq + static_cast<long long>(qh) * hd + vec * 8;
+        if (there) src += static_cast<long long>(s.qrow + token) * a.ldq + static_cast<long long>(s.head * group + qh) * hd + vec * 8;
         if (vec < 2 * q_steps) cp_async16(spot(row, vec >> 1) + (vec & 1) * C::Q_PIECE, src, there ? 16 : 0);
+        row += kStep;
+        for (qh += kStep; qh >= group; qh -= group) ++token;
       }
     };
     auto turn_queries = [&]() {  // this thread's row; returns what makes log2 units of a raw score times the key's scale
@@ -1067,9 +1071,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
             if (sh.segment[(seg + 1) % kSegments].n > 0) copy_queries(sh.segment[(seg + 1) % kSegments]);
           }
           const uint32_t s_addr = lane_base + buf * C::TM_S;
-          // columns of this tile that the row sees (a row past the unit's: all, of a query of zeros)
+          // columns of this tile that the row sees (a row past the unit's: all, of a query of zeros; none in a warp of such rows)
           const int j0 = k.first + (n - 1 - i) * C::BN;
-          const int hi = mine ? pos + 1 - j0 : C::BN, reach = mine && a.window > 0 ? a.window : INT_MAX;
+          const int hi = mine ? pos + 1 - j0 : tile * 128 + (warp & 3) * 32 < k.rows ? C::BN : 0, reach = mine && a.window > 0 ? a.window : INT_MAX;
           bool waited = i == 0;  // for the outputs of the tile before
           uint32_t every = 0xFFFFFFFFu;
 #pragma unroll
@@ -1093,6 +1097,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
               }
             }
             const int lo = max(hi, 0) - reach;
+            if ((sh.valid[ring][2 * c] | sh.valid[ring][2 * c + 1]) == 0 ||
+                !__any_sync(0xFFFFFFFFu, hi > 64 * c && lo < 64 * c + 64)) {  // no row of the warp sees any of these tokens
+              const uint32_t none[16] = {};
+              tmem_st16(s_addr + 32 * c, none);
+              tmem_st16(s_addr + 32 * c + 16, none);
+              continue;
+            }
             const float to = reference64(s_addr + 64 * c, ks, vs, f, 64 * c, lo, hi, &sh.valid[ring][2 * c]);
             float back = 1.0f;
             // (not for less than 2^8: the weights may be as much above where a reference puts them)
