@@ -68,3 +68,27 @@ def test_binding_refuses_what_does_not_fit(monkeypatch):
                    dict(q=torch.zeros(64, 4, dtype=torch.bfloat16).t()), dict(workspace=torch.zeros(8, 4, dtype=torch.uint8).t())):
         with pytest.raises(ValueError):
             q.qurl_kv_attn_chunk(**(good | change))
+
+
+def test_binding_refuses_outputs_over_queries(monkeypatch):
+    """Rows of q are still read where out is already written."""
+    monkeypatch.setattr(q, "_here", lambda *a: None)
+    h = torch.zeros(6, 128, dtype=torch.bfloat16)
+    c, s = torch.zeros(8, 1, 16, dtype=torch.uint8), torch.ones(8, 1)
+    i4 = lambda *n: torch.zeros(n, dtype=torch.int32)  # noqa: E731
+    call = lambda x, out: q.qurl_kv_attn_chunk(x, 4, c, s, c, s, i4(2, 2), 2, i4(3), i4(2), 1.0, out,  # noqa: E731
+                                               torch.zeros(16, dtype=torch.uint8))
+    for x, out in ((h[:4], h[:4]), (h[:4], h[1:5]), (h[:4], h[:4, 32:]), (h[1:5, 32:], h[:4])):
+        with pytest.raises(ValueError, match="overlaps"):
+            call(x, out)
+
+    class Launched(Exception):
+        pass
+
+    def load():
+        raise Launched
+
+    monkeypatch.setattr(q, "load", load)
+    for x, out in ((h[:4], h[:4, 64:]), (h[:4, 64:], h[:4]), (h[:3], h[3:]), (h[:4], torch.empty_like(h[:4]))):
+        with pytest.raises(Launched):  # (columns side by side, other rows, another matrix)
+            call(x, out)

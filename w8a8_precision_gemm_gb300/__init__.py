@@ -417,14 +417,18 @@ def qurl_kv_attn_chunk(q, q_heads, k_cache, k_scale, v_cache, v_scale, block_tab
     if block_table.dtype is not torch.int32:
         raise ValueError("block_table is int32 [B, blocks]")
     _dense(workspace)
+    ldq, ldo = _ld(q), _ld(out)
+    if M and q.data_ptr() == out.data_ptr():
+        raise ValueError("out overlaps the input")
+    _apart(M, q, ldq, q_heads * head_dim, out, ldo, q_heads * head_dim)
     ks, vs = _vec(torch.float32, num_slots * kv_heads, (k_scale, "k_scale"), (v_scale, "v_scale"))
     lens, = _vec(torch.int32, B, (seq_lens, "seq_lens"))
     cu, = _vec(torch.int32, B + 1, (cu_new, "cu_new"))
     lse_at, = _vec(torch.float32, M * q_heads, (lse, "lse"))
-    _ok(load().qurl_kv_attn_chunk(q.data_ptr(), _ld(q), M, q_heads, kv_heads, head_dim, k_cache.data_ptr(), ks,
+    _ok(load().qurl_kv_attn_chunk(q.data_ptr(), ldq, M, q_heads, kv_heads, head_dim, k_cache.data_ptr(), ks,
                                   v_cache.data_ptr(), vs, num_slots, block_table.data_ptr(),
                                   _ld(block_table) if max_blocks else 0, max_blocks, block_size, cu, lens, B, window,
-                                  scale, out.data_ptr(), _ld(out), lse_at, workspace.data_ptr(),
+                                  scale, out.data_ptr(), ldo, lse_at, workspace.data_ptr(),
                                   workspace.numel() * workspace.element_size(), _stream(stream)),
         "qurl_kv_attn_chunk")
 

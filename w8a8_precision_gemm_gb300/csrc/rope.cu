@@ -261,7 +261,7 @@ cudaError_t launch_rope(const RopeArgs& args, bool f32, bool cache, int num_sms,
   // (the angles of an item cost about as much as three passes; the last round of items may leave warps without one)
   a.parts = 1;
   long long best = -1;
-  for (int parts = 1; parts <= passes; ++parts) {
+  for (int parts = 1; parts <= passes && parts <= 256; ++parts) {
     const long long cost = (a.M * parts + warps - 1) / warps * ((passes + parts - 1) / parts + 3);
     if (best < 0 || cost < best) {
       best = cost;
