@@ -37,7 +37,7 @@
 //
 // A unit of work is (row tiles of a sequence, KV head).  The token tiles of all units in a
 // row, each unit with a fixed amount for its start and end, are cut into equal
-// ranges, one per CTA, whatever the lengths; a unit that lies in several ranges leaves
+// ranges, one per CTA, whatever the lengths (units of few tiles stay whole); a unit that lies in several ranges leaves
 // partial sums in the workspace, and the CTA that is done with it last joins
 // them in order: one launch, the same result every run.  The tiles of a segment are taken from its end, so that the
 // masked tile and the one that sets the reference are the same.
@@ -45,7 +45,7 @@
 // Measured (GB300, 40 query and 8 KV heads of 128): 2048 tokens behind 30720, 1356 us, 980 TFLOP/s (dense, as the formula
 // counts), 52% of a cuBLAS bf16 GEMM: a tile of 256 rows takes 5000 cycles, of which the MMAs, two fp8 passes and one in fp16,
 // are 2050 if nothing held them up; their operands, the codes on their way through shared memory and the scales that
-// every row reads are together as many bytes as it can deliver.  Eight prompts of 1000 tokens: 235 us.  64 sequences
+// every row reads are together as many bytes as it can deliver.  Eight prompts of 1000 tokens: 224 us.  64 sequences
 // of 4 tokens behind 8192 or fewer: 254 us, 2.3 TB/s: a tile of tokens is 4100 cycles of one row tile's chain from scores to
 // weights to outputs.
 #include <cuda_bf16.h>
@@ -72,10 +72,13 @@ static_assert(2 * kRegsSoftmax + kRegsConvert + kRegsMma <= 4 * 128, "registers 
 constexpr int kRing = 8;          // tiles whose scales are kept
 constexpr int kSegments = 4;      // segments handed out ahead
 // Costs: a tile of one row tile 2, of two 3 (4100 and 5000 cycles: the tensor core has more to do, the loads are the same), a
-// unit beside its tiles 12 (eight prompts of 1000 tokens 235 us, at 15 and 20 240 and 243; one of 1000 tokens 62, 70 and 68),
-// and the least that a range gets 8 (with more, up to 48, calls of few units take longer: 4 tokens behind 4096 26 us, 58 at 48).
+// unit beside its tiles 12 (eight prompts of 1000 tokens 234 us, at 14 237; one of 1000 tokens 61, 69),
+// the least that a range gets 8 (with more, up to 48, calls of few units take longer: 4 tokens behind 4096 26 us, 58 at 48).
+// Units of kWhole tiles or fewer are not cut: to start, store and join a part costs more (one prompt of 300 tokens 25 us,
+// cut 35; of 1000 tokens 51, cut 61; eight of them 224, cut 234; at 10 a batch with a window of 1000 takes 89 us, at 8 73).
 constexpr int kUnitCost = 12;
 constexpr int kMinRange = 8;
+constexpr int kWhole = 8;
 constexpr float kWide = 0x1p24f;  // scores from here on are not told apart from their neighbours
 constexpr float kFar = 100.0f;    // a reference lies no further than this below the largest score
 constexpr float kHeavy = 0x1p15f; // weights above this move the reference, and so do exponentials whose sum is above
@@ -346,7 +349,15 @@ struct Walk {
       at -= w.cost();
     }
   }
-  __device__ long long tiles_of(long long cost) const { return w.weight == 2 ? (cost + 1) / 2 : (cost + 2) / 3; }
+  // The tiles of this unit before a border at cost x (tile t costs [at + kUnitCost + t weight, + weight)); a unit of
+  // few tiles stays whole, in the range that has more of it.
+  __device__ int cut(long long x) const {
+    const long long cost = x - at - kUnitCost;
+    if (cost <= 0) return 0;
+    const long long t = w.weight == 2 ? (cost + 1) / 2 : (cost + 2) / 3;
+    if (t >= w.tiles) return w.tiles;
+    return w.tiles > kWhole ? static_cast<int>(t) : 2 * t <= w.tiles ? 0 : w.tiles;
+  }
   __device__ bool next() {
     const long long start = end < 0 ? 0 : range_start(sh, blockIdx.x);
     while (true) {
@@ -364,16 +375,21 @@ struct Walk {
           w = unit_of<C>(a, s, group, u);
         } while (w.tiles == 0);
       }
-      const long long base = at + kUnitCost;  // tile t costs [base + t weight, + weight)
-      t0 = start > base ? static_cast<int>(min(tiles_of(start - base), static_cast<long long>(w.tiles))) : 0;
-      t1 = end > base ? static_cast<int>(min(tiles_of(end - base), static_cast<long long>(w.tiles))) : 0;
+      t0 = cut(start);
+      t1 = cut(end);
       if (t1 > t0) return true;
     }
   }
-  // the range that holds a tile of this unit
-  __device__ int range_of(int t) const {
-    const long long p = at + kUnitCost + static_cast<long long>(t) * w.weight;
-    return static_cast<int>(((p + 1) * sh.ranges - 1) / sh.total);
+  // the first and the last range that hold tiles of this unit
+  __device__ int first_range() const {
+    int r = static_cast<int>(((at + kUnitCost + 1) * sh.ranges - 1) / sh.total);  // (of its first tile's border)
+    while (cut(range_start(sh, r + 1)) == 0) ++r;
+    return r;
+  }
+  __device__ int last_range() const {
+    int r = static_cast<int>(((at + w.cost()) * sh.ranges - 1) / sh.total);
+    while (cut(range_start(sh, r)) == w.tiles) --r;
+    return r;
   }
 };
 
@@ -943,8 +959,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
                  k.s.len - k.s.fresh + (k.w.row + k.w.rows - 1) / group + 1,
                  whole ? -1 : 2 * static_cast<int>(blockIdx.x) + (k.t0 == 0 ? 1 : 0), 0, 0};
             if (!whole) {
-              g.r0 = k.range_of(0);
-              g.r1 = k.range_of(k.w.tiles - 1);
+              g.r0 = k.first_range();
+              g.r1 = k.last_range();
             }
           }
           sh.segment[slot] = g;
