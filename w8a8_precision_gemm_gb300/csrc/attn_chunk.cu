@@ -42,8 +42,8 @@
 // them in order: one launch, the same result every run.  The tiles of a segment are taken from its end, so that the
 // masked tile and the one that sets the reference are the same.
 //
-// Measured (GB300, 40 query and 8 KV heads of 128): 2048 tokens behind 30720, 1356 us, 980 TFLOP/s (dense, as the formula
-// counts), 52% of a cuBLAS bf16 GEMM: a tile of 256 rows takes 5000 cycles, of which the MMAs, two fp8 passes and one in fp16,
+// Measured (GB300, 40 query and 8 KV heads of 128): 2048 tokens behind 30720, 1331 us, 1000 TFLOP/s (dense, as the formula
+// counts), 53% of a cuBLAS bf16 GEMM: a tile of 256 rows takes 5000 cycles, of which the MMAs, two fp8 passes and one in fp16,
 // are 2050 if nothing held them up; their operands, the codes on their way through shared memory and the scales that
 // every row reads are together as many bytes as it can deliver.  Eight prompts of 1000 tokens: 224 us.  64 sequences
 // of 4 tokens behind 8192 or fewer: 254 us, 2.3 TB/s: a tile of tokens is 4100 cycles of one row tile's chain from scores to
