@@ -46,7 +46,7 @@
 // counts), 53% of a cuBLAS bf16 GEMM: a tile of 256 rows takes 5000 cycles, of which the MMAs, two fp8 passes and one in fp16,
 // are 2050 if nothing held them up; their operands, the codes on their way through shared memory and the scales that
 // every row reads are together as many bytes as it can deliver.  Eight prompts of 1000 tokens: 224 us.  64 sequences
-// of 4 tokens behind 8192 or fewer: 254 us, 2.3 TB/s: a tile of tokens is 4100 cycles of one row tile's chain from scores to
+// of 4 tokens behind 8192 or fewer: 230 us, 2.5 TB/s: a tile of tokens is 3700 cycles of one row tile's chain from scores to
 // weights to outputs.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -747,8 +747,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
   bool ok = true;
   if (warp >= 8 && warp < 12) {
     // ------------------------------------------------------------ converters: lane = token row for the lookups
-    // Short loops over shared memory rather than unrolled ones over registers: straight-line code of several KB runs
-    // at the rate at which instructions are fetched.
+    // (Loops of 8 copies and 4 conversions: with 2 and 2, which chain their latencies, 64 x 4 tokens take 274 us for 245; with
+    // 8 and 8 prompts take 232 for 227, straight-line code of several KB running at the rate at which it is fetched.)
     fewer_regs<kRegsConvert>();
     const int w = warp - 8, chunks = hd >> 4;  // 16-byte pieces of a head
     const int sub = lane / C::LANES, piece = lane % C::LANES;
@@ -789,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
         }
         const long long byte = at >= 0 ? at * hd : -1;
         const uint32_t k_st = s_k + st * C::K_BYTES + (piece >> 3) * (C::BN * 128), raw_st = raw + (g & 1) * C::RAW_BYTES;
-#pragma unroll 2
+#pragma unroll 8
         for (int i = 0; i < C::LOADS; ++i) {
           const int r = i * (32 / C::LANES) + sub, row = w * C::WARP_ROWS + r;
           const long long off = __shfl_sync(0xFFFFFFFFu, byte, r);
@@ -824,7 +824,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
         if (!ok) break;
         const uint32_t base = s_v + (h & 1) * C::V_BYTES + (piece >> 2) * (C::BN * 128);
         const bool swap = (piece & 4) != 0;
-#pragma unroll 2
+#pragma unroll 4
         for (int i = 0; i < C::LOADS; ++i) {
           const int row = w * C::WARP_ROWS + i * (32 / C::LANES) + sub;
           if (loads) {
