@@ -14,13 +14,14 @@
 //
 // Bound by HBM: every value is read and written once.  A warp takes some heads of a token (all of them where there are
 // many tokens), then the same of a later token: a lane holds the same 8 dimensions of every head it meets (groups of
-// lanes per head), so that it turns them by angles that it computes itself, 8 a token, from turns per position that stay
-// in its registers.  No warp waits for another.  The other half of a pair comes from the partner lane; a rotary width
-// whose halves do not fall on vectors of 8 goes through shared memory instead.
+// lanes per head), so that it turns them by angles that it computes itself, 8 a token, from the turns per position of each
+// pair, which a CTA works out once.  No warp waits for another.  The other half of a pair comes from the partner lane; a
+// rotary width whose halves do not fall on vectors of 8 goes through shared memory instead.
 //
-// Measured (GB300): 8192 tokens of 48 heads of 128 in bf16, 201 MB: 38 us, 5.3 TB/s; with the cache, 8192 tokens of 40 + 8 + 8
-// heads, 218 MB: 61 us, 3.6 TB/s, where instructions bound it (0.67 of a scheduler's slots issue: the 16 quantized heads of
-// a token take as many as its 40 others).  A CTA for each token, its angles in shared memory, took 75 and 108 us.
+// Measured (GB300): 8192 tokens of 48 heads of 128 in bf16, 201 MB: 36 us, 5.5 TB/s; with the cache, 8192 tokens of 40 + 8 + 8
+// heads, 218 MB: 59 us, 3.7 TB/s, where instructions bound it (0.67 of a scheduler's slots issue: the 16 quantized heads of
+// a token take as many as its 40 others).  A CTA for each token, its angles in shared memory, took 75 and 108 us; turns kept
+// in registers, spilling others, 38 and 61.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -42,7 +43,7 @@ constexpr int kInterleaved = 2;  // 2 i and 2 i + 1
 
 constexpr int kInFlight = 4;  // vectors a lane loads before it works on the first
 constexpr int kThreads = 256;
-constexpr int kResident = 3;  // CTAs of an SM (2 with 8 vectors on their way: 39 and 69 us)
+constexpr int kResident = 3;  // CTAs of an SM (4: 39 and 62 us)
 
 // 8 values as they lie in memory.
 template <typename T>
@@ -100,6 +101,7 @@ __device__ __forceinline__ uint64_t turns_per_position(double f) {
 
 template <typename T, int LAYOUT, bool CACHE>
 __global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const RopeArgs a) {
+  __shared__ uint64_t turns[128];                           // per position, of each pair
   extern __shared__ float mix[];                            // kHalfAny: a warp's values, 256 each
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int group = a.group, sub = lane & (group - 1);      // lanes per head (a power of two), this lane's place
@@ -114,12 +116,9 @@ __global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const RopeArg
   griddep_launch_dependents();
 
   constexpr int kPairs = LAYOUT == kInterleaved ? 4 : 8;    // pairs that this lane's values belong to
-  uint64_t turns[kPairs];
-#pragma unroll
-  for (int e = 0; e < kPairs; ++e) {
-    const int d = LAYOUT == kInterleaved ? d0 + 2 * e : d0 + e;
-    turns[e] = d < a.rot ? turns_per_position(a.inv_freq[LAYOUT == kInterleaved ? d >> 1 : d < half ? d : d - half]) : 0;
-  }
+  const int pair0 = LAYOUT == kInterleaved ? d0 >> 1 : d0 < half ? d0 : d0 - half;
+  for (int i = threadIdx.x; i < 128; i += kThreads) turns[i] = i < half ? turns_per_position(a.inv_freq[i]) : 0;
+  __syncthreads();
   const long long items = a.M * a.parts, step = static_cast<long long>(gridDim.x) * (kThreads / 32);
   for (long long item = static_cast<long long>(blockIdx.x) * (kThreads / 32) + warp; item < items; item += step) {
     // (the tokens' last heads first: keys and values take longer)
@@ -149,9 +148,12 @@ __global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const RopeArg
     float2 co[4], si[4];  // si: what the other value of the pair is multiplied with
 #pragma unroll
     for (int e = 0; e < kPairs; ++e) {
-      // the top 32 bits of p turns[e] modulo 2^64
-      const uint32_t pu = static_cast<uint32_t>(p), low = static_cast<uint32_t>(turns[e]);
-      const uint32_t at = __umulhi(pu, low) + pu * static_cast<uint32_t>(turns[e] >> 32) - (p < 0 ? low : 0);
+      // the top 32 bits of p times the turns, modulo 2^64
+      int i = pair0 + e;
+      if (LAYOUT == kHalfAny && d0 < half && i >= half) i -= half;  // (the halves' border within this lane's values)
+      const uint64_t per = turns[i & 127];
+      const uint32_t pu = static_cast<uint32_t>(p), low = static_cast<uint32_t>(per);
+      const uint32_t at = __umulhi(pu, low) + pu * static_cast<uint32_t>(per >> 32) - (p < 0 ? low : 0);
       float s, c;
       sincospif(static_cast<float>(static_cast<int>(at)) * 0x1p-31f, &s, &c);
       c *= a.factor;
