@@ -43,9 +43,10 @@
 // masked tile and the one that sets the reference are the same.
 //
 // Measured (GB300, 40 query and 8 KV heads of 128): 2048 tokens behind 30720, 1331 us, 1000 TFLOP/s (dense, as the formula
-// counts), 53% of a cuBLAS bf16 GEMM: a tile of 256 rows takes 5000 cycles, of which the MMAs, two fp8 passes and one in fp16,
-// are 2050 if nothing held them up; their operands, the codes on their way through shared memory and the scales that
-// every row reads are together as many bytes as it can deliver.  Eight prompts of 1000 tokens: 224 us.  64 sequences
+// counts), 53% of a cuBLAS bf16 GEMM: a tile of 256 rows takes 5000 cycles.  The softmax of a row
+// tile takes 2700 of them and its MMAs, two fp8 passes and one in fp16, 1500 (1024 if nothing held them up), in turn with the
+// other's.  Tensor pipe 34% busy, issue slots 46%, shared memory two thirds (operands, the codes on their way, the scales
+// that every row reads).  Eight prompts of 1000 tokens: 224 us.  64 sequences
 // of 4 tokens behind 8192 or fewer: 230 us, 2.5 TB/s: a tile of tokens is 3700 cycles of one row tile's chain from scores to
 // weights to outputs.
 #include <cuda_bf16.h>
@@ -65,7 +66,7 @@ namespace {
 constexpr int kSoftmax = 256;     // threads 0..255: two groups of 128, a row a thread
 constexpr int kConverters = 128;  // threads 256..383
 constexpr int kThreads = 512;     // and two warps that issue the MMAs, one that hands out the segments, one without work
-// Registers a thread: 128 at launch (512 threads), moved between the warpgroups: the softmax threads' loop over 32
+// Registers a thread: 128 at launch (512 threads), moved between the warpgroups: the softmax threads' loop over 64
 // scores at a time needs room to overlap its loads, products and exponentials.
 constexpr int kRegsSoftmax = 168, kRegsConvert = 88, kRegsMma = 88;
 static_assert(2 * kRegsSoftmax + kRegsConvert + kRegsMma <= 4 * 128, "registers at launch");
@@ -280,7 +281,7 @@ struct Shared {
   uint64_t kfull[3], kempty[3], vfull[2], vempty[2];  // a stage of keys, of values
   uint64_t scfull[kRing];                             // the scales of a tile
   uint64_t sgfull[kSegments], sgempty[kSegments];     // a segment
-  uint64_t qfull;                                     // a segment's queries, and its outputs may be overwritten
+  uint64_t qfull;                                     // a segment's queries, and the scores of the one before have been used
   uint64_t sfull[2], pfull[2], ofull[2];              // scores, weights (per score buffer), outputs (per row tile)
   uint64_t turn[2];                                   // a row tile's MMAs of a step are issued
   uint64_t meet;                                      // the softmax threads
