@@ -494,3 +494,17 @@ def test_behind_a_timeout_of_another_kernel():
     ws.zero_()
     got = run(a, ws=ws)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 3, 2 ** 30, 5, 1])
+def test_rows_before_the_first_token_and_windows(window):
+    """More new tokens than the length says, whatever the window: zeros and -inf there, all else as ever."""
+    a = make([(0, 40), (300, 30), (0, 3), (2000, 270), (10, 9)], 6, 2, 64, 16, seed=9)
+    a["lens"][0], a["lens"][2], a["lens"][4] = 15, -4, 5
+    a["window"] = window
+    out = torch.full_like(a["q"], 7.0)
+    lse = torch.full((a["q"].shape[0], 6), 7.0, device="cuda")
+    q.qurl_kv_attn_chunk(a["q"], 6, a["k"], a["ks"], a["v"], a["vs"], a["table"], 16, a["cu"], a["lens"], a["scale"], out,
+                         q.kv_attn_chunk_workspace(6, 2, 64), window, lse)
+    check(a, (out, lse))
+    assert bool((out[:25] == 0).all()) and bool((lse[:25] == float("-inf")).all()) and bool((out[70:73] == 0).all())

@@ -255,7 +255,8 @@ __device__ __forceinline__ Unit unit_of(const AttnChunkArgs& a, const Seq& s, in
   w.row = u * C::ROWS;
   w.rows = min(C::ROWS, s.fresh * group - w.row);
   const int first = s.len - s.fresh + w.row / group, last = s.len - s.fresh + (w.row + w.rows - 1) / group;
-  const int lo = a.window > 0 ? max(0, first - a.window + 1) : 0;
+  // (first is below zero for rows that stand before the first token, and a window may be as large as an int)
+  const int lo = a.window > 0 && first >= a.window ? first - a.window + 1 : 0;
   w.tile0 = lo / C::BN;
   w.tiles = last < 0 ? 0 : last / C::BN + 1 - w.tile0;
   w.weight = w.rows > 128 ? 3 : 2;
