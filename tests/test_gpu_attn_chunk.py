@@ -508,3 +508,21 @@ def test_rows_before_the_first_token_and_windows(window):
                          q.kv_attn_chunk_workspace(6, 2, 64), window, lse)
     check(a, (out, lse))
     assert bool((out[:25] == 0).all()) and bool((lse[:25] == float("-inf")).all()) and bool((out[70:73] == 0).all())
+
+
+@pytest.mark.parametrize("first,second", [(290, 200), (290, 270), (290, 3), (100, 290), (19990, 40), (19990, 12000), (60, 19990)])
+@pytest.mark.parametrize("gap", [0, 30, 60, 100])
+def test_value_scales_far_apart_between_blocks(first, second, gap):
+    """A token of the largest score and a value scale of 2^-100, and one whose score is `gap` less (in log2 units) and whose
+    value scale is 2^100, in different blocks, tiles and parts of a unit: the outputs are the second one's values, the sum of
+    exponentials is the first one's."""
+    n = 20000 if max(first, second) > 300 else 300
+    a = make([(n - 1, 1)], 1, 1, 64, 16, seed=81)
+    at = lambda j: int(a["table"][0, j // 16]) * 16 + j % 16  # noqa: E731
+    a["q"].fill_(1.0)
+    a["k"].view(torch.uint8).zero_()
+    for j, x, e in ((first, 110.0, -100), (second, 110.0 - gap, 100)):
+        a["k"][at(j)] = torch.full((1, 64), 448.0, device="cuda").to(torch.float8_e4m3fn)
+        a["ks"][at(j)] = x / 1.4426950408889634 / (448.0 * 64 * a["scale"])
+        a["vs"][at(j)] = 2.0 ** e
+    check(a)

@@ -1123,17 +1123,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
               continue;
             }
             const float to = reference64(s_addr + 64 * c, ks, vs, f, 64 * c, lo, hi, &sh.valid[ring][2 * c]);
-            float back = 1.0f;
+            float half = 1.0f;  // the square root of what the old reference's terms are multiplied by
             // (not for less than 2^8: the weights may be as much above where a reference puts them)
             const bool moves = to > R + 8.0f || (fabsf(to) >= kWide && to > R);
             if (moves) {
-              back = ex2(R - to);
+              half = ex2(0.5f * (R - to));
               R = to;
             }
             wide = __any_sync(0xFFFFFFFFu, wide || (fabsf(R) >= kWide && R > -INFINITY));
             if (!fresh && __any_sync(0xFFFFFFFFu, moves)) {
-              // what was summed by the old reference is scaled
-              l *= back;
+              // What was summed by the old reference is scaled: the exponentials' sum in two steps, as it may be as large as
+              // 2^kFar by a reference and still count where that moves by more than fp32 has exponents.
+              l = l * half * half;
+              const float back = half * half;
               if (!waited) {
                 ok = wait_phase(&sh.ofull[tile], (done - 1) & 1, a.status);
                 ok = __all_sync(0xFFFFFFFFu, ok);
@@ -1271,9 +1273,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
             const float to = fmaxf(m[y], ml[y].x);
-            const float f0 = m[y] > -INFINITY ? ex2(m[y] - to) : 0.0f, f1 = ml[y].x > -INFINITY ? ex2(ml[y].x - to) : 0.0f;
+            // (the square roots of the factors: a sum is scaled in two steps, as where a reference moves)
+            const float h0 = m[y] > -INFINITY ? ex2(0.5f * (m[y] - to)) : 0.0f;
+            const float h1 = ml[y].x > -INFINITY ? ex2(0.5f * (ml[y].x - to)) : 0.0f;
+            const float f0 = h0 * h0, f1 = h1 * h1;
             m[y] = to;
-            sum[y] = sum[y] * f0 + ml[y].y * f1;
+            sum[y] = sum[y] * h0 * h0 + ml[y].y * h1 * h1;
             o[y].x = o[y].x * f0 + v[y].x * f1;
             o[y].y = o[y].y * f0 + v[y].y * f1;
             o[y].z = o[y].z * f0 + v[y].z * f1;
