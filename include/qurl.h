@@ -546,9 +546,10 @@ qurl_status qurl_kv_attn_decode(const void* q, int ldq, int B, int q_heads, int 
  *                workspace serves calls of any other layout it is large enough for), 16-byte aligned, ZERO-FILLED
  *                before its first use: it holds counters that every call leaves zero.  Calls that
  *                may run at the same time need separate workspaces; qurl_kv_attn_decode's is another.
- * Lengths, rows and pages are read on the device: a token whose page is negative or past num_slots is left out,
+ * Lengths, rows and pages are read on the device: a token that a row sees whose page is negative or past num_slots is left out,
  * a length past max_blocks * block_size is cut to it, rows past M or in decreasing order count as none, and
- * each latches QURL_ERR_INVALID_ARG in the device status word.
+ * each latches QURL_ERR_INVALID_ARG in the device status word.  Entries of the table whose tokens no new token sees (behind the
+ * window, past the length) are not read.
  * Sums are fp32.  A value of q enters exactly, or (below 2^-13 of its row's largest) within 2^-21 of that.  A weight
  * softmax(s)_j * v_scale is within 2^-10.9 of its value, or 2^-27 of the row's largest, whatever the tokens' scales
  * from 2^-100 to 2^100; for scores of 2^24 and more (in log2 units), which are not told apart from

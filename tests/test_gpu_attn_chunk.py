@@ -526,3 +526,19 @@ def test_value_scales_far_apart_between_blocks(first, second, gap):
         a["ks"][at(j)] = x / 1.4426950408889634 / (448.0 * 64 * a["scale"])
         a["vs"][at(j)] = 2.0 ** e
     check(a)
+
+
+@pytest.mark.parametrize("block", [16, 24, 128])
+@pytest.mark.parametrize("window", [1, 100, 128, 129, 1000])
+def test_pages_behind_the_window(window, block):
+    """Pages that no row's window reaches have been given back: neither they nor their tokens are read."""
+    a = make([(1500, 200), (900, 1), (3000, 7), (300, 40), (0, 250)], 10, 2, 128, block, seed=window)
+    a["window"] = window
+    want = run(a)
+    check(a, want)
+    for b in range(5):
+        cached = int(a["lens"][b]) - int(a["cu"][b + 1] - a["cu"][b])
+        a["table"][b, :max(0, cached + 1 - window) // block] = -1 if b % 2 else 2 ** 30
+    got = run(a)
+    q.qurl_check_device_status()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

@@ -241,6 +241,7 @@ __device__ __forceinline__ Seq seq_of(const AttnChunkArgs& a, int b, bool* bad =
 // A unit's rows [row, row + rows) of (token, head) pairs, and the tiles of tokens they see.
 struct Unit {
   int row, rows, tile0, tiles;
+  int low;     // the first token that a row sees
   int weight;  // the cost of a tile
   __device__ int cost() const { return tiles == 0 ? 0 : kUnitCost + tiles * weight; }
 };
@@ -257,6 +258,7 @@ __device__ __forceinline__ Unit unit_of(const AttnChunkArgs& a, const Seq& s, in
   const int first = s.len - s.fresh + w.row / group, last = s.len - s.fresh + (w.row + w.rows - 1) / group;
   // (first is below zero for rows that stand before the first token, and a window may be as large as an int)
   const int lo = a.window > 0 && first >= a.window ? first - a.window + 1 : 0;
+  w.low = lo;
   w.tile0 = lo / C::BN;
   w.tiles = last < 0 ? 0 : last / C::BN + 1 - w.tile0;
   w.weight = w.rows > 128 ? 3 : 2;
@@ -272,7 +274,8 @@ struct Segment {
   int pos;     // its position
   int row;     // the unit's first (token, head) pair of the sequence, and
   int rows;    // how many
-  int first;   // first token of the first tile
+  int first;   // first token of the first tile, and
+  int low;     // the first that a row of the unit sees
   int stop;    // tokens that the unit's last row sees
   int part;    // the whole unit: -1; else the place of these partial sums,
   int r0, r1;  // the first and last range with tiles of the unit
@@ -341,7 +344,7 @@ struct Walk {
     group = a.q_heads / a.kv_heads;
     b = sh.b, u = sh.u, head = sh.head - 1, at = sh.at;
     t0 = t1 = 0;
-    w = {0, 0, 0, 0, 0};
+    w = {};
     s = {0, 0, 0};
     end = static_cast<int>(blockIdx.x) < sh.ranges ? range_start(sh, blockIdx.x + 1) : -1;
     if (end < 0) at = 0;
@@ -762,7 +765,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
     bool more = next_segment(sh, 0, k, ok, a.status);
     auto look_up = [&]() {  // the page of this lane's token in tile t of the segment, from its end
       const int j = k.first + (k.n - 1 - t) * C::BN + w * C::WARP_ROWS + lane, blk = j / a.block_size;
-      in_page = lane < C::WARP_ROWS && j < k.stop ? j - blk * a.block_size : -1;
+      // (nor the pages before the unit's windows: they may have been given back)
+      in_page = lane < C::WARP_ROWS && j >= k.low && j < k.stop ? j - blk * a.block_size : -1;
       if (in_page >= 0) page = __ldg(a.block_table + static_cast<long long>(k.b) * a.ld_table + blk);
       head = k.head;
     };
@@ -957,7 +961,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
           Segment g = {};
           if (more) {
             const bool whole = k.t0 == 0 && k.t1 == k.w.tiles;
-            g = {k.t1 - k.t0, k.b, k.head, k.s.row0, k.s.len - k.s.fresh, k.w.row, k.w.rows, (k.w.tile0 + k.t0) * C::BN,
+            g = {k.t1 - k.t0, k.b, k.head, k.s.row0, k.s.len - k.s.fresh, k.w.row, k.w.rows, (k.w.tile0 + k.t0) * C::BN, k.w.low,
                  k.s.len - k.s.fresh + (k.w.row + k.w.rows - 1) / group + 1,
                  whole ? -1 : 2 * static_cast<int>(blockIdx.x) + (k.t0 == 0 ? 1 : 0), 0, 0};
             if (!whole) {
