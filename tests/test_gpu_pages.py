@@ -214,3 +214,26 @@ def test_another_stream():
     s.synchronize()
     assert [v.tolist() for v in out] + [t.tolist()] == list(want[:5])
     assert int(nf) == n + sum(-(-c // 16) for c in cached)
+
+
+@pytest.mark.parametrize("M", [3000, 7000, 15000, 30000])
+def test_counts_and_lengths_in_place_by_several_ctas(M):
+    """The number of free pages and the lengths are read and written by all CTAs of a call at the same place: every step of a
+    growing batch, as many times over, takes the pages and the places that the rules say."""
+    r, B, block, per, pages = random.Random(M), 400, 8, 24, 400 * 24
+    lens, new = [r.randint(0, 30) for _ in range(B)], None
+    order = list(range(pages))
+    r.shuffle(order)
+    table = [[order.pop() if k < -(-c // block) else -5 for k in range(per)] for c in lens]
+    free, n = order + [0] * (pages - len(order)), len(order)
+    for _ in range(4):
+        new = [r.randint(0, 30) for _ in range(B)]
+        new = [min(v, M // B) for v in new]
+        want = append(lens, new, table, block, free, n, M)
+        for _ in range(5):
+            t, nf, l, f = i4(table), i4([n]), i4(lens), i4(free)
+            slots = torch.full((M,), 7, dtype=torch.int64, device="cuda")
+            pos, cu = i4([7] * M), i4([7] * (B + 1))
+            q.qurl_kv_append(l, i4(new), t, block, f, nf, nf, slots, pos, cu, l)
+            assert [v.tolist() for v in (slots, pos, cu, l, t)] + [int(nf)] == list(want)
+        lens, table, n = want[3], want[4], want[5]

@@ -130,7 +130,9 @@ __global__ void __launch_bounds__(kPageThreads, 1) kv_append_kernel(const KvAppe
   }
   if (bad && rank == 0) latch_bad_index(a.status);
   __syncthreads();
-  cluster_arrive();  // this CTA has read the lengths and the number of free pages
+  // This CTA has read the lengths and the number of free pages: an arrival that orders those reads (release), as the
+  // writes behind the wait (acquire) may be to the same words.
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 
   auto page_of = [&](int j) { return j < nf ? __ldg(a.free_pages + (nf - 1 - j)) : -1; };
   const int step = ranks * kPageThreads;
@@ -153,7 +155,7 @@ __global__ void __launch_bounds__(kPageThreads, 1) kv_append_kernel(const KvAppe
     a.slots[i] = slot;
     a.positions[i] = pos;
   }
-  cluster_wait();  // every CTA has
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // every CTA has
   for (int b = rank * kPageThreads + tid; b <= a.B; b += step) {
     a.cu[b] = cu[b];
     if (b < a.B) a.seq_lens[b] = held[b] + cu[b + 1] - cu[b];
