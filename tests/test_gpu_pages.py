@@ -237,3 +237,13 @@ def test_counts_and_lengths_in_place_by_several_ctas(M):
             q.qurl_kv_append(l, i4(new), t, block, f, nf, nf, slots, pos, cu, l)
             assert [v.tolist() for v in (slots, pos, cu, l, t)] + [int(nf)] == list(want)
         lens, table, n = want[3], want[4], want[5]
+
+
+def test_as_many_rows_as_an_int_counts():
+    """A step padded to 2^31 - 1 rows: the tokens in front, padding up to the last row."""
+    M, t, n = 2 ** 31 - 1, i4([[5, -5], [-5, -5]]), i4([3])
+    slots, pos, cu, lens = q.kv_append(i4([10, 0]), i4([9, 2]), t, 16, i4([2, 8, 4]), n, M)
+    assert slots[:12].tolist() == [90, 91, 92, 93, 94, 95, 64, 65, 66, 128, 129, -1]
+    assert pos[:12].tolist() == [10, 11, 12, 13, 14, 15, 16, 17, 18, 0, 1, 0]
+    assert bool((slots[11:] == -1).all()) and bool((pos[11:] == 0).all())
+    assert cu.tolist() == [0, 9, 11] and lens.tolist() == [19, 2] and t.tolist() == [[5, 4], [8, -5]] and int(n) == 1

@@ -135,14 +135,16 @@ __global__ void __launch_bounds__(kPageThreads, 1) kv_append_kernel(const KvAppe
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 
   auto page_of = [&](int j) { return j < nf ? __ldg(a.free_pages + (nf - 1 - j)) : -1; };
-  const int step = ranks * kPageThreads;
-  for (int j = rank * kPageThreads + tid; j < taken; j += step) {
-    const int b = owner(need, a.B, j);
+  // (unsigned: a step past the last row may be past 2^31)
+  const unsigned begin = rank * kPageThreads + tid, step = ranks * kPageThreads;
+  for (unsigned u = begin; u < static_cast<unsigned>(taken); u += step) {
+    const int j = static_cast<int>(u), b = owner(need, a.B, j);
     const int k = blocks_of(held[b], a.block_size) + j - need[b];
     a.table[static_cast<long long>(b) * a.ld_table + k] = page_of(j);
   }
 #pragma unroll 4
-  for (int i = rank * kPageThreads + tid; i < a.M; i += step) {
+  for (unsigned u = begin; u < static_cast<unsigned>(a.M); u += step) {
+    const int i = static_cast<int>(u);
     long long slot = -1;
     int pos = 0;
     if (i < total) {
@@ -156,7 +158,7 @@ __global__ void __launch_bounds__(kPageThreads, 1) kv_append_kernel(const KvAppe
     a.positions[i] = pos;
   }
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // every CTA has
-  for (int b = rank * kPageThreads + tid; b <= a.B; b += step) {
+  for (int b = static_cast<int>(begin); b <= a.B; b += static_cast<int>(step)) {
     a.cu[b] = cu[b];
     if (b < a.B) a.seq_lens[b] = held[b] + cu[b + 1] - cu[b];
   }
