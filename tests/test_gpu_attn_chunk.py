@@ -542,3 +542,16 @@ def test_pages_behind_the_window(window, block):
     got = run(a)
     q.qurl_check_device_status()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_rows_of_nearly_as_many_columns_as_an_int_counts():
+    """A row that sees nothing, of 2^27 - 1 heads of 16: zeros up to its last column, and nothing behind it."""
+    heads = 2 ** 27 - 1
+    a = make([(0, 1)], 1, 1, 16, 16)
+    x = torch.zeros(heads * 16, dtype=torch.bfloat16, device="cuda")
+    out = torch.full((heads * 16 + 4096,), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((1, heads), 7.0, device="cuda")
+    a["lens"].zero_()
+    q.qurl_kv_attn_chunk(x.view(1, -1), heads, a["k"], a["ks"], a["v"], a["vs"], a["table"], 16, a["cu"], a["lens"], 0.25,
+                         out[:heads * 16].view(1, -1), q.kv_attn_chunk_workspace(heads, 1, 16), lse=lse)
+    assert bool((out[:heads * 16] == 0).all()) and bool((out[heads * 16:] == 7).all()) and bool((lse == float("-inf")).all())

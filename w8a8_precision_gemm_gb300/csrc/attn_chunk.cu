@@ -986,7 +986,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
       const int none = min(s.fresh, s.fresh - s.len);
       for (int i = 0; i < none; ++i) {
         const long long row = s.row0 + i;
-        for (int c = tid; c < a.q_heads * hd; c += kSoftmax) a.out[row * a.ldo + c] = __float2bfloat16_rn(0.0f);
+        for (unsigned c = tid; c < static_cast<unsigned>(a.q_heads * hd); c += kSoftmax)  // (a row may have nearly 2^31 columns)
+          a.out[row * a.ldo + c] = __float2bfloat16_rn(0.0f);
         if (a.lse)
           for (int c = tid; c < a.q_heads; c += kSoftmax) a.lse[row * a.q_heads + c] = -INFINITY;
       }
