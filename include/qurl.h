@@ -551,7 +551,7 @@ qurl_status qurl_kv_attn_decode(const void* q, int ldq, int B, int q_heads, int 
  * each latches QURL_ERR_INVALID_ARG in the device status word.  Entries of the table whose tokens no new token sees (behind the
  * window, past the length) are not read.
  * Sums are fp32.  A value of q enters exactly, or (below 2^-13 of its row's largest) within 2^-21 of that.  A weight
- * softmax(s)_j * v_scale is within 2^-10.9 of its value, or 2^-27 of the row's largest, whatever the tokens' scales
+ * softmax(s)_j * v_scale is within 2^-10.9 of its value plus 2^-27 of the row's largest, whatever the tokens' scales
  * from 2^-100 to 2^100; for scores of 2^24 and more (in log2 units), which are not told apart from
  * their neighbours, scales from 2^-14 to 2^15.  Results are identical run to run.
  * B = 0 and M = 0 are valid.  Errors: INVALID_ARG (NULL, a size out of range, q_heads % kv_heads, ld_table <

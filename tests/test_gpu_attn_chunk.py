@@ -555,3 +555,34 @@ def test_rows_of_nearly_as_many_columns_as_an_int_counts():
     q.qurl_kv_attn_chunk(x.view(1, -1), heads, a["k"], a["ks"], a["v"], a["vs"], a["table"], 16, a["cu"], a["lens"], 0.25,
                          out[:heads * 16].view(1, -1), q.kv_attn_chunk_workspace(heads, 1, 16), lse=lse)
     assert bool((out[:heads * 16] == 0).all()) and bool((out[heads * 16:] == 7).all()) and bool((lse == float("-inf")).all())
+
+
+def test_weights_are_rounded_once_where_a_reference_moves():
+    """Pairs of tokens with the same score and opposite values, w_a v_a = - w_b v_b, in the first half of a tile, and a token that
+    moves the reference in the second half: what is left of a pair is the rounding of its weights.  One rounding
+    to fp16 leaves 2^-11 of each (2^-10.9 with the fp32 roundings of the product and the sum), which bf16 rounds by 2^-9; the
+    magnitude itself, from scores that are off by 2^-12 at most, is within 2^-9."""
+    a = make([(100, 28)], 16, 1, 128, 16, seed=91)
+    g = _gen(92)
+    slot = a["table"][0].long().repeat_interleave(16)[:128] * 16 + torch.arange(128, device="cuda") % 16
+    k = torch.zeros((128, 128), device="cuda")
+    k[:64, 1:] = torch.randn((32, 127), device="cuda", generator=g).repeat_interleave(2, 0)
+    k[64, 0] = 448.0
+    v = torch.zeros((128, 128), device="cuda")
+    pair = torch.arange(32, device="cuda")
+    v[2 * pair, pair], v[2 * pair + 1, pair] = 416.0, -448.0
+    for n, x in (("k", k), ("v", v)):
+        a[n].view(torch.uint8)[slot, 0] = x.to(torch.float8_e4m3fn).view(torch.uint8)
+    a["ks"][slot] = 0.555
+    a["ks"][slot[64]] = 12.5 / 1.4426950408889634 / (448.0 * a["scale"])
+    a["vs"][slot] = 448.0 * 2.0 ** -15
+    a["vs"][slot[2 * pair + 1]] = 416.0 * 2.0 ** -15
+    a["q"].view(28, 16, 128)[..., 0] = 1.0
+    o = run(a)[0].double().view(28, 16, 128)
+    keys = k.to(torch.float8_e4m3fn).double() * a["ks"][slot].double()
+    s = a["q"].double().view(28, 16, 128) @ keys.T * a["scale"]
+    s = s.masked_fill(torch.arange(128, device="cuda") > torch.arange(100, 128, device="cuda")[:, None, None], float("-inf"))
+    size = torch.softmax(s, -1)[..., :64:2] * 2 * 416 * 448 * 2.0 ** -15
+    assert bool((o[..., 32:] == 0).all())
+    worst = float((o[..., :32].abs() / size).max())
+    assert worst <= 2.0 ** -10.9 * (1 + 2.0 ** -8), worst * 2 ** 10.9

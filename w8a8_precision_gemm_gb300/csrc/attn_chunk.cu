@@ -16,9 +16,10 @@
 //     Products are exact, sums fp32, the keys' scales are applied to them in fp32.
 //   * Outputs: kind::f16, an e4m3 code being an fp16 number.  The weights w_ij = exp2(x_ij - R_i) vs_j (x: scores in
 //     log2 units) are rounded to fp16, half a step: 2^-11 of a value of 2^-14 or more, 2^-25 below.  The reference
-//     R_i puts the largest weight of the first tokens it is taken from at 2^3, and moves when one
-//     grows past 2^15 (in blocks that are masked, past 2^11): what is lost of a row is below 2^-27 of its largest weight
-//     for every token.  So the softmax need not look for a maximum: one pass, and the largest
+//     R_i, a whole number, puts the largest weight of the first tokens it is taken from between 2^2.1 and 2^3.2, and moves when
+//     one grows past 2^15 (in blocks that are masked, past 2^11.1): what is lost of a row is below 2^-27 of its largest weight
+//     for every token.  What was summed before is then scaled by a power of two, exactly, and so are the weights of the same tile that
+//     are rounded already.  So the softmax need not look for a maximum: one pass, and the largest
 //     weight, which every block yields, says whether it may stand.
 //
 // Rows of the MMAs are (token, query head of the group) pairs in a row, so a group of any
@@ -559,8 +560,8 @@ __device__ __forceinline__ float weights64_slow(uint32_t taddr, uint32_t to, uin
   return sum.x + sum.y;
 }
 
-// The reference that puts the largest weight of the same tokens at 2^3 (see kWide and kFar for its limits), from their
-// scores; -infinity if none counts.
+// The whole number that, as a reference, puts the largest weight of the same tokens between 2^2.1 and 2^3.2 (see kWide and kFar
+// for its limits), from their scores; -infinity if none counts.
 __device__ __forceinline__ float reference64(uint32_t taddr, uint32_t ks, uint32_t vs, float f, int at, int lo, int hi,
                                              const uint32_t* valid) {
   float most[4], heavy[4];
@@ -585,7 +586,16 @@ __device__ __forceinline__ float reference64(uint32_t taddr, uint32_t ks, uint32
   }
   most[0] = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
   heavy[0] = fmaxf(fmaxf(heavy[0], heavy[1]), fmaxf(heavy[2], heavy[3]));
-  return fabsf(most[0]) < kWide ? fmaxf(heavy[0] - 3.0f, most[0] - kFar) : most[0];
+  // (The scores are whole numbers from kWide on.  Rounded down, or to the nearest, references move more often: one prompt of
+  // 1000 tokens 57 or 51 us, up 48.)
+  return fabsf(most[0]) < kWide ? ceilf(fmaxf(heavy[0] - 3.125f, most[0] - kFar)) : most[0];
+}
+
+// 2^d as a product, for the difference d <= 0 of two references: a sum of exponentials may be as large as 2^kFar by the
+// one and still count by the other, where 2^d itself is 0 in fp32.  (-infinity: 2^-252.)
+__device__ __forceinline__ float2 factors(float d) {
+  const int n = max(static_cast<int>(d), -252);
+  return make_float2(pow2(n / 2), pow2(n - n / 2));
 }
 
 // The natural logarithm of a row's sum of exponentials, from its reference and its sum by it (the reference may
@@ -1128,19 +1138,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
               continue;
             }
             const float to = reference64(s_addr + 64 * c, ks, vs, f, 64 * c, lo, hi, &sh.valid[ring][2 * c]);
-            float half = 1.0f;  // the square root of what the old reference's terms are multiplied by
-            // (not for less than 2^8: the weights may be as much above where a reference puts them)
+            float2 by = make_float2(1.0f, 1.0f);  // what the old reference's terms are multiplied by
+            // (not for 2^8 or less: the weights may be as much above where a reference puts them)
             const bool moves = to > R + 8.0f || (fabsf(to) >= kWide && to > R);
             if (moves) {
-              half = ex2(0.5f * (R - to));
+              by = factors(R - to);
               R = to;
             }
             wide = __any_sync(0xFFFFFFFFu, wide || (fabsf(R) >= kWide && R > -INFINITY));
             if (!fresh && __any_sync(0xFFFFFFFFu, moves)) {
-              // What was summed by the old reference is scaled: the exponentials' sum in two steps, as it may be as large as
-              // 2^kFar by a reference and still count where that moves by more than fp32 has exponents.
-              l = l * half * half;
-              const float back = half * half;
+              // what was summed by the old reference is scaled
+              l = l * by.x * by.y;
+              const float back = by.x * by.y;
               if (!waited) {
                 ok = wait_phase(&sh.ofull[tile], (done - 1) & 1, a.status);
                 ok = __all_sync(0xFFFFFFFFu, ok);
@@ -1278,7 +1287,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
             const float to = fmaxf(m[y], ml[y].x);
-            // (the square roots of the factors: a sum is scaled in two steps, as where a reference moves)
+            // (the square roots of the factors: a sum is scaled in two steps, as where a reference moves; nothing has been rounded
+            // to 16 bits here, so that they need not be exact)
             const float h0 = m[y] > -INFINITY ? ex2(0.5f * (m[y] - to)) : 0.0f;
             const float h1 = ml[y].x > -INFINITY ? ex2(0.5f * (ml[y].x - to)) : 0.0f;
             const float f0 = h0 * h0, f1 = h1 * h1;
