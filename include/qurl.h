@@ -553,7 +553,8 @@ qurl_status qurl_kv_attn_decode(const void* q, int ldq, int B, int q_heads, int 
  * Sums are fp32.  A value of q enters exactly, or (below 2^-13 of its row's largest) within 2^-21 of that.  A weight
  * softmax(s)_j * v_scale is within 2^-10.9 of its value plus 2^-27 of the row's largest, whatever the tokens' scales
  * from 2^-100 to 2^100; for scores of 2^24 and more (in log2 units), which are not told apart from
- * their neighbours, scales from 2^-14 to 2^15.  Results are identical run to run.
+ * their neighbours, scales from 2^-14 to 2^15.  A code that is no number (0x7F, 0xFF) makes NaN of its head's outputs in the rows that
+ * see the token (all head_dim of them; a key's also of lse), and of nothing else.  Results are identical run to run.
  * B = 0 and M = 0 are valid.  Errors: INVALID_ARG (NULL, a size out of range, q_heads % kv_heads, ld_table <
  * max_blocks, window < 0, scale not finite), UNSUPPORTED (head_dim; M * q_heads of 2^31 or more, max_blocks *
  * block_size above 2^30, B above 16384), ALIGNMENT, WORKSPACE.  One kernel launch.  If its bounded waits run out, or a

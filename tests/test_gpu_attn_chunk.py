@@ -586,3 +586,32 @@ def test_weights_are_rounded_once_where_a_reference_moves():
     assert bool((o[..., 32:] == 0).all())
     worst = float((o[..., :32].abs() / size).max())
     assert worst <= 2.0 ** -10.9 * (1 + 2.0 ** -8), worst * 2 ** 10.9
+
+
+@pytest.mark.parametrize("window", [0, 150])
+@pytest.mark.parametrize("q_heads,kv_heads,hd", [(10, 2, 128), (2, 2, 64), (4, 2, 256)])
+def test_values_that_are_no_numbers(q_heads, kv_heads, hd, window):
+    """A value code that is no number makes NaN of its head's outputs in the rows that see the token, and of nothing else."""
+    a = make([(0, 300), (200, 60), (20000, 3), (40, 1), (700, 90)], q_heads, kv_heads, hd, 16, seed=95)
+    a["window"] = window
+    a["q"].mul_(0.25)
+    nans = {0: (5, 128, 131, 290), 1: (100, 215), 2: (19950, 20001) if window else (64, 11000, 20001), 3: (), 4: (650, 789)}
+    slots = {b: [int(a["table"][b, j // 16]) * 16 + j % 16 for j in js] for b, js in nans.items()}
+    every = [s for ss in slots.values() for s in ss]
+    a["v"].view(torch.uint8)[every, 1, 7] = 0
+    want = run(a)
+    check(a, want)
+    a["v"].view(torch.uint8)[every[::2], 1, 7] = 0x7F
+    a["v"].view(torch.uint8)[every[1::2], 1, 7] = 0xFF
+    o, l = run(a)
+    assert torch.equal(l, want[1])
+    sees = torch.zeros(o.shape[0], dtype=torch.bool, device="cuda")
+    for b, js in nans.items():
+        r0, r1 = int(a["cu"][b]), int(a["cu"][b + 1])
+        pos = int(a["lens"][b]) - (r1 - r0) + torch.arange(r1 - r0, device="cuda")
+        for j in js:
+            sees[r0:r1] |= (j <= pos) & ((pos - window < j) if window else True)
+    o, w = o.view(-1, kv_heads, q_heads // kv_heads * hd), want[0].view(-1, kv_heads, q_heads // kv_heads * hd)
+    assert bool(sees.any()) and not bool(sees.all())
+    assert bool(torch.isnan(o[sees, 1]).all())
+    assert torch.equal(o[~sees, 1], w[~sees, 1]) and torch.equal(o[:, 0], w[:, 0])

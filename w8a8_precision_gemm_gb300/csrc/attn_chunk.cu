@@ -303,6 +303,7 @@ struct Shared {
   alignas(16) float vs[kRing][128];
   uint32_t valid[kRing][4];   // tokens whose page exists
   int last;
+  int nan;                    // a value code that is no number has been met
 };
 
 // The cost of a sequence's units for one KV head; sequences of many units are summed by
@@ -399,14 +400,12 @@ struct Walk {
   }
 };
 
-// 16 codes -> 32 bytes of fp16.  (A code that is no number becomes 512: what lies behind a query's own position
-// meets weights of zero, and must stay out.)
+// 16 codes -> 32 bytes of fp16.
 __device__ __forceinline__ void widen4(uint32_t c, uint32_t& lo, uint32_t& hi) {
-  asm("{\n\t.reg .b16 l, h;\n\t.reg .b32 x, y;\n\tmov.b32 {l, h}, %2;\n\t"
-      "cvt.rn.f16x2.e4m3x2 x, l;\n\tcvt.rn.f16x2.e4m3x2 y, h;\n\t"
-      "min.f16x2 %0, x, %3;\n\tmin.f16x2 %1, y, %3;\n\t}"
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
       : "=&r"(lo), "=&r"(hi)
-      : "r"(c), "r"(0x60006000u));
+      : "r"(c));
 }
 __device__ __forceinline__ void widen16(const uint4 c, uint4& lo, uint4& hi) {
   widen4(c.x, lo.x, lo.y);
@@ -414,6 +413,20 @@ __device__ __forceinline__ void widen16(const uint4 c, uint4& lo, uint4& hi) {
   widen4(c.z, hi.x, hi.y);
   widen4(c.w, hi.z, hi.w);
 }
+
+// NaN in a half of `acc` once one of the values is; no finite values make one: a product is exact (below 2^18) within
+// the operation, and the sum never below zero.
+__device__ __forceinline__ void note_nan(const uint4 v, uint32_t& acc) {
+  asm("fma.rn.relu.f16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(v.x), "r"(v.y));
+  asm("fma.rn.relu.f16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(v.z), "r"(v.w));
+}
+__device__ __forceinline__ bool has_nan(uint32_t f16x2) { return (((f16x2 & 0x7FFF7FFFu) + 0x03FF03FFu) & 0x80008000u) != 0; }
+// The codes that are no number (magnitude 0x7F): the top bit of their bytes, and the codes with 0 in their place.
+__device__ __forceinline__ uint32_t no_numbers(uint32_t c) { return ((c & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+__device__ __forceinline__ bool no_numbers(const uint4 c) {
+  return (no_numbers(c.x) | no_numbers(c.y) | no_numbers(c.z) | no_numbers(c.w)) != 0;
+}
+__device__ __forceinline__ uint32_t numbers_only(uint32_t c) { return c & ~((no_numbers(c) >> 7) * 0xFFu); }
 
 __device__ __forceinline__ void st_shared(uint32_t at, const uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
@@ -627,6 +640,32 @@ __device__ __forceinline__ bool next_segment(Shared& sh, int seg, Segment& g, bo
   return g.n > 0;
 }
 
+// Whether any of the segment's tokens that a row sees, those in (pos - reach, pos], has a value that is no number.  Called by
+// whole warps, once converters have met such a value: the codes are read again, 32 tokens at a time.
+template <class C>
+__device__ __forceinline__ bool sees_nan(const AttnChunkArgs& a, const Segment& k, bool mine, int pos, int reach) {
+  const int stop = min(k.first + k.n * C::BN, k.stop), lane = threadIdx.x & 31;
+  bool found = false;
+#pragma unroll 1
+  for (int j0 = max(k.first, k.low); j0 < stop; j0 += 32) {
+    bool bad = false;
+    const int j = j0 + lane;
+    if (j < stop) {
+      const int blk = j / a.block_size, page = __ldg(a.block_table + static_cast<long long>(k.b) * a.ld_table + blk);
+      const long long slot = static_cast<long long>(page) * a.block_size + (j - blk * a.block_size);
+      if (page >= 0 && slot < a.num_slots) {
+        const uint4* v = reinterpret_cast<const uint4*>(a.v_cache + (slot * a.kv_heads + k.head) * a.head_dim);
+#pragma unroll 1
+        for (int c = 0; c < a.head_dim >> 4; ++c) bad |= no_numbers(__ldg(v + c));
+      }
+    }
+    const uint32_t tokens = __ballot_sync(0xFFFFFFFFu, bad);
+    const int hi = mine ? pos + 1 - j0 : 0;
+    found |= seen32(max(hi, 0) - reach, hi, 0, tokens) != 0;
+  }
+  return found;
+}
+
 template <int PANELS>
 __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnChunkArgs a, const ChunkPlan p) {
   using C = ChunkCfg<PANELS>;
@@ -637,6 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
   const int hd = a.head_dim, group = a.q_heads / a.kv_heads;
 
   if (tid == 0) {
+    sh.nan = 0;
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.vfull[i], kConverters);
       mbar_init(&sh.vempty[i], 2);
@@ -838,17 +878,34 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
         if (h >= 2) ok = wait_phase(&sh.vempty[h & 1], ((h >> 1) & 1) ^ 1, a.status);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
-        const uint32_t base = s_v + (h & 1) * C::V_BYTES + (piece >> 2) * (C::BN * 128);
+        const uint32_t base = s_v + (h & 1) * C::V_BYTES + (piece >> 2) * (C::BN * 128), from = raw + (h & 1) * C::RAW_BYTES;
         const bool swap = (piece & 4) != 0;
-#pragma unroll 4
-        for (int i = 0; i < C::LOADS; ++i) {
+        uint32_t nan = 0;
+        auto widen = [&](int i, const uint4 codes) {
           const int row = w * C::WARP_ROWS + i * (32 / C::LANES) + sub;
-          if (loads) {
-            uint4 lo, hi;
-            widen16(ld_shared(raw + (h & 1) * C::RAW_BYTES + i * (kConverters * 16)), lo, hi);
-            const uint32_t c0 = ((2 * piece) & 7) ^ (row & 7);
-            st_shared(base + row * 128 + ((swap ? c0 ^ 1 : c0) << 4), swap ? hi : lo);
-            st_shared(base + row * 128 + ((swap ? c0 : c0 ^ 1) << 4), swap ? lo : hi);
+          uint4 lo, hi;
+          widen16(codes, lo, hi);
+          note_nan(lo, nan);
+          note_nan(hi, nan);
+          const uint32_t c0 = ((2 * piece) & 7) ^ (row & 7);
+          st_shared(base + row * 128 + ((swap ? c0 ^ 1 : c0) << 4), swap ? hi : lo);
+          st_shared(base + row * 128 + ((swap ? c0 : c0 ^ 1) << 4), swap ? lo : hi);
+        };
+        // A value that is no number must not meet the weights of zero of the rows that do not see its token: its code becomes 0 and
+        // the pieces are widened again; the rows that see it are found once the segment is done (sees_nan).  Watching for it, two
+        // instructions per 8 codes in place of a minimum that would hide it, costs 3% (eight prompts of 1000 tokens 234 us, 228).
+#pragma unroll 1
+        for (int clean = 0; clean < 2; ++clean) {
+          nan = 0;
+#pragma unroll 4
+          for (int i = 0; i < C::LOADS; ++i)
+            if (loads) widen(i, ld_shared(from + i * (kConverters * 16)));
+          if (__builtin_expect(!has_nan(nan), 1)) break;
+          sh.nan = 1;
+#pragma unroll 1
+          for (int i = 0; i < C::LOADS; ++i) {
+            const uint4 c = ld_shared(from + i * (kConverters * 16));
+            st_shared(from + i * (kConverters * 16), make_uint4(numbers_only(c.x), numbers_only(c.y), numbers_only(c.z), numbers_only(c.w)));
           }
         }
         mbar_arrive(&sh.vfull[h & 1]);
@@ -1088,6 +1145,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
       const uint32_t o_addr = lane_base + C::TM_O + tile * 64 * PANELS;
       float R = -INFINITY, l = 0.0f;
       bool wide = false, fresh = true;  // (fresh: no reference yet)
+      bool nan = false;                 // one of the values that the row sees is no number
       if (active) {
 #pragma unroll 1
         for (int i = 0; i < n; ++i) {
@@ -1199,6 +1257,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;  // nothing is stored, counted or joined
         tc_fence_after();
+        // (set before the last outputs' values were handed over)
+        if (__builtin_expect(*reinterpret_cast<volatile int*>(&sh.nan) != 0, 0))
+          nan = sees_nan<C>(a, k, mine, pos, mine && a.window > 0 ? a.window : INT_MAX);
       }
       // (the group without rows waits for the other: the score buffers' and the scales' phases that it did not watch
       // have passed when it watches them again)
@@ -1226,6 +1287,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
         for (int c = 0; c < hd; c += 16) {
           uint32_t u[16];
           tmem_ld16(o_addr + c, u);
+          if (__builtin_expect(nan, 0)) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) u[e] = 0x7FC00000u;
+          }
           if (mine && whole) {
             uint32_t w[8];
 #pragma unroll
