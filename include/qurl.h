@@ -404,8 +404,8 @@ qurl_status qurl_kv_cache_dequant(const void* cache, const float* scale, const i
  *   a' = factor (a cos - b sin),   b' = factor (a sin + b cos)
  * and the rest of the head stays.  inverse = 1 turns the other way (sin negated): with
  * the same factor it is the transpose, the gradient of the rotation with respect to X.
- * Arithmetic is fp32; the angle is taken modulo a turn in fixed point, within 2^-31 of a
- * turn and |p inv_freq| 2^-52 radians for any position.  Frequencies scaled for long contexts and the
+ * Arithmetic is fp32; the angle is taken modulo a turn in fixed point and then in fp32, within 2^-27.9 of a turn for fp32 rows,
+ * 2^-25.9 for bf16 ones, and |p inv_freq| 2^-52 radians for any position.  Frequencies scaled for long contexts and the
  * factor that goes with them are the caller's (the Python binding's rope_frequencies
  * gives the usual ones).
  *   X, out     [M, heads * head_dim] of x_type (bf16 or fp32), row strides ldx, ldo; out may be X

@@ -303,3 +303,25 @@ def test_streams_graphs_and_empty_calls():
     check(out, *[t.reshape(M, -1) for t in rotated(x[:, :heads * hd].reshape(M, heads, hd), pos, freq, q.ROPE_HALF, 1.0)])
     assert q.rope(x[:0], heads, pos[:0], freq, head_dim=hd).shape == (0, heads * hd)
     assert q.rope_kv_cache_quant(x[:0], heads, pos[:0], freq, slot[:0], *caches).shape == (0, heads * hd)
+
+
+@pytest.mark.parametrize("layout", [q.ROPE_HALF, q.ROPE_INTERLEAVED])
+def test_fp32_angles(layout):
+    """Cosines and sines themselves: the angle is taken modulo a turn in fixed point (2^-32 of a turn), what is left of the nearest
+    quarter, at most an eighth of a turn, in fp32 (2^-28 of a turn): 2^-25.2 radians, and an ulp (2^-24) of a cosine or a sine
+    that is at most 1: 2^-23.48."""
+    M, hd = 4001, 64
+    freq, _ = q.rope_frequencies(hd, 500.0)
+    pos = torch.arange(M, dtype=torch.int32, device="cuda") - 2000
+    x = torch.zeros((M, hd), device="cuda")
+    first, second = (slice(0, 32), slice(32, 64)) if layout == q.ROPE_HALF else (slice(0, 64, 2), slice(1, 64, 2))
+    x[:, first] = 1.0
+    got = q.rope(x, 1, pos, freq, layout=layout).double()
+    a = pos.double()[:, None] * freq
+    # (2^-52 of the angle for the reference's own product, as much for the frequency in turns)
+    bound = 2.0 ** -23.48 + a.abs() * 2.0 ** -51
+    for part, want in ((first, torch.cos(a)), (second, torch.sin(a))):
+        d = (got[:, part] - want).abs()
+        assert bool(d.le(bound).all()), float((d / bound).max())
+    back = q.rope(x, 1, pos, freq, layout=layout, inverse=True).double()
+    assert torch.equal(back[:, first], got[:, first]) and torch.equal(back[:, second], -got[:, second])

@@ -10,7 +10,7 @@
 // radians are known to 1/16), and fp64 arithmetic is slow here.  f_i / 2 pi is
 // taken as a 64-bit fixed-point fraction of a turn; times p modulo 2^64 the
 // whole turns fall away exactly, and the top 32 bits, the signed fraction of a
-// turn, go to sincospi in fp32.
+// turn, go to sincospi in fp32 (for fp32 rows less the nearest quarter, which keeps two more bits).
 //
 // Bound by HBM: every value is read and written once.  A warp takes some heads of a token (all of them where there are
 // many tokens), then the same of a later token: a lane holds the same 8 dimensions of every head it meets (groups of
@@ -99,6 +99,23 @@ __device__ __forceinline__ uint64_t turns_per_position(double f) {
   return (bits >> 63) != 0 ? 0 - u : u;
 }
 
+// Sine and cosine of `at` units of 2^-32 of a turn (signed).  fp32 has 24 bits for them, 2^-26 of a turn; where the results are
+// rounded to 8 bits or fewer that is enough.  FINE (fp32 rows): what is left of the nearest quarter of a turn, 2^-28.
+template <bool FINE>
+__device__ __forceinline__ void sine_cosine(uint32_t at, float& s, float& c) {
+  if constexpr (!FINE) {
+    sincospif(static_cast<float>(static_cast<int>(at)) * 0x1p-31f, &s, &c);
+  } else {
+    const uint32_t quarter = (at + 0x20000000u) >> 30;
+    float u, v;
+    sincospif(static_cast<float>(static_cast<int>(at - (quarter << 30))) * 0x1p-31f, &u, &v);
+    s = (quarter & 1) != 0 ? v : u;
+    c = (quarter & 1) != 0 ? u : v;
+    if ((quarter & 2) != 0) s = -s;
+    if (((quarter + 1) & 2) != 0) c = -c;
+  }
+}
+
 template <typename T, int LAYOUT, bool CACHE>
 __global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const RopeArgs a) {
   __shared__ uint64_t turns[128];                           // per position, of each pair
@@ -155,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const RopeArg
       const uint32_t pu = static_cast<uint32_t>(p), low = static_cast<uint32_t>(per);
       const uint32_t at = __umulhi(pu, low) + pu * static_cast<uint32_t>(per >> 32) - (p < 0 ? low : 0);
       float s, c;
-      sincospif(static_cast<float>(static_cast<int>(at)) * 0x1p-31f, &s, &c);
+      sine_cosine<sizeof(T) == 4>(at, s, c);
       c *= a.factor;
       s = (a.inverse ? -s : s) * a.factor;
       if constexpr (LAYOUT == kInterleaved) {
