@@ -22,6 +22,7 @@ SOURCES = ["api.cu", "quant.cu", "gemm_common.cu", "gemm_fp8.cu", "gemm_fp8p.cu"
            "static_scratch.cu", "probe.cu", "nvfp4.cu", "attn_decode.cu", "sample.cu", "logprob.cu", "residual.cu",
            "pages.cu", "rope.cu", "attn_chunk.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
+FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 
 
 def nvcc() -> str:
@@ -44,8 +45,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
         return LIB
     os.makedirs(LIBDIR, exist_ok=True)
     cc = nvcc()
-    flags = ARCH + ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC",
-                    "-I", INCLUDE, "-I", CSRC] + (extra_flags or [])
+    flags = FLAGS + (extra_flags or [])
     objs = []
 
     def compile_one(src):
