@@ -170,7 +170,6 @@ qurl_status check_gemm(const void* Xq, const void* Wq, int M, int N, int K, int 
   return QURL_OK;
 }
 
-// Rows of logits (bf16 or fp32) of V values, row stride ld elements.
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // The table and the list of free pages of qurl_kv_append and qurl_kv_release.
@@ -194,6 +193,7 @@ qurl_status check_rope(int M, int heads, int head_dim, int rot_dim, int layout, 
   return QURL_OK;
 }
 
+// Rows of logits (bf16 or fp32) of V values, row stride ld elements.
 qurl_status check_logits(const void* x, int type, int V, int ld) {
   if (!x || !valid_dim(V) || ld < V || (type != QURL_BF16 && type != QURL_FP32)) return QURL_ERR_INVALID_ARG;
   if (V > (1 << 30)) return QURL_ERR_UNSUPPORTED;
