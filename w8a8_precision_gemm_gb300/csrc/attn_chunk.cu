@@ -43,12 +43,12 @@
 // them in order: one launch, the same result every run.  The tiles of a segment are taken from its end, so that the
 // masked tile and the one that sets the reference are the same.
 //
-// Measured (GB300, 40 query and 8 KV heads of 128): 2048 tokens behind 30720, 1331 us, 1000 TFLOP/s (dense, as the formula
+// Measured (GB300, 40 query and 8 KV heads of 128): 2048 tokens behind 30720, 1335 us, 1000 TFLOP/s (dense, as the formula
 // counts), 53% of a cuBLAS bf16 GEMM: a tile of 256 rows takes 5000 cycles.  The softmax of a row
 // tile takes 2700 of them and its MMAs, two fp8 passes and one in fp16, 1500 (1024 if nothing held them up), in turn with the
 // other's.  Tensor pipe 34% busy, issue slots 46%, shared memory two thirds (operands, the codes on their way, the scales
-// that every row reads).  Eight prompts of 1000 tokens: 224 us.  64 sequences
-// of 4 tokens behind 8192 or fewer: 230 us, 2.5 TB/s: a tile of tokens is 3700 cycles of one row tile's chain from scores to
+// that every row reads).  Eight prompts of 1000 tokens: 234 us.  64 sequences
+// of 4 tokens behind 8192 or fewer: 232 us, 2.5 TB/s: a tile of tokens is 3200 cycles of one row tile's chain from scores to
 // weights to outputs.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -73,11 +73,11 @@ constexpr int kRegsSoftmax = 168, kRegsConvert = 88, kRegsMma = 88;
 static_assert(2 * kRegsSoftmax + kRegsConvert + kRegsMma <= 4 * 128, "registers at launch");
 constexpr int kRing = 8;          // tiles whose scales are kept
 constexpr int kSegments = 4;      // segments handed out ahead
-// Costs: a tile of one row tile 2, of two 3 (4100 and 5000 cycles: the tensor core has more to do, the loads are the same), a
-// unit beside its tiles 12 (eight prompts of 1000 tokens 234 us, at 14 237; one of 1000 tokens 61, 69),
-// the least that a range gets 8 (with more, up to 48, calls of few units take longer: 4 tokens behind 4096 26 us, 58 at 48).
+// Costs: a tile of one row tile 2, of two 3 (3200 and 5000 cycles: the tensor core has more to do, the loads are the same), a
+// unit beside its tiles 12 (eight prompts of 1000 tokens 236 us, at 14 242),
+// the least that a range gets 8 (with more, up to 48, calls of few units take longer: 4 tokens behind 4096 27 us, 57 at 48).
 // Units of kWhole tiles or fewer are not cut: to start, store and join a part costs more (one prompt of 300 tokens 25 us,
-// cut 35; of 1000 tokens 51, cut 61; eight of them 224, cut 234; at 10 a batch with a window of 1000 takes 89 us, at 8 73).
+// cut 35; of 1000 tokens 49, cut 62; eight of them 236, cut 249; at 10 a batch with a window of 1000 takes 89 us, at 8 76).
 constexpr int kUnitCost = 12;
 constexpr int kMinRange = 8;
 constexpr int kWhole = 8;
@@ -802,8 +802,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
   bool ok = true;
   if (warp >= 8 && warp < 12) {
     // ------------------------------------------------------------ converters: lane = token row for the lookups
-    // (Loops of 8 copies and 4 conversions: with 2 and 2, which chain their latencies, 64 x 4 tokens take 274 us for 245; with
-    // 8 and 8 prompts take 232 for 227, straight-line code of several KB running at the rate at which it is fetched.)
+    // (Loops of 8 copies and 4 conversions: with 2 and 2, which chain their latencies, 64 x 4 tokens take 282 us for 252; with
+    // 8 and 8 prompts take 242 for 236, straight-line code of several KB running at the rate at which it is fetched.)
     fewer_regs<kRegsConvert>();
     const int w = warp - 8, chunks = hd >> 4;  // 16-byte pieces of a head
     const int sub = lane / C::LANES, piece = lane % C::LANES;
@@ -893,7 +893,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
         };
         // A value that is no number must not meet the weights of zero of the rows that do not see its token: its code becomes 0 and
         // the pieces are widened again; the rows that see it are found once the segment is done (sees_nan).  Watching for it, two
-        // instructions per 8 codes in place of a minimum that would hide it, costs 3% (eight prompts of 1000 tokens 234 us, 228).
+        // instructions per 8 codes in place of a minimum that would hide it, costs 3% (eight prompts of 1000 tokens 235 us, 228).
 #pragma unroll 1
         for (int clean = 0; clean < 2; ++clean) {
           nan = 0;
