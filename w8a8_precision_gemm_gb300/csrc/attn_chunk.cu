@@ -46,7 +46,7 @@
 // Measured (GB300, 40 query and 8 KV heads of 128): 2048 tokens behind 30720, 1335 us, 1000 TFLOP/s (dense, as the formula
 // counts), 53% of a cuBLAS bf16 GEMM: a tile of 256 rows takes 5000 cycles.  The softmax of a row
 // tile takes 2700 of them and its MMAs, two fp8 passes and one in fp16, 1500 (1024 if nothing held them up), in turn with the
-// other's.  Tensor pipe 34% busy, issue slots 46%, shared memory two thirds (operands, the codes on their way, the scales
+// other's.  Tensor pipe 34% busy, issue slots 45%, shared memory two thirds (operands, the codes on their way, the scales
 // that every row reads).  Eight prompts of 1000 tokens: 234 us.  64 sequences
 // of 4 tokens behind 8192 or fewer: 232 us, 2.5 TB/s: a tile of tokens is 3200 cycles of one row tile's chain from scores to
 // weights to outputs.
