@@ -710,12 +710,14 @@ qurl_status qurl_check_device_status(qurl_stream_t stream);
 /* Fault injection, for testing the failure path: the next GEMM this process
  * launches (any linear / gemm_acc entry) skips the first k-block load of each
  * CTA, so a shared-memory stage is never filled -- or, in a fused decode call,
- * its first CTA does not arrive at the handoff; the waits run out after ~1 s,
+ * its first CTA does not arrive at the handoff; if qurl_kv_attn_chunk is launched
+ * first, the keys of each CTA's first tile are never handed over instead; the waits run out after ~1 s,
  * the kernel latches QURL_ERR_TIMEOUT in the device status word, lets its own
  * copies land, frees its tensor memory and exits.  Its outputs are then
  * undefined; qurl_check_device_status() returns QURL_ERR_TIMEOUT and clears
  * the word, and later calls run normally (after a fused call, once the
- * workspace's last 256 bytes are zeroed again).  One-shot; always QURL_OK. */
+ * workspace's last 256 bytes are zeroed again, after the attention once its
+ * workspace is).  One-shot; always QURL_OK. */
 qurl_status qurl_debug_inject_timeout(void);
 
 /* Where a fused quantize -> linear entry (qurl_rmsnorm_quant_linear,

@@ -615,3 +615,25 @@ def test_values_that_are_no_numbers(q_heads, kv_heads, hd, window):
     assert bool(sees.any()) and not bool(sees.all())
     assert bool(torch.isnan(o[sees, 1]).all())
     assert torch.equal(o[~sees, 1], w[~sees, 1]) and torch.equal(o[:, 0], w[:, 0])
+
+
+def test_waits_that_run_out():
+    """The keys of each CTA's first tile are never handed over: the call ends and says so, nothing of a sequence that sees a
+    token is stored wrong, and with the workspace zeroed the next call gives what the one before gave, to the bit."""
+    for spans, q_heads, kv_heads, hd in (([(3000, 9), (0, 300), (0, 0), (700, 77)], 10, 2, 128), ([(500, 70), (0, 5)], 2, 1, 256)):
+        a = make(spans, q_heads, kv_heads, hd, 16, seed=61)
+        ws = q.kv_attn_chunk_workspace(q_heads, kv_heads, hd)
+        want = run(a, ws=ws)
+        out, lse = torch.full_like(want[0], 7.0), torch.full_like(want[1], 7.0)
+        torch.cuda.synchronize()
+        q.qurl_debug_inject_timeout()
+        q.qurl_kv_attn_chunk(a["q"], q_heads, a["k"], a["ks"], a["v"], a["vs"], a["table"], 16, a["cu"], a["lens"], a["scale"], out,
+                             ws, lse=lse)
+        with pytest.raises(q.QurlError) as e:
+            q.qurl_check_device_status()
+        assert e.value.status == 6  # QURL_ERR_TIMEOUT
+        assert bool((out == 7.0).all()) and bool((lse == 7.0).all())
+        ws.zero_()
+        got = run(a, ws=ws)
+        q.qurl_check_device_status()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

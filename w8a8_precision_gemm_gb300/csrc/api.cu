@@ -1045,6 +1045,7 @@ qurl_status qurl_kv_attn_chunk(const void* q, int ldq, int M, int q_heads, int k
   a.lse = lse;
   a.ws = workspace;
   a.status = dev->status;
+  a.fault = g_inject_timeout.exchange(0);
   QURL_CUDA(qurl::launch_kv_attn_chunk(a, dev->num_sms, reinterpret_cast<cudaStream_t>(stream)));
   return QURL_OK;
 }

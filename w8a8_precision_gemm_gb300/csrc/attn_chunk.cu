@@ -857,7 +857,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
           }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
-        cp_async_arrive(&sh.kfull[st]);
+        if (a.fault == 0 || g != 0) cp_async_arrive(&sh.kfull[st]);
         cp_async_arrive(&sh.scfull[ring]);
         if (lane == 0) {
           if (C::WARP_ROWS == 32) sh.valid[ring][w] = valid;

@@ -96,6 +96,7 @@ struct AttnChunkArgs {
   float* lse;  // null: not wanted
   void* ws;
   int* status;
+  int fault;  // nonzero: the keys of each CTA's first tile are never handed over (tests of the waits)
 };
 size_t attn_chunk_workspace_bytes(int q_heads, int kv_heads, int head_dim, int num_sms);
 cudaError_t launch_kv_attn_chunk(const AttnChunkArgs& a, int num_sms, cudaStream_t st);
