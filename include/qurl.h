@@ -426,7 +426,8 @@ qurl_status qurl_rope(const void* X, qurl_ftype x_type, int M, int ldx, int head
  * qurl_kv_cache_quant: the queries are rotated into q_out, the keys are rotated and, in
  * fp32 as they come out of the rotation, quantized into the cache, the values are
  * quantized as they are.  A token with a negative slot (padding) writes no key and no value; its query
- * is rotated all the same.  A head whose largest magnitude is below 2^-140 is stored as zeros.
+ * is rotated all the same.  A head whose largest magnitude is below 2^-140 is stored as zeros, but for NaN
+ * (a code that is no number, as in qurl_kv_cache_quant).
  *   qkv    [M, ldq] bf16: q_heads, kv_heads and kv_heads heads of head_dim columns.
  *   q_out  [M, ldo] bf16, ldo >= q_heads * head_dim; may be qkv (ldo == ldq), whose
  *          keys and values stay, and must not overlap it otherwise.

@@ -325,3 +325,33 @@ def test_fp32_angles(layout):
         assert bool(d.le(bound).all()), float((d / bound).max())
     back = q.rope(x, 1, pos, freq, layout=layout, inverse=True).double()
     assert torch.equal(back[:, first], got[:, first]) and torch.equal(back[:, second], -got[:, second])
+
+
+def test_cache_of_what_is_no_number():
+    """NaN in a head of keys or of values is in its codes, whatever stands beside it: of values as qurl_kv_cache_quant has it, of
+    keys in both of a turned pair (at position 0 too: a NaN times a sine of 0 is one)."""
+    M, heads, kvh, hd = 6, 2, 2, 64
+    x, pos = inputs(M, heads + 2 * kvh, hd, torch.bfloat16, 16)
+    v = x.view(M, -1, hd)
+    nan = float("nan")
+    v[0] = nan                                       # nothing else
+    v[1] = 0.0
+    v[1, :, 5] = nan                                 # beside zeros
+    v[2] = 2.0 ** -133
+    v[2, :, 40] = nan                                # beside the smallest values
+    v[3, :, 7] = nan                                 # beside values
+    slot = torch.arange(M, device="cuda")
+    freq, _ = q.rope_frequencies(hd)
+    a, b = new_cache(M, kvh, hd), new_cache(M, kvh, hd)
+    rows = torch.tensor([0, 1, 3, 4, 5], device="cuda")  # (the quantizer's step of values that small is not compared)
+    q.qurl_kv_cache_quant(x[rows], heads * hd, kvh, hd, slot[rows], *a)
+    for p in (torch.zeros_like(pos), pos):
+        q.rope_kv_cache_quant(x, heads, p, freq, slot, *b)
+        keys, values = b[0].view(torch.uint8) & 0x7F, b[2].view(torch.uint8) & 0x7F
+        assert torch.equal(values[rows], a[2].view(torch.uint8)[rows] & 0x7F) and torch.equal(b[3][rows], a[3][rows])
+        assert bool((keys[0] == 0x7F).all()) and bool((values[0] == 0x7F).all())
+        for row, d in ((1, 5), (2, 40), (3, 7)):
+            assert (keys[row] == 0x7F).nonzero()[:, 1].view(kvh, -1).tolist() == [sorted((d, (d + 32) % 64))] * kvh
+            assert (values[row] == 0x7F).nonzero()[:, 1].view(kvh, -1).tolist() == [[d]] * kvh
+        for c in (keys, values):
+            assert int((c[1] != 0).sum()) == int((c[1] == 0x7F).sum()) and not bool((c[4:] == 0x7F).any())

@@ -244,13 +244,13 @@ __global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const RopeArg
             }
             if (h >= a.heads && h < heads) {
               const int kv = h - a.heads, value = kv >= a.kv_heads;
-              // (a head so small that its step would be 0 is a head of zeros)
+              // (a head so small that its step would be 0 is a head of zeros, but for what is no number: `top` passes that over)
               const Enc en = make_enc(top >= 0x1p-140f ? top : 0.0f, kQFp8);
               const long long at = slot * a.kv_heads + (value ? kv - a.kv_heads : kv);
               if (on) {
                 if (top < 0x1p-140f)
 #pragma unroll
-                  for (int e = 0; e < 4; ++e) y[e] = make_float2(0.0f, 0.0f);
+                  for (int e = 0; e < 4; ++e) y[e] = make_float2(isnan(y[e].x) ? y[e].x : 0.0f, isnan(y[e].y) ? y[e].y : 0.0f);
                 *reinterpret_cast<uint2*>((value ? a.v_cache : a.k_cache) + at * hd + d0) = encode8_f8(y, en);
               }
               if (sub == 0) (value ? a.v_scale : a.k_scale)[at] = en.scale;
