@@ -637,3 +637,24 @@ def test_waits_that_run_out():
         got = run(a, ws=ws)
         q.qurl_check_device_status()
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("scale", [float("inf"), float("nan")])
+def test_value_scales_that_are_no_numbers(scale):
+    """A value scale of infinity or NaN reaches the outputs of the rows that see its token, not their lse, and nothing of the
+    other rows."""
+    a = make([(0, 300), (200, 60), (9000, 2), (40, 1)], 10, 2, 128, 16, seed=97)
+    at = [int(a["table"][b, j // 16]) * 16 + j % 16 for b, j in ((0, 150), (1, 100), (2, 70))]
+    a["v"].view(torch.uint8)[at] = 0x38  # 1
+    plain = a | dict(vs=a["vs"].clone())
+    a["vs"][at, 1] = scale
+    plain["vs"][at, 1] = 1.0 / 448
+    o, l = run(a)
+    ro, rl, to, tl = reference(plain)
+    assert bool((l.double() - rl).abs().le(tl).all()), float(((l.double() - rl).abs() / tl).max())
+    sees = torch.ones(o.shape[0], dtype=torch.bool, device="cuda")
+    sees[:150], sees[-1] = False, False
+    o, ro, to = (t.view(-1, 2, 640) for t in (o, ro, to))
+    assert not bool(torch.isfinite(o[sees, 1]).any())
+    assert bool((o[:, 0].double() - ro[:, 0]).abs().le(to[:, 0]).all())
+    assert bool((o[~sees, 1].double() - ro[~sees, 1]).abs().le(to[~sees, 1]).all())

@@ -601,7 +601,9 @@ __device__ __forceinline__ float reference64(uint32_t taddr, uint32_t ks, uint32
   heavy[0] = fmaxf(fmaxf(heavy[0], heavy[1]), fmaxf(heavy[2], heavy[3]));
   // (The scores are whole numbers from kWide on.  Rounded down, or to the nearest, references move more often: one prompt of
   // 1000 tokens 57 or 51 us, up 48.)
-  return fabsf(most[0]) < kWide ? ceilf(fmaxf(heavy[0] - 3.125f, most[0] - kFar)) : most[0];
+  // (An infinite scale is no measure for the exponentials: it makes its weights infinite by any reference.)
+  const float heaviest = heavy[0] < INFINITY ? heavy[0] - 3.125f : most[0];
+  return fabsf(most[0]) < kWide ? ceilf(fmaxf(heaviest, most[0] - kFar)) : most[0];
 }
 
 // 2^d as a product, for the difference d <= 0 of two references: a sum of exponentials may be as large as 2^kFar by the
