@@ -158,3 +158,14 @@ def test_frequencies():
                 dict(rot_dim=8, scaling="ramp"), dict(rot_dim=8, scaling="yarn", original_len=10, low_turns=3.0, high_turns=2.0)):
         with pytest.raises(ValueError):
             q.rope_frequencies(**bad, device="cpu")
+
+
+def test_helpers_refuse_what_they_cannot_divide_by(monkeypatch):
+    monkeypatch.setattr(q, "_here", lambda *a: None)
+    x, i4 = torch.zeros(4, 64), torch.zeros(4, dtype=torch.int32)
+    f = torch.ones(4, dtype=torch.float64)
+    for heads in (0, -1):
+        with pytest.raises(ValueError, match="heads"):
+            q.rope(x, heads, i4, f)
+    with pytest.raises(ValueError, match="base"):
+        q.rope_frequencies(64, 1.0, "yarn", 4.0, 4096, device="cpu")

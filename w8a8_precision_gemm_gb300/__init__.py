@@ -817,6 +817,8 @@ def rope_frequencies(rot_dim, base=10000.0, scaling=None, factor=1.0, original_l
         if scaling == "ramp":
             keep = (original_len * freq / (2 * math.pi) - low_turns) / (high_turns - low_turns)
         else:
+            if base <= 1:
+                raise ValueError("a ramp in the pair's index takes a base above 1")
             # the pair that makes a number of turns over original_len
             pair = lambda turns: rot_dim * math.log(original_len / (2 * math.pi * turns)) / (2 * math.log(base))  # noqa: E731
             low, high = max(math.floor(pair(high_turns)), 0), min(math.ceil(pair(low_turns)), rot_dim - 1)
@@ -834,6 +836,8 @@ def rope(X, heads, positions, inv_freq, head_dim=None, layout=ROPE_HALF, factor=
          stream=None):
     """Rotary positions of X [M, heads * head_dim]; inverse gives the gradient's rotation.  head_dim defaults to the
     columns over heads."""
+    if heads <= 0:
+        raise ValueError("heads is positive")
     hd = X.shape[1] // heads if head_dim is None else head_dim
     if head_dim is None and X.shape[1] != heads * hd:
         raise ValueError("X has heads * head_dim columns (give head_dim for wider rows)")
