@@ -538,7 +538,7 @@ qurl_status qurl_kv_attn_decode(const void* q, int ldq, int B, int q_heads, int 
  * tokens j <= p and, with window > 0, j > p - window.  Scores, weights, out and lse
  * as in qurl_kv_attn_decode, a row of q in the place of a sequence's.  A row that sees no token (p < 0) gets out = 0 and
  * lse = -inf.  Rows of q, out and lse outside cu_new[0] .. cu_new[B] - 1 (padding) are neither read nor written.
- *   q            [M, ldq] bf16, finite, the q_heads * head_dim query columns first.
+ *   q            [M, ldq] bf16, the q_heads * head_dim query columns first (infinity or NaN in a head of a row: out and lse are NaN there).
  *   caches, block_table [B, ld_table], window, scale   as in qurl_kv_attn_decode.
  *   cu_new       [B + 1] int32, not decreasing, within [0, M] (as qurl_kv_append gives it).
  *   seq_lens     [B] int32, the new tokens included; negative counts as 0.

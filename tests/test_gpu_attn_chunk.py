@@ -658,3 +658,27 @@ def test_value_scales_that_are_no_numbers(scale):
     assert not bool(torch.isfinite(o[sees, 1]).any())
     assert bool((o[:, 0].double() - ro[:, 0]).abs().le(to[:, 0]).all())
     assert bool((o[~sees, 1].double() - ro[~sees, 1]).abs().le(to[~sees, 1]).all())
+
+
+@pytest.mark.parametrize("hd", [64, 128, 256])
+def test_queries_that_are_no_numbers(hd):
+    """Infinity or NaN in a head of a query makes NaN of its outputs and lse; other heads and rows are as ever, and a row that
+    sees nothing stays a row that sees nothing."""
+    a = make([(0, 300), (2000, 3), (40, 1), (0, 5)], 10, 2, hd, 16, seed=98)
+    a["lens"][3] = 3
+    bad = [(0, 3, float("inf")), (140, 9, float("nan")), (299, 0, -float("inf")), (301, 5, float("inf")), (303, 1, float("nan"))]
+    plain = a | dict(q=a["q"].clone())
+    for row, head, v in bad + [(304, 2, float("inf"))]:
+        a["q"].view(-1, 10, hd)[row, head, 17 % hd] = v
+        plain["q"].view(-1, 10, hd)[row, head] = 0.0
+    o, l = run(a)
+    ro, rl, to, tl = reference(plain)
+    hit = torch.zeros(l.shape, dtype=torch.bool, device="cuda")
+    for row, head, _ in bad:
+        hit[row, head] = True
+    o, ro, to = (t.view(-1, 10, hd) for t in (o, ro, to))
+    assert bool(torch.isnan(o[hit]).all()) and bool(torch.isnan(l[hit]).all())
+    assert bool((o.double() - ro).abs().le(to)[~hit].all())
+    assert torch.equal(torch.isinf(l)[~hit], torch.isinf(rl)[~hit]) and bool((o[304:306] == 0).all())
+    d = torch.where(torch.isinf(rl), 0.0, l.double() - rl).abs()
+    assert bool(d.le(tl)[~hit].all())

@@ -1127,7 +1127,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_chunk_kernel(const AttnCh
         st_shared(spot(r, i) + C::Q_PIECE, make_uint4(lo[0], lo[1], lo[2], lo[3]));
       }
       fence_proxy_async_smem();
-      return fabsf(a.scale) * 1.44269504088896340736f / fabsf(f1) / f2;
+      // (e4m3 and e5m2 here end at their largest numbers: an infinite value is not in the pieces, so it is in the factor)
+      return top < INFINITY ? fabsf(a.scale) * 1.44269504088896340736f / fabsf(f1) / f2 : __uint_as_float(0x7FC00000u);
     };
     Segment k;
     float f = 0.0f;
